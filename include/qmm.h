@@ -42,11 +42,22 @@
  * qoff = align16(K/32)); the codes are laid out exactly as above, so a
  * 64-block is two consecutive 32-code runs under one Delta.
  *
+ * Microscaled 4-bit blocks, type MXFP4 ("A Complete Guide to llama.cpp ...",
+ * §2.2: a block of weights shares one scale), K % 32 == 0: the scale is a
+ * power of two stored as one byte s, meaning 2^(s - 127) (255: not a number),
+ * and a code is a four-bit float: sign, two exponent bits, one significand
+ * bit, the values +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}.
+ *     bytes [0, K/32)         the scale byte of block b at offset b
+ *     zero padding up to qoff = align16(K/32)
+ *     bytes [qoff + 16b, +16) block b, byte j = code_j | code_{j+16} << 4
+ * (17 bytes per 32 weights).
+ *
  * Ownership and errors (all entry points):
  *  - Every buffer is caller-owned DEVICE memory; the library allocates
  *    nothing, keeps no pointer after returning and holds no global state.
  *  - `stream` is a hipStream_t passed as void*; NULL is the default stream.
- *    Work is enqueued asynchronously; nothing synchronizes.
+ *    Work is enqueued asynchronously; nothing synchronizes.  Kernels run on
+ *    the current device, which must be the stream's and the buffers'.
  *  - Arguments are validated on the host before anything is enqueued.  A
  *    non-zero (negative) return means nothing was enqueued and every output
  *    is untouched.  A launch failure returns QMM_ERR_DEVICE; faults during
@@ -79,7 +90,8 @@ typedef enum {
     QMM_TYPE_Q8_0 = 3,  /* 32-blocks: fp16 Delta + 32 int8 codes in [-127, 127]   */
     QMM_TYPE_Q4_0 = 4,  /* 32-blocks: fp16 Delta + 32 four-bit codes (value - 8)  */
     QMM_TYPE_Q8_B64 = 5,/* 64-blocks: fp16 Delta + 64 int8 codes in [-127, 127]   */
-    QMM_TYPE_Q4_B64 = 6 /* 64-blocks: fp16 Delta + 64 four-bit codes (value - 8)  */
+    QMM_TYPE_Q4_B64 = 6,/* 64-blocks: fp16 Delta + 64 four-bit codes (value - 8)  */
+    QMM_TYPE_MXFP4 = 7  /* 32-blocks: one power-of-two scale byte + 32 e2m1 codes */
 } qmm_type;
 
 typedef enum {
@@ -91,7 +103,7 @@ typedef enum {
     QMM_ERR_ALIAS       = -5,  /* the output overlaps an input                       */
     QMM_ERR_UNSUPPORTED = -6,  /* n_dims > 2, ne[2] or ne[3] != 1, or K*N too large */
     QMM_ERR_DEVICE      = -7,  /* the HIP runtime refused the launch                 */
-    QMM_ERR_SCRATCH     = -8   /* more scratch than the static array holds           */
+    QMM_ERR_SCRATCH     = -8   /* more scratch than the static array (or workspace) holds */
 } qmm_status;
 
 /* Tensor descriptor ("No Python! ...", §4: Tensor {n_dims, ne[4], nb[4],
@@ -123,7 +135,7 @@ typedef struct qmm_tensor {
  * block, then the block's codes), 34 bytes per 32 Q8_0 weights and 18 per
  * 32 Q4_0 weights, with the scales first and each part 16-byte aligned.
  * Q8_0: align16(ne0/16) + align16(ne0);  Q4_0: align16(ne0/16) + align16(ne0/2);
- * Q8_B64: align16(ne0/32) + align16(ne0);  Q4_B64: align16(ne0/32) + align16(ne0/2). */
+ * Q8_B64: align16(ne0/32) + align16(ne0);  Q4_B64 and MXFP4: align16(ne0/32) + align16(ne0/2). */
 QMM_API size_t qmm_row_size(int32_t type, int64_t ne0);
 
 /* Quantize F32 rows into Q8_0, Q4_0, Q8_B64 or Q4_B64 rows (load time, once
@@ -135,7 +147,13 @@ QMM_API size_t qmm_row_size(int32_t type, int64_t ne0);
  * half away from zero, one IEEE binary32 division by the stored Delta;
  * Q8_0 clamps to [-127, 127], Q4_0 stores code + 8 clamped to [0, 15];
  * Delta = 0 gives all-zero codes.  Bit-exact and deterministic.  Inputs must
- * be finite with amax / 127 (Q8_0) or amax / 8 (Q4_0) below 65520. */
+ * be finite with amax / 127 (Q8_0) or amax / 8 (Q4_0) below 65520.
+ * MXFP4: the scale is 2^e, e = max(floor(log2 amax) - 2, -127), so amax / 2^e is
+ * in [4, 8); each code is w / 2^e rounded to the nearest e2m1 value, ties to
+ * the even code, above 6 to 6, keeping the sign (-0 is code 8).  A zero block
+ * has scale byte 0.  A block holding an infinity or a NaN has scale byte 255
+ * and zero codes: every W' of it is NaN.  src may also be BF16 for dst MXFP4
+ * (data and nb[1] 16-byte aligned): the activations of qmm_gemm. */
 QMM_API int qmm_quantize(const qmm_tensor *src_f32, qmm_tensor *dst_q, void *stream);
 
 /* Quantization rules of qmm_quantize_rule. */
@@ -156,7 +174,7 @@ typedef enum {
  * QMM_ERR_UNSUPPORTED.  Inputs must be finite with amax / 7 below 65520. */
 QMM_API int qmm_quantize_rule(const qmm_tensor *src_f32, qmm_tensor *dst_q, int32_t rule, void *stream);
 
-/* Expand Q8_0 / Q4_0 / Q8_B64 / Q4_B64 / F16 rows to F32 (W' = Delta * code, exact in binary32;
+/* Expand Q8_0 / Q4_0 / Q8_B64 / Q4_B64 / MXFP4 / F16 rows to F32 (W' = Delta * code, exact in binary32;
  * "Development Guide ...", §6.2 step "Dequantization").
  * src ne = [K, M];  dst: F32 ne = [K, M].  Bit-exact. */
 QMM_API int qmm_dequantize(const qmm_tensor *src, qmm_tensor *dst_f32, void *stream);
@@ -165,14 +183,16 @@ QMM_API int qmm_dequantize(const qmm_tensor *src, qmm_tensor *dst_f32, void *str
  * token per step makes every projection a GEMV; Development Guide §6.2: the
  * codes are unpacked to their signed values and scaled before the
  * multiply-add).
- * w: Q8_0, Q4_0, Q8_B64, Q4_B64 or F16, ne = [K, M];  x: F32 ne = [K, N],
+ * w: Q8_0, Q4_0, Q8_B64, Q4_B64, MXFP4 or F16, ne = [K, M];  x: F32 ne = [K, N],
  * 1 <= N <= 8
  * (N > 8: QMM_ERR_SHAPE);  y: F32 ne = [M, N], must not overlap w or x.
  * Each lane keeps its slice of x in registers, which bounds K: the call
  * returns QMM_ERR_UNSUPPORTED when K exceeds 32768 (Q4_0, Q8_0) or 16384
  * (F16), when the row pitch nb[1] of w exceeds 2^28 bytes (loads address
  * a few rows with 32-bit offsets), or when M or the row pitch of x or y (in
- * elements) reaches 2^31.  Tokens are processed in groups that fit
+ * elements) reaches 2^31.  (MXFP4: any K, with a row pitch up to 2^26 bytes;
+ * every product is exact and only the binary32 accumulation rounds; an
+ * infinite activation or a weight above 2^128 may give NaN.)  Tokens are processed in groups that fit
  * the registers (one pass over the weights per group).
  * Weights are read once from HBM and dequantized in registers; binary32
  * multiply-add; the accumulation order is unspecified (results agree with
@@ -192,7 +212,7 @@ QMM_API int qmm_dequantize(const qmm_tensor *src, qmm_tensor *dst_f32, void *str
  * quantized per block too, x_i ~= Delta_x qx_i, the block dot product is
  * Delta Delta_x sum_i q_i qx_i, an integer sum): when x is Q8_0 (ne = [K, N],
  * the activations quantized with qmm_quantize, 1 <= N <= 8), w must be
- * quantized (else QMM_ERR_TYPE; with 64-blocks, Delta_w(m,b) below is the
+ * Q8_0, Q4_0, Q8_B64 or Q4_B64 (else QMM_ERR_TYPE; with 64-blocks, Delta_w(m,b) below is the
  * scale of the 64-block holding the 32-block b) and
  *   y[n][m] = sum_b Delta_w(m,b) Delta_x(n,b) sum_i q_i qx_i
  * with each block's integer sum exact (int8 dot products into int32) and
@@ -249,12 +269,19 @@ QMM_API int qmm_gemv_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up,
                             const qmm_tensor *x_f32, qmm_tensor *h_f32, void *stream);
 
 /* Prefill GEMM ("No Python! ...", §6: C_ij = sum_k A_ik B_kj, with many tokens
- * per step).  w: Q4_0, Q8_0, Q4_B64, Q8_B64 or F16 (F16 with K % 32 == 0, else
+ * per step).  w: Q4_0, Q8_0, Q4_B64, Q8_B64, MXFP4 or F16 (F16 with K % 32 == 0, else
  * QMM_ERR_UNSUPPORTED), ne = [K, M];  x: BF16 ne = [K, N], any N >= 0;
  * y: F32 ne = [M, N], must not overlap w or x.  Weight tiles are dequantized
  * (F16: converted) to bfloat16 (round to nearest even) and multiplied on the
  * bf16 matrix cores with binary32 accumulation (results agree with the exact
- * sum of the weights within 1e-2 * sum_k |W'[m][k] x[n][k]| + 1e-5). */
+ * sum of the weights within 1e-2 * sum_k |W'[m][k] x[n][k]| + 1e-5; MXFP4
+ * weights are exact in bfloat16, so only the accumulation rounds).
+ * x may also be MXFP4, ne = [K, N], with w MXFP4 (else QMM_ERR_TYPE): both are
+ * microscaled (x by qmm_quantize), the scaled matrix instructions multiply the
+ * codes exactly and apply both scales, and the sum of W' x' (x' the values x
+ * stands for) rounds in binary32 only.  qmm_gemm_ws and qmm_gemm_noalloc take
+ * such x too and use no workspace for it; the batch and SwiGLU forms take
+ * BF16 only. */
 QMM_API int qmm_gemm(const qmm_tensor *w, const qmm_tensor *x_bf16, qmm_tensor *y_f32, void *stream);
 
 /* qmm_gemm with a caller-owned workspace that lets a product with too few
@@ -336,6 +363,54 @@ QMM_API int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stre
 QMM_API int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *x_bf16,
                             qmm_tensor *h_f32, void *stream);
 
+/* ---- Mixture-of-experts layer for a few tokens: the feed-forward block of
+ * "Development Guide for Small AI Models (TinyLLaMA, etc.) Using C++", §4.4,
+ * with E experts of which each token uses top_k.  The router's logits are a
+ * matrix product (qmm_gemv, qmm_gemm). */
+#define QMM_MOE_MAX_TOKENS 8      /* tokens of one qmm_moe_swiglu call  */
+#define QMM_MOE_MAX_TOP_K 16      /* experts per token                  */
+#define QMM_MOE_MAX_ROUTED 1024   /* experts qmm_moe_route chooses from */
+
+/* What the weights of the chosen experts are normalized over. */
+typedef enum {
+    QMM_ROUTE_ALL = 0,      /* softmax over all experts                      */
+    QMM_ROUTE_CHOSEN = 1    /* softmax over the chosen experts (they add to 1) */
+} qmm_route_rule;
+
+/* The experts of each token: the top_k largest of its E logits, largest first,
+ * ties to the lower index, and their softmax weights (binary32).
+ * logits: F32 ne = [E, N], any N >= 0, E <= QMM_MOE_MAX_ROUTED (else
+ * QMM_ERR_UNSUPPORTED);  1 <= top_k <= min(E, QMM_MOE_MAX_TOP_K) (else
+ * QMM_ERR_SHAPE);  ids, weights: top_k consecutive values per token, token n's
+ * at ids + n * top_k, 4-byte aligned device memory overlapping neither each
+ * other nor the logits.  A logit of -Inf or NaN masks its expert: it counts
+ * for nothing in the softmax and is never chosen; slots left over when fewer
+ * than top_k experts remain hold id -1 and weight 0.  Infinite logits share
+ * the whole weight. */
+QMM_API int qmm_moe_route(const qmm_tensor *logits_f32, int32_t top_k, int32_t rule, int32_t *ids, float *weights,
+                          void *stream);
+
+/* The chosen experts' SwiGLU blocks:
+ *   y[n] = sum_s weights[n][s] Wd_e (Swish(Wg_e x[n]) * (Wu_e x[n])), e = ids[n][s].
+ * w_gate, w_up: ne = [K, F, E] (n_dims 3, nb[2] bytes between experts, a
+ * multiple of 16, at least one expert's matrix);  w_down: ne = [F, M, E];  all
+ * of one type, Q8_0, Q4_0, Q8_B64, Q4_B64 or MXFP4 (else QMM_ERR_TYPE);
+ * x: F32 ne = [K, N], N <= QMM_MOE_MAX_TOKENS;  y: F32 ne = [M, N];
+ * 1 <= top_k <= QMM_MOE_MAX_TOP_K (else QMM_ERR_SHAPE);  ids, weights: as
+ * qmm_moe_route writes them, read on the device.  A slot whose id is negative
+ * or not below E is empty, whatever its weight; an expert named twice by a
+ * token counts with both weights; a token without experts gets zeros.
+ * Every chosen expert's weights are read once.  The three products and the
+ * epilogue keep binary32 accuracy (the products of weights and activations
+ * are exact, sums and the epilogue round); the result depends on no timing.
+ * workspace: qmm_moe_workspace_size bytes (fewer: QMM_ERR_SCRATCH) of device
+ * memory, 16-byte aligned, overlapping no operand; scratch as in qmm_gemm_ws,
+ * for this call alone until its kernels have run. */
+QMM_API size_t qmm_moe_workspace_size(const qmm_tensor *w_gate, const qmm_tensor *x_f32, int32_t top_k);
+QMM_API int qmm_moe_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *w_down,
+                           const qmm_tensor *x_f32, const int32_t *ids, const float *weights, int32_t top_k,
+                           qmm_tensor *y_f32, void *workspace, size_t workspace_bytes, void *stream);
+
 /* GGUF-style block records ("Development Guide for Small AI Models (TinyLLaMA,
  * etc.) Using C++", §3.2: a GGUF file's tensor data is an aligned array;
  * §6.1: a Q4_0 block is one FP16 scale (2 bytes) followed by 32 4-bit
@@ -358,7 +433,7 @@ QMM_API int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, co
  * M * K/32 records of src_q to `records`.  Both are bit-exact and
  * asynchronous on `stream`.
  * Errors: QMM_ERR_NULL (no tensor, or NULL records for a non-empty tensor),
- * QMM_ERR_TYPE (not Q8_0 / Q4_0: the _B64 types have no GGUF record), QMM_ERR_SHAPE / QMM_ERR_LAYOUT (the tensor
+ * QMM_ERR_TYPE (not Q8_0 / Q4_0: the _B64 types and MXFP4 have no record here), QMM_ERR_SHAPE / QMM_ERR_LAYOUT (the tensor
  * rules), QMM_ERR_LAYOUT (records not 16-byte aligned), QMM_ERR_ALIAS
  * (records overlap the rows), QMM_ERR_UNSUPPORTED (M * K/32 >= 2^31).
  * An empty tensor enqueues nothing. */

@@ -18,9 +18,10 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqmm.so")
 
 # qmm_type
-F32, F16, BF16, Q8_0, Q4_0, Q8_B64, Q4_B64 = 0, 1, 2, 3, 4, 5, 6
+F32, F16, BF16, Q8_0, Q4_0, Q8_B64, Q4_B64, MXFP4 = 0, 1, 2, 3, 4, 5, 6, 7
 TYPE_NAMES = {F32: "F32", F16: "F16", BF16: "BF16", Q8_0: "Q8_0", Q4_0: "Q4_0",
-              Q8_B64: "Q8_B64", Q4_B64: "Q4_B64"}
+              Q8_B64: "Q8_B64", Q4_B64: "Q4_B64",
+              MXFP4: "MXFP4"}
 
 # qmm_status
 OK, ERR_NULL, ERR_TYPE, ERR_SHAPE, ERR_LAYOUT, ERR_ALIAS, ERR_UNSUPPORTED, ERR_DEVICE, ERR_SCRATCH = \
@@ -29,8 +30,11 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 
 EXPORTS = ("qmm_row_size", "qmm_quantize", "qmm_quantize_rule", "qmm_dequantize", "qmm_gemv", "qmm_gemv_batch",
            "qmm_gemv_swiglu", "qmm_gemm", "qmm_gemm_ws", "qmm_gemm_noalloc", "qmm_gemm_workspace_size", "qmm_gemm_batch", "qmm_gemm_swiglu", "qmm_record_size", "qmm_records_to_rows",
-           "qmm_rows_to_records", "qmm_stream_read", "qmm_clock_probe", "qmm_wall_clock_khz", "qmm_strerror")
+           "qmm_rows_to_records", "qmm_moe_route", "qmm_moe_workspace_size", "qmm_moe_swiglu", "qmm_stream_read", "qmm_clock_probe", "qmm_wall_clock_khz", "qmm_strerror")
 GEMV_BATCH_MAX = 8
+MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_MAX_ROUTED = 8, 16, 1024
+# qmm_route_rule
+ROUTE_ALL, ROUTE_CHOSEN = 0, 1
 
 
 class QmmTensor(ctypes.Structure):
@@ -99,6 +103,13 @@ def lib() -> ctypes.CDLL:
         h.qmm_rows_to_records.restype = ctypes.c_int
         h.qmm_gemv_batch.argtypes = [ctypes.POINTER(QmmGemvItem), ctypes.c_int32, ctypes.c_void_p]
         h.qmm_gemv_batch.restype = ctypes.c_int
+        V, I = ctypes.c_void_p, ctypes.c_int32
+        h.qmm_moe_route.argtypes = [P, I, I, V, V, V]
+        h.qmm_moe_route.restype = ctypes.c_int
+        h.qmm_moe_workspace_size.argtypes = [P, P, I]
+        h.qmm_moe_workspace_size.restype = ctypes.c_size_t
+        h.qmm_moe_swiglu.argtypes = [P, P, P, P, V, V, I, P, V, ctypes.c_size_t, V]
+        h.qmm_moe_swiglu.restype = ctypes.c_int
         for f in ("qmm_quantize", "qmm_dequantize", "qmm_gemv", "qmm_gemm"):
             getattr(h, f).restype = ctypes.c_int
         h.qmm_stream_read.argtypes = [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int32,
@@ -142,7 +153,7 @@ def make_desc(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int, n_dims: i
 class Weight:
     """A weight matrix W (ne = [K, M]): M rows of K weights on the GPU.
 
-    data is uint8 (M, pitch) for quantized rows (Q8_0, Q4_0, Q8_B64, Q4_B64) in the row-planar layout of
+    data is uint8 (M, pitch) for quantized rows (Q8_0, Q4_0, Q8_B64, Q4_B64, MXFP4) in the row-planar layout of
     include/qmm.h, or float16 (M, >= K) for F16 rows."""
     data: torch.Tensor
     type: int
@@ -196,7 +207,8 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
              stream=None) -> Weight:
     """Quantize fp32 rows w (M, K) on the GPU into Q8_0 / Q4_0 rows, or their
     64-weight-block variants Q8_B64 / Q4_B64 (rule: QUANT_DEFAULT, or
-    QUANT_Q4_AMAX7 for the symmetric amax/7 Q4 rule)."""
+    QUANT_Q4_AMAX7 for the symmetric amax/7 Q4 rule), or MXFP4 rows (fp32 or
+    bf16 w)."""
     _need_gpu(w)
     M, K = w.shape
     rs = row_size(type_, K)
@@ -205,7 +217,7 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
     if pitch > rs:
         out[:, rs:].zero_()
     wt = Weight(out, type_, K, M)
-    src, dst = _dense_desc(w, F32), wt.desc()
+    src, dst = _dense_desc(w, BF16 if w.dtype == torch.bfloat16 else F32), wt.desc()
     _check(lib().qmm_quantize_rule(ctypes.byref(src), ctypes.byref(dst), rule, _stream(stream)),
            "qmm_quantize_rule")
     return wt
@@ -326,22 +338,28 @@ def gemm_workspace_size(w: Weight, x: torch.Tensor) -> int:
     return int(lib().qmm_gemm_workspace_size(ctypes.byref(wd), ctypes.byref(xd)))
 
 
-def gemm(w: Weight, x: torch.Tensor, *, out: torch.Tensor | None = None, workspace="auto",
+def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
          stream=None) -> torch.Tensor:
-    """y (N, M) fp32 = x (N, K) bf16 times W'^T on the bf16 matrix cores.
+    """y (N, M) fp32 = x (N, K) bf16 times W'^T on the bf16 matrix cores, or, for
+    an MXFP4 w, an MXFP4 Weight x of N rows on the scaled matrix instructions.
 
     workspace: "auto" allocates the split-K workspace the shapes call for (a
     torch allocation, so it is graph-capture safe), None runs without one
     (qmm_gemm), or a uint8 device tensor to use as is."""
-    _need_gpu(w.data, x)
+    if isinstance(x, Weight):
+        _need_gpu(w.data, x.data)
+        n, dev, xd = x.M, x.data.device, x.desc()
+    else:
+        _need_gpu(w.data, x)
+        n, dev, xd = x.shape[0], x.device, _dense_desc(x, BF16)
     if out is None:
-        out = torch.empty((x.shape[0], w.M), dtype=torch.float32, device=x.device)
-    wd, xd, yd = w.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
+        out = torch.empty((n, w.M), dtype=torch.float32, device=dev)
+    wd, yd = w.desc(), _dense_desc(out, F32)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         n = int(lib().qmm_gemm_workspace_size(ctypes.byref(wd), ctypes.byref(xd)))
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         if workspace is not None and stream is not None:
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
@@ -399,6 +417,87 @@ def gemm_batch(items, *, stream=None) -> list:
     arr = (QmmGemmItem * max(1, len(descs)))(*descs)
     _check(lib().qmm_gemm_batch(arr, len(descs), _stream(stream)), "qmm_gemm_batch")
     return outs
+
+
+@dataclass
+class Experts:
+    """E weight matrices of one type and shape (ne = [K, M, E]): data is uint8
+    (E, M, pitch), quantized rows of K weights as in Weight."""
+    data: torch.Tensor
+    type: int
+    K: int
+    M: int
+
+    def desc(self) -> QmmTensor:
+        t = make_desc(self.type, self.K, self.M, self.data.stride(1) * self.data.element_size(), self.data.data_ptr(),
+                      n_dims=3)
+        t.ne[2], t.nb[2] = self.data.shape[0], self.data.stride(0) * self.data.element_size()
+        return t
+
+    def expert(self, e: int) -> Weight:
+        """Expert e's matrix: no copy."""
+        return Weight(self.data[e], self.type, self.K, self.M)
+
+
+def quantize_experts(w: torch.Tensor, type_: int, *, stream=None) -> Experts:
+    """Quantize fp32 matrices w (E, M, K) on the GPU into Experts."""
+    if w.dim() != 3:
+        raise ValueError("expected a 3-D tensor")
+    E, M, K = w.shape
+    q = quantize(w.reshape(E * M, K), type_, stream=stream)
+    return Experts(q.data.view(E, M, -1), type_, K, M)
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, stream=None) -> tuple:
+    """(ids int32, weights fp32), each (N, top_k): every token's top_k experts of
+    its logits (N, E) fp32, largest first, with softmax weights over all
+    experts (ROUTE_ALL) or over the chosen ones (ROUTE_CHOSEN).  Experts
+    masked by -inf are never chosen; empty slots hold id -1 and weight 0."""
+    _need_gpu(logits)
+    n = logits.shape[0]
+    ids = torch.empty((n, top_k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((n, top_k), dtype=torch.float32, device=logits.device)
+    ld = _dense_desc(logits, F32)
+    _check(lib().qmm_moe_route(ctypes.byref(ld), top_k, rule, ctypes.c_void_p(ids.data_ptr()),
+                               ctypes.c_void_p(weights.data_ptr()), _stream(stream)), "qmm_moe_route")
+    return ids, weights
+
+
+def moe_workspace_size(w_gate: Experts, x: torch.Tensor, top_k: int) -> int:
+    """Bytes of workspace qmm_moe_swiglu needs for these shapes."""
+    gd, xd = w_gate.desc(), _dense_desc(x, F32)
+    return int(lib().qmm_moe_workspace_size(ctypes.byref(gd), ctypes.byref(xd), top_k))
+
+
+def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor, ids: torch.Tensor,
+               weights: torch.Tensor, *, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """y (N, M) fp32: the sum over each token's slots of weights times the
+    SwiGLU block of expert ids (int32), both (N, top_k) and contiguous;
+    x (N, K) fp32, N <= 8.  workspace: a uint8 device tensor of at least
+    moe_workspace_size bytes, or None to allocate one (graph-capture safe)."""
+    _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights)
+    top_k = ids.shape[1]
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("ids must be int32 and weights float32")
+    if ids.shape != weights.shape or ids.shape[0] != x.shape[0] or not (ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous and (N, top_k)")
+    if out is None:
+        out = torch.empty((x.shape[0], w_down.M), dtype=torch.float32, device=x.device)
+    gd, ud, dd, xd, yd = w_gate.desc(), w_up.desc(), w_down.desc(), _dense_desc(x, F32), _dense_desc(out, F32)
+    if workspace is None:
+        n = int(lib().qmm_moe_workspace_size(ctypes.byref(gd), ctypes.byref(xd), top_k))
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        if stream is not None:
+            # freed when this call returns: keep the allocator from handing it
+            # out again before the kernels on `stream` have run
+            workspace.record_stream(stream)
+    _need_gpu(workspace)
+    _check(lib().qmm_moe_swiglu(ctypes.byref(gd), ctypes.byref(ud), ctypes.byref(dd), ctypes.byref(xd),
+                                ctypes.c_void_p(ids.data_ptr()), ctypes.c_void_p(weights.data_ptr()), top_k,
+                                ctypes.byref(yd), ctypes.c_void_p(workspace.data_ptr()),
+                                workspace.numel() * workspace.element_size(), _stream(stream)), "qmm_moe_swiglu")
+    return out
 
 
 def call_batch_raw(triples, count=None, stream: int = 0) -> int:

@@ -15,8 +15,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqmm.so")
-SOURCES = ["qmm_api.cpp", "quant.hip", "gemv.hip", "gemv_i8.hip", "gemv_mf.hip",
-           "gemm.hip", "gemm_rq.hip", "records.hip", "probe.hip"]
+SOURCES = ["qmm_api.cpp", "moe_api.cpp", "quant.hip", "gemv.hip", "gemv_i8.hip", "gemv_mf.hip",
+           "gemv_mx.hip", "gemm.hip", "gemm_rq.hip", "gemm_mx.hip", "moe.hip", "records.hip", "probe.hip"]
 ARCH = os.environ.get("QMM_OFFLOAD_ARCH", "gfx950")
 
 

@@ -193,6 +193,7 @@ hipError_t launch_gemm(const WeightView &w, const ActView &x, const OutView &y,
                        float *ws, uint64_t ws_bytes, hipStream_t stream)
 {
     if (w.M == 0 || x.N == 0) return hipSuccess;
+    if (x.type == W_MXFP4) return launch_gemm_mx(w, x, y, stream);
     const GemmPlan plan = gemm_plan(w.M, w.K, x.N, ws ? ws_bytes : 0);
     return launch_items(&w, &x, &y, 1, plan, ws, stream);
 }

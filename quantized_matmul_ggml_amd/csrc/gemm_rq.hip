@@ -1,4 +1,4 @@
-// gemm_rq.hip -- prefill GEMM for Q4_0 / Q8_0 weights with the codes
+// gemm_rq.hip -- prefill GEMM for Q4_0 / Q8_0 / MXFP4 weights with the codes
 // dequantized in the registers of the waves that multiply them.
 //
 // Y[n][m] = sum_k W'[m][k] * X[n][k] for a tile of 128 weight rows x 128
@@ -60,6 +60,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 template <int WT> struct RqFmt;
 template <> struct RqFmt<W_Q4_0> { static constexpr int QB = 16, GS = 4; };
 template <> struct RqFmt<W_Q8_0> { static constexpr int QB = 32, GS = 2; };
+// MXFP4: Q4_0's code bytes; its one-byte scales are staged like fp16 scales
+// that two 32-blocks share (SS = 1), a 2-byte unit holding both bytes
+template <> struct RqFmt<W_MXFP4> { static constexpr int QB = 16, GS = 4; };
 // F16 rows: 64 bytes per 32 weights, no scales; a group is one K-step
 template <> struct RqFmt<W_F16> { static constexpr int QB = 64, GS = 1; };
 template <int WT>
@@ -214,6 +217,29 @@ struct Deq<W_Q8_0> {
     }
 };
 
+// MXFP4: v_cvt_scalef32_pk_bf16_fp4 turns the two nibbles of one byte into
+// two bf16 values times the power of two in its third operand, exactly (two
+// significant bits), and to NaN where the scale byte is 255; the even and odd
+// bytes' nibbles are first put side by side, so that a pair holds
+// neighbouring k.
+template <>
+struct Deq<W_MXFP4> {
+    uint32_t v;
+    float d;
+    template <int P>
+    __device__ inline void part(u32x2 c, uint32_t sbyte, bool live, uint32_t (&b)[8])
+    {
+        // part P: b[4 (P / 4) + 2 i + (P % 2)] of dword i = (P / 2) % 2
+        constexpr int chunk = P / 4, i = (P / 2) % 2, odd = P % 2;
+        if constexpr (P == 0) d = __builtin_bit_cast(float, live ? sbyte << 23 : 0u);
+        if constexpr (odd == 0) {
+            const uint32_t t = chunk == 0 ? c[i] & 0x0F0F0F0Fu : (c[i] >> 4) & 0x0F0F0F0Fu;
+            v = t | (t >> 4);
+        }
+        b[P] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, d, odd == 0 ? 0 : 2));
+    }
+};
+
 // F16: the lane's 16 weights are two runs of 8 halves (k = 8 h .. 8 h + 7 of
 // each chunk); each becomes the bf16 rounding (nearest even) of its exact
 // binary32 value.  A block past K reads the next row's bytes, which may be
@@ -362,7 +388,8 @@ __global__ __launch_bounds__(THREADS) void gemm_rq_kernel(const GemmArgs a)
         // dwords past the group's scales read zeros in every group
         soff[i] = 2 * sdw < SPG ? (uint32_t)((row - lrow) * pm) + 2u * (uint32_t)((2 * s0) >> SS) + 4u * sdw : OUT_OF_RANGE;
     }
-    const int64_t nscales = nblk_r >> SS;        // scales of the range
+    // scales of the range (2-byte units: an odd MXFP4 block count ends inside one)
+    const int64_t nscales = WT == W_MXFP4 ? (nblk_r + 1) >> 1 : nblk_r >> SS;
     // FAST: group g is known to be < full_groups
     auto code_load = [&](auto FAST, int i, int g) {
         const uint32_t dst = lds0 + LDS_GROUP_OFF + (uint32_t)((g % NB) * GROUP_BYTES) + 1024u * (CODE_LOADS * cw + i);
@@ -400,7 +427,7 @@ __global__ __launch_bounds__(THREADS) void gemm_rq_kernel(const GemmArgs a)
             const int unit = WT == W_F16 ? 4 * bi + 2 * c + h : (QB / 16) * bi + c;
             crd[u][c] = (uint32_t)(rl * 128 + 16 * (unit ^ ((rl >> 1) & 7)) + (WT == W_F16 ? 0 : 8 * h));
         }
-        srd[u] = (uint32_t)(rl * 16 + 2 * (bi >> SS));
+        srd[u] = (uint32_t)(rl * 16 + (WT == W_MXFP4 ? bi : 2 * (bi >> SS)));
     }
     uint32_t trd[4][2];           // token offsets (within a stage) of tile j, chunk c
 #pragma unroll
@@ -437,7 +464,9 @@ __global__ __launch_bounds__(THREADS) void gemm_rq_kernel(const GemmArgs a)
             r.c0 = *reinterpret_cast<const u32x4 *>(cg + crd[u][0]);
             r.c1 = *reinterpret_cast<const u32x4 *>(cg + crd[u][1]);
         } else {
-            r.sbits = *reinterpret_cast<const uint16_t *>(lds + LDS_SCALE_OFF + gb * SGROUP_BYTES + srd[u]);
+            const uint8_t *sp = lds + LDS_SCALE_OFF + gb * SGROUP_BYTES + srd[u];
+            if constexpr (WT == W_MXFP4) r.sbits = *sp;
+            else r.sbits = *reinterpret_cast<const uint16_t *>(sp);
             r.c0 = *reinterpret_cast<const u32x2 *>(cg + crd[u][0]);
             r.c1 = QB == 32 ? *reinterpret_cast<const u32x2 *>(cg + crd[u][CR - 1]) : r.c0;
         }
@@ -448,7 +477,7 @@ __global__ __launch_bounds__(THREADS) void gemm_rq_kernel(const GemmArgs a)
     auto dequant_part = [&](auto P, const Raw &r, int s, uint32_t (&b)[8]) {
         constexpr int p = decltype(P)::value;
         const bool live = 2 * s + par < nblk32;
-        if constexpr (WT == W_Q4_0) dq.template part<p>(r.c0, r.sbits, live, b);
+        if constexpr (WT == W_Q4_0 || WT == W_MXFP4) dq.template part<p>(r.c0, r.sbits, live, b);
         else if constexpr (WT == W_Q8_0) dq.template part<p>(r.c0, r.c1, r.sbits, live, b);
         else dq.template part<p>(r.c0, r.c1, live, b);
     };
@@ -641,13 +670,14 @@ hipError_t launch_rq(const GemmArgs &a, unsigned blocks, bool sw, hipStream_t st
 
 bool gemm_rq_handles(int type)
 {
-    return type == W_Q4_0 || type == W_Q8_0 || type == W_F16;
+    return type == W_Q4_0 || type == W_Q8_0 || type == W_F16 || type == W_MXFP4;
 }
 
 hipError_t launch_gemm_rq(const GemmArgs &a, unsigned blocks, int type, int ss, bool sw, hipStream_t stream)
 {
     if (type == W_Q4_0) return ss ? launch_rq<W_Q4_0, 1>(a, blocks, sw, stream) : launch_rq<W_Q4_0, 0>(a, blocks, sw, stream);
     if (type == W_Q8_0) return ss ? launch_rq<W_Q8_0, 1>(a, blocks, sw, stream) : launch_rq<W_Q8_0, 0>(a, blocks, sw, stream);
+    if (type == W_MXFP4) return launch_rq<W_MXFP4, 1>(a, blocks, sw, stream);
     if (type == W_F16 && !ss) return launch_rq<W_F16, 0>(a, blocks, sw, stream);
     return hipErrorInvalidValue;
 }

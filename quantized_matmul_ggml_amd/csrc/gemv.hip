@@ -959,6 +959,7 @@ hipError_t launch_gemv_batch(const GemvTask *tasks, int count, hipStream_t strea
     int64_t m_total = 0;
     for (int i = 0; i < count; ++i) m_total += tasks[i].w.M;
     if (m_total == 0 || N == 0) return hipSuccess;
+    if (type == W_MXFP4) return launch_gemv_mx(tasks, count, stream);
     // The matrix-core kernels' cost does not grow with the token count.
     const bool mf = type == W_F16 ? use_matrix_cores_f16(N, m_total, K) : use_matrix_cores(N, m_total, K);
     if (mf && gemv_mf_supported(tasks, count)) return launch_gemv_mf(tasks, count, stream);
@@ -1030,6 +1031,7 @@ hipError_t launch_gemv_swiglu(const WeightView &wg, const WeightView &wu, const 
     const int type = wg.type;
     const int64_t K = wg.K, M = wg.M, N = x.N;
     if (M == 0 || N == 0) return hipSuccess;
+    if (type == W_MXFP4) return launch_gemv_mx_swiglu(wg, wu, x, h, stream);
     // From 3 tokens the matrix-core kernel (2 x 5632 x 2048 Q4_0, graph-
     // replayed, 3 / 8 tokens: 7.8 / 8.2 us against 9.9 / 21.0 us here).
     if (N >= 3 && gemv_mf_swiglu_supported(wg, wu, x)) return launch_gemv_mf_swiglu(wg, wu, x, h, stream);

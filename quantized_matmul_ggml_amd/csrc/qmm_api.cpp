@@ -8,113 +8,11 @@
 // ne[0] contiguous).  Operand roles of MUL_MAT: same page, §5 (the result
 // takes ne = {a.ne[0], b.ne[1]} with b "transposed") read together with the
 // stride definition: W ne = [K, M], x ne = [K, N], y ne = [M, N].
-#include "../../include/qmm.h"
-#include "qmm_internal.h"
+#include "api_checks.h"
+
+using namespace qmm::api;
 
 namespace {
-
-using qmm::W_BF16;
-using qmm::W_F16;
-using qmm::W_F32;
-using qmm::W_Q4_0;
-using qmm::W_Q8_0;
-
-bool is_quant(int t)
-{
-    return t == QMM_TYPE_Q8_0 || t == QMM_TYPE_Q4_0 || t == QMM_TYPE_Q8_B64 || t == QMM_TYPE_Q4_B64;
-}
-bool is_b64(int t) { return t == QMM_TYPE_Q8_B64 || t == QMM_TYPE_Q4_B64; }
-// Weights per fp16 scale of a quantized type.
-int64_t block_len(int t) { return is_b64(t) ? 64 : 32; }
-
-int64_t elem_size(int t)
-{
-    switch (t) {
-    case QMM_TYPE_F32: return 4;
-    case QMM_TYPE_F16: return 2;
-    case QMM_TYPE_BF16: return 2;
-    default: return 0;
-    }
-}
-
-// Largest element count per dimension and byte span of one tensor the
-// library accepts (far beyond any device memory, and small enough that
-// every size computed from them fits 64 bits).
-constexpr int64_t kMaxElems = (int64_t)1 << 48;
-constexpr uint64_t kMaxSpan = 1ull << 62;
-
-// Shape / layout rules shared by every operand.  `align` is the byte
-// alignment required of data and nb[1].
-int check_tensor(const qmm_tensor *t, uint64_t align)
-{
-    if (!t) return QMM_ERR_NULL;
-    if (t->type < QMM_TYPE_F32 || t->type > QMM_TYPE_Q4_B64) return QMM_ERR_TYPE;
-    if (t->n_dims < 1 || t->n_dims > 4) return QMM_ERR_UNSUPPORTED;
-    if (t->n_dims > 2 || t->ne[2] != 1 || t->ne[3] != 1) return QMM_ERR_UNSUPPORTED;
-    if (t->ne[0] < 0 || t->ne[1] < 0) return QMM_ERR_SHAPE;
-    if (t->ne[0] > kMaxElems || t->ne[1] > kMaxElems) return QMM_ERR_UNSUPPORTED;
-    if (t->n_dims == 1 && t->ne[1] != 1) return QMM_ERR_SHAPE;
-    if (is_quant(t->type)) {
-        if (t->ne[0] % block_len(t->type) != 0) return QMM_ERR_SHAPE;
-        if (t->nb[0] != 0) return QMM_ERR_LAYOUT;
-    } else if ((int64_t)t->nb[0] != elem_size(t->type)) {
-        return QMM_ERR_LAYOUT;
-    }
-    const uint64_t rs = qmm_row_size(t->type, t->ne[0]);
-    if (t->ne[1] > 1 && t->nb[1] < rs) return QMM_ERR_LAYOUT;
-    if (t->ne[1] > 1 && t->nb[1] % align != 0) return QMM_ERR_LAYOUT;
-    // the bytes the tensor spans must be a range of the address space
-    uint64_t span = rs;
-    if (t->ne[1] > 1) {
-        uint64_t rows;
-        if (__builtin_mul_overflow((uint64_t)(t->ne[1] - 1), t->nb[1], &rows) || rows > kMaxSpan)
-            return QMM_ERR_UNSUPPORTED;
-        span = rows + rs;
-    }
-    if (span > kMaxSpan || (uintptr_t)t->data > UINTPTR_MAX - span) return QMM_ERR_UNSUPPORTED;
-    const bool empty = t->ne[0] == 0 || t->ne[1] == 0;
-    if (!t->data && !empty) return QMM_ERR_NULL;
-    if ((uintptr_t)t->data % align != 0) return QMM_ERR_LAYOUT;
-    return QMM_OK;
-}
-
-// Byte range [lo, hi) a 2-D tensor touches.
-void extent(const qmm_tensor *t, uintptr_t *lo, uintptr_t *hi)
-{
-    const uint64_t rs = qmm_row_size(t->type, t->ne[0]);
-    *lo = (uintptr_t)t->data;
-    *hi = *lo + (t->ne[1] > 0 ? (uint64_t)(t->ne[1] - 1) * t->nb[1] + rs : 0);
-}
-
-bool overlaps(const qmm_tensor *a, const qmm_tensor *b)
-{
-    uintptr_t alo, ahi, blo, bhi;
-    extent(a, &alo, &ahi);
-    extent(b, &blo, &bhi);
-    if (alo == ahi || blo == bhi) return false;
-    return alo < bhi && blo < ahi;
-}
-
-qmm::WeightView weight_view(const qmm_tensor *w)
-{
-    qmm::WeightView v;
-    v.base = static_cast<const uint8_t *>(w->data);
-    v.pitch = w->ne[1] > 1 ? w->nb[1] : qmm_row_size(w->type, w->ne[0]);
-    v.K = w->ne[0];
-    v.M = w->ne[1];
-    // the 64-block types are their code format with one scale per two runs
-    v.type = w->type == QMM_TYPE_Q8_B64 ? W_Q8_0 : w->type == QMM_TYPE_Q4_B64 ? W_Q4_0 : w->type;
-    v.scale_shift = is_b64(w->type) ? 1 : 0;
-    return v;
-}
-
-uint64_t pitch_elems(const qmm_tensor *t)
-{
-    const int64_t es = elem_size(t->type);
-    return t->ne[1] > 1 ? t->nb[1] / (uint64_t)es : (uint64_t)t->ne[0];
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? QMM_OK : QMM_ERR_DEVICE; }
 
 // Common checks of MUL_MAT operands.
 int check_mul_mat(const qmm_tensor *w, const qmm_tensor *x, const qmm_tensor *y,
@@ -151,6 +49,7 @@ size_t qmm_row_size(int32_t type, int64_t ne0)
     case QMM_TYPE_Q4_0: return (k % 32) ? 0 : a16(k / 16) + a16(k / 2);
     case QMM_TYPE_Q8_B64: return (k % 64) ? 0 : a16(k / 32) + a16(k);
     case QMM_TYPE_Q4_B64: return (k % 64) ? 0 : a16(k / 32) + a16(k / 2);
+    case QMM_TYPE_MXFP4: return (k % 32) ? 0 : a16(k / 32) + a16(k / 2);
     default: return 0;
     }
 }
@@ -164,11 +63,13 @@ int qmm_quantize_rule(const qmm_tensor *src, qmm_tensor *dst, int32_t rule, void
 {
     if (rule != QMM_QUANT_DEFAULT && rule != QMM_QUANT_Q4_AMAX7) return QMM_ERR_UNSUPPORTED;
     if (!src || !dst) return QMM_ERR_NULL;
-    int rc = check_tensor(src, 4);
+    // BF16 rows (16-byte aligned, as qmm_gemm takes them) go to MXFP4 only
+    const bool bf16 = src->type == QMM_TYPE_BF16 && dst->type == QMM_TYPE_MXFP4;
+    int rc = check_tensor(src, bf16 ? 16 : 4);
     if (rc) return rc;
     rc = check_tensor(dst, 16);
     if (rc) return rc;
-    if (src->type != QMM_TYPE_F32 || !is_quant(dst->type)) return QMM_ERR_TYPE;
+    if (!(src->type == QMM_TYPE_F32 || bf16) || !is_quant(dst->type)) return QMM_ERR_TYPE;
     if (src->ne[0] != dst->ne[0] || src->ne[1] != dst->ne[1]) return QMM_ERR_SHAPE;
     if (src->ne[0] % block_len(dst->type) != 0) return QMM_ERR_SHAPE;
     if (overlaps(dst, src)) return QMM_ERR_ALIAS;
@@ -177,7 +78,8 @@ int qmm_quantize_rule(const qmm_tensor *src, qmm_tensor *dst, int32_t rule, void
     const qmm::WeightView d = weight_view(dst);
     return status_of(qmm::launch_quantize(static_cast<const float *>(src->data), pitch_elems(src),
                                           src->ne[0], src->ne[1],
-                                          static_cast<uint8_t *>(dst->data), d.pitch, d.type,
+                                          static_cast<uint8_t *>(dst->data), d.pitch,
+                                          d.type | (bf16 ? qmm::kSrcBf16 : 0),
                                           static_cast<hipStream_t>(stream),
                                           rule == QMM_QUANT_Q4_AMAX7, d.scale_shift));
 }
@@ -205,7 +107,7 @@ int qmm_gemv(const qmm_tensor *w, const qmm_tensor *x, qmm_tensor *y, void *stre
         // the integer-activation path ("A Complete Guide to llama.cpp ...", §2.2)
         int rc = check_mul_mat(w, x, y, QMM_TYPE_Q8_0, 16);
         if (rc) return rc;
-        if (!is_quant(w->type)) return QMM_ERR_TYPE;
+        if (!is_int_quant(w->type)) return QMM_ERR_TYPE;
         if (x->ne[1] > 8) return QMM_ERR_SHAPE;
         if (x->ne[1] == 0 || w->ne[1] == 0) return QMM_OK;
         const qmm::WeightView wv = weight_view(w), xv = weight_view(x);
@@ -223,8 +125,10 @@ int qmm_gemv(const qmm_tensor *w, const qmm_tensor *x, qmm_tensor *y, void *stre
     if (x->ne[1] == 0 || w->ne[1] == 0) return QMM_OK;
     // The activation slice of every lane lives in registers (at most 128
     // floats per lane), which bounds K; tokens are split into chunks that fit.
+    // (The MXFP4 kernel keeps activations in LDS, a range of K at a time.)
     qmm::GemvConfig cfg;
-    if (!qmm::gemv_config(weight_view(w).type, w->ne[0], w->ne[1], 1, &cfg)) return QMM_ERR_UNSUPPORTED;
+    if (w->type != QMM_TYPE_MXFP4 && !qmm::gemv_config(weight_view(w).type, w->ne[0], w->ne[1], 1, &cfg))
+        return QMM_ERR_UNSUPPORTED;
     qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
     qmm::OutView yv{static_cast<float *>(y->data), pitch_elems(y)};
     if (!qmm::gemv_supported(weight_view(w), xv, yv)) return QMM_ERR_UNSUPPORTED;
@@ -244,7 +148,7 @@ int qmm_gemv_batch(const qmm_gemv_item *items, int32_t count, void *stream)
         const qmm_tensor *w = items[i].w, *x = items[i].x_f32, *y = items[i].y_f32;
         int rc = i8 ? check_mul_mat(w, x, y, QMM_TYPE_Q8_0, 16) : check_mul_mat(w, x, y, QMM_TYPE_F32, 4);
         if (rc) return rc;
-        if (i8 ? !is_quant(w->type) : !(is_quant(w->type) || w->type == QMM_TYPE_F16)) return QMM_ERR_TYPE;
+        if (i8 ? !is_int_quant(w->type) : !(is_quant(w->type) || w->type == QMM_TYPE_F16)) return QMM_ERR_TYPE;
         if (x->ne[1] > 8) return QMM_ERR_SHAPE;
         if (i > 0) {
             const qmm_tensor *w0 = items[0].w, *x0 = items[0].x_f32;
@@ -283,7 +187,8 @@ int qmm_gemv_batch(const qmm_gemv_item *items, int32_t count, void *stream)
         return status_of(qmm::launch_gemv_i8_batch(wv, xv, yv, count, N, static_cast<hipStream_t>(stream)));
     }
     qmm::GemvConfig cfg;
-    if (!qmm::gemv_config(tasks[0].w.type, items[0].w->ne[0], m_total, 1, &cfg))
+    if (items[0].w->type != QMM_TYPE_MXFP4 &&
+        !qmm::gemv_config(tasks[0].w.type, items[0].w->ne[0], m_total, 1, &cfg))
         return QMM_ERR_UNSUPPORTED;
     return status_of(qmm::launch_gemv_batch(tasks, count, static_cast<hipStream_t>(stream)));
 }
@@ -297,7 +202,7 @@ int qmm_gemv_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_
         if (rc) return rc;
         rc = check_mul_mat(w_up, x, h, QMM_TYPE_Q8_0, 16);
         if (rc) return rc;
-        if (!is_quant(w_gate->type)) return QMM_ERR_TYPE;
+        if (!is_int_quant(w_gate->type)) return QMM_ERR_TYPE;
         if (w_up->type != w_gate->type) return QMM_ERR_TYPE;
         if (w_up->ne[0] != w_gate->ne[0] || w_up->ne[1] != w_gate->ne[1]) return QMM_ERR_SHAPE;
         if (x->ne[1] > 8) return QMM_ERR_SHAPE;
@@ -321,7 +226,8 @@ int qmm_gemv_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_
     if (x->ne[1] > 8) return QMM_ERR_SHAPE;
     if (x->ne[1] == 0 || w_gate->ne[1] == 0) return QMM_OK;
     qmm::GemvConfig cfg;
-    if (!qmm::gemv_config(weight_view(w_gate).type, w_gate->ne[0], 2 * w_gate->ne[1], 1, &cfg))
+    if (w_gate->type != QMM_TYPE_MXFP4 &&
+        !qmm::gemv_config(weight_view(w_gate).type, w_gate->ne[0], 2 * w_gate->ne[1], 1, &cfg))
         return QMM_ERR_UNSUPPORTED;
     qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
     qmm::OutView hv{static_cast<float *>(h->data), pitch_elems(h)};
@@ -380,16 +286,18 @@ int qmm_rows_to_records(const qmm_tensor *src, void *records, void *stream)
 
 namespace {
 
-int check_gemm(const qmm_tensor *w, const qmm_tensor *x, const qmm_tensor *y)
+// mx_x: whether MXFP4 activations are accepted (with MXFP4 weights).
+int check_gemm(const qmm_tensor *w, const qmm_tensor *x, const qmm_tensor *y, bool mx_x)
 {
-    const int rc = check_mul_mat(w, x, y, QMM_TYPE_BF16, 16);
+    const bool mx = mx_x && x && x->type == QMM_TYPE_MXFP4;
+    const int rc = check_mul_mat(w, x, y, mx ? QMM_TYPE_MXFP4 : QMM_TYPE_BF16, 16);
     if (rc) return rc;
+    if (mx && w->type != QMM_TYPE_MXFP4) return QMM_ERR_TYPE;
     if (!(is_quant(w->type) || w->type == QMM_TYPE_F16)) return QMM_ERR_TYPE;
     // the GEMM stages F16 rows in whole 32-weight blocks
     if (w->type == QMM_TYPE_F16 && w->ne[0] % 32 != 0) return QMM_ERR_UNSUPPORTED;
     if (w->ne[1] == 0 || x->ne[1] == 0) return QMM_OK;
-    qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
-    if (!qmm::gemm_supported(weight_view(w), xv)) return QMM_ERR_UNSUPPORTED;
+    if (!qmm::gemm_supported(weight_view(w), gemm_act(x))) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }
 
@@ -427,7 +335,7 @@ int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stream)
     qmm::OutView yv[QMM_GEMM_BATCH_MAX];
     for (int i = 0; i < count; ++i) {           // every item on its own first
         const qmm_tensor *w = items[i].w, *x = items[i].x_bf16, *y = items[i].y_f32;
-        const int rc = check_gemm(w, x, y);
+        const int rc = check_gemm(w, x, y, false);
         if (rc) return rc;
         if (i > 0) {
             const qmm_tensor *w0 = items[0].w, *x0 = items[0].x_bf16;
@@ -452,9 +360,9 @@ int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stream)
 int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *x, qmm_tensor *h,
                     void *stream)
 {
-    int rc = check_gemm(w_gate, x, h);
+    int rc = check_gemm(w_gate, x, h, false);
     if (rc) return rc;
-    rc = check_gemm(w_up, x, h);
+    rc = check_gemm(w_up, x, h, false);
     if (rc) return rc;
     if (w_up->type != w_gate->type) return QMM_ERR_TYPE;
     if (w_up->ne[0] != w_gate->ne[0] || w_up->ne[1] != w_gate->ne[1]) return QMM_ERR_SHAPE;
@@ -468,10 +376,11 @@ int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_
 int qmm_gemm_ws(const qmm_tensor *w, const qmm_tensor *x, qmm_tensor *y, void *workspace,
                 size_t workspace_bytes, void *stream)
 {
-    const int rc = check_gemm(w, x, y);
+    const int rc = check_gemm(w, x, y, true);
     if (rc) return rc;
     if (w->ne[1] == 0 || x->ne[1] == 0) return QMM_OK;
-    if (!workspace) workspace_bytes = 0;
+    // MXFP4 activations use no workspace
+    if (!workspace || x->type == QMM_TYPE_MXFP4) workspace_bytes = 0;
     if (workspace_bytes) {
         if ((uintptr_t)workspace % 16 != 0) return QMM_ERR_LAYOUT;
         const uint64_t used = qmm::gemm_plan(w->ne[1], w->ne[0], x->ne[1], workspace_bytes).ws_bytes;
@@ -480,24 +389,23 @@ int qmm_gemm_ws(const qmm_tensor *w, const qmm_tensor *x, qmm_tensor *y, void *w
             range_overlaps(lo, lo + used, y))
             return QMM_ERR_ALIAS;
     }
-    qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
     qmm::OutView yv{static_cast<float *>(y->data), pitch_elems(y)};
-    return status_of(qmm::launch_gemm(weight_view(w), xv, yv, static_cast<float *>(workspace),
+    return status_of(qmm::launch_gemm(weight_view(w), gemm_act(x), yv, static_cast<float *>(workspace),
                                       workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int qmm_gemm_noalloc(const qmm_tensor *w, const qmm_tensor *x, qmm_tensor *y, size_t workspace_bytes,
                      void *stream)
 {
-    const int rc = check_gemm(w, x, y);
+    const int rc = check_gemm(w, x, y, true);
     if (rc) return rc;
     if (workspace_bytes > QMM_NOALLOC_SCRATCH_BYTES) return QMM_ERR_SCRATCH;
     if (w->ne[1] == 0 || x->ne[1] == 0) return QMM_OK;
+    if (x->type == QMM_TYPE_MXFP4) workspace_bytes = 0;
     void *ws = nullptr;
     if (workspace_bytes && qmm::static_scratch(&ws) != hipSuccess) return QMM_ERR_DEVICE;
-    qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
     qmm::OutView yv{static_cast<float *>(y->data), pitch_elems(y)};
-    return status_of(qmm::launch_gemm(weight_view(w), xv, yv, static_cast<float *>(ws), workspace_bytes,
+    return status_of(qmm::launch_gemm(weight_view(w), gemm_act(x), yv, static_cast<float *>(ws), workspace_bytes,
                                       static_cast<hipStream_t>(stream)));
 }
 

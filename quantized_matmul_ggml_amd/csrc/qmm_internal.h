@@ -11,10 +11,14 @@
 namespace qmm {
 
 // Weight encodings the kernels understand (same values as qmm_type).
-enum WType : int { W_F32 = 0, W_F16 = 1, W_BF16 = 2, W_Q8_0 = 3, W_Q4_0 = 4, W_Q8_B64 = 5, W_Q4_B64 = 6 };
+enum WType : int { W_F32 = 0, W_F16 = 1, W_BF16 = 2, W_Q8_0 = 3, W_Q4_0 = 4, W_Q8_B64 = 5, W_Q4_B64 = 6, W_MXFP4 = 7 };
+// Added to launch_quantize's type: the source rows are bf16 (MXFP4 only),
+// and src / src_pitch_elems count those 2-byte elements.
+constexpr int kSrcBf16 = 0x100;
 
 // Byte offset of the codes inside a quantized row: the fp16 scales come
 // first (K/32 of them, or K/64 with scale_shift 1), padded to 16 bytes.
+// MXFP4's K/32 one-byte scales fill the bytes of K/64 halves: scale_shift 1.
 __host__ __device__ inline int64_t quant_offset(int64_t K, int scale_shift = 0)
 {
     return ((K >> (4 + scale_shift)) + 15) / 16 * 16;
@@ -37,7 +41,7 @@ constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
 
 // One weight matrix as the kernels see it: M rows of K weights, row r at
 // base + r * pitch (bytes).  type is the code format (W_Q8_0, W_Q4_0 or
-// W_F16); the 64-block types arrive as their code format with scale_shift 1
+// W_F16) or W_MXFP4 (scale_shift 1); the 64-block types arrive as their code format with scale_shift 1
 // (one scale per two 32-weight runs: the scale of run c is scale c >> 1).
 struct WeightView {
     const uint8_t *base;
@@ -48,11 +52,13 @@ struct WeightView {
     int scale_shift = 0;
 };
 
-// Activations: N rows of K values, row n at data + n * pitch_elems elements.
+// Activations: N rows of K values, row n at data + n * pitch_elems elements
+// (bytes when type is W_MXFP4: packed rows, qmm_gemm only).
 struct ActView {
     const void *data;
     uint64_t pitch_elems;
     int64_t N;
+    int type = W_BF16;
 };
 
 // Output: N rows of M floats, row n at data + n * pitch_elems.
@@ -75,10 +81,11 @@ struct GemvConfig {
 bool gemv_config(int type, int64_t K, int64_t M, int64_t N, GemvConfig *cfg);
 // Whether the GEMV kernels can address the operands: loads span a few rows
 // with 32-bit buffer offsets, so the weight row pitch is bounded (2^28
-// bytes), and row counts and activation / output pitches are 32-bit.
+// bytes), and row counts and activation / output pitches are 32-bit.  The
+// MXFP4 kernel spans 16 rows with such offsets.
 inline bool gemv_supported(const WeightView &w, const ActView &x, const OutView &y)
 {
-    return w.pitch <= (1ull << 28) && w.M < (1ll << 31) && x.pitch_elems < (1ull << 31) &&
+    return w.pitch <= (w.type == W_MXFP4 ? 1ull << 26 : 1ull << 28) && w.M < (1ll << 31) && x.pitch_elems < (1ull << 31) &&
            y.pitch_elems < (1ull << 31);
 }
 
@@ -125,6 +132,32 @@ hipError_t launch_gemv_i8_swiglu(const WeightView &wg, const WeightView &wu, con
 // wg and wu share the type, K and M.
 hipError_t launch_gemv_swiglu(const WeightView &wg, const WeightView &wu, const ActView &x,
                               const OutView &h, hipStream_t stream);
+
+// The MXFP4 GEMV and its fused gate/up pair (gemv_mx.hip), 1 to 8 tokens.
+hipError_t launch_gemv_mx(const GemvTask *tasks, int count, hipStream_t stream);
+hipError_t launch_gemv_mx_swiglu(const WeightView &wg, const WeightView &wu, const ActView &x, const OutView &h,
+                                 hipStream_t stream);
+// The prefill GEMM of MXFP4 weights and MXFP4 activations on the scaled
+// matrix instructions (gemm_mx.hip).
+hipError_t launch_gemm_mx(const WeightView &w, const ActView &x, const OutView &y, hipStream_t stream);
+
+// The mixture-of-experts layer (moe.hip).  ExpertView: E matrices of one
+// type and shape, expert e's rows at w.base + e * expert_pitch.
+struct ExpertView {
+    WeightView w;
+    uint64_t expert_pitch;
+    int64_t E;
+};
+// The k largest of each token's E logits (E <= 1024) and their weights, of
+// all logits' softmax or renormalized over the chosen ones.
+hipError_t launch_moe_route(const float *logits, uint64_t pitch, int64_t N, int E, int k, bool all, int32_t *ids,
+                            float *weights, hipStream_t stream);
+// Workspace bytes of launch_moe_swiglu; shapes as checked by the caller
+// (N * k pairs of at most QMM_MOE_MAX_TOKENS * QMM_MOE_MAX_TOP_K).
+uint64_t moe_workspace(int64_t N, int64_t k, int64_t F);
+hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const ExpertView &down, const ActView &x,
+                             const int32_t *ids, const float *weights, int k, const OutView &y, void *ws,
+                             hipStream_t stream);
 
 // Which launches the matrix-core kernels take (measured on the decoder's
 // shapes, graph-replayed): from 5 tokens every one; at 3 and 4 tokens those

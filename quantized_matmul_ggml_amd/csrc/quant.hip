@@ -153,6 +153,128 @@ __global__ __launch_bounds__(256) void f16_to_f32_kernel(const uint8_t *__restri
     }
 }
 
+// MXFP4 (microscaled e2m1 values: 32 weights share one power-of-two scale).
+// Scale 2^e with e = floor(log2 amax) - 2, so that amax lands in [4, 8), where
+// e2m1's largest value 6 is; stored as the byte e + 127, e at least -127.  The
+// codes are w / 2^e rounded to e2m1 (nearest even, above 6 to 6, the sign of
+// w kept): v_cvt_scalef32_pk_fp4_f32 divides by the scale and rounds two
+// values at once.  A block holding an infinity or a NaN stores the scale byte
+// 255 (not a number) and zero codes.
+//
+// Bound by memory (4 or 2 bytes read per weight, 17/32 written).  Four lanes
+// share a block, eight neighbouring weights each, so a wave's loads are
+// contiguous; amax comes by two DPP exchanges within the four.  Byte j holds
+// codes j and j + 16, so lane pairs (0, 2) and (1, 3) exchange their packed
+// nibbles and lanes 0 and 1 store 8 code bytes each.
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const void *__restrict__ src, uint64_t src_pitch,
+                                                             int64_t K, int64_t M, uint8_t *__restrict__ dst,
+                                                             uint64_t dst_pitch)
+{
+    const int64_t nblk = K / 32;
+    const int64_t total = M * nblk * 4;
+    const int64_t qoff = quant_offset(K, 1);
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    // total and step are multiples of 4: a block's four lanes stay together
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        const int64_t bi = i >> 2;
+        const int part = (int)(i & 3);
+        const int64_t r = bi / nblk;
+        const int64_t b = bi - r * nblk;
+        float v[8];
+        if constexpr (BF16) {
+            const uint4 h = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + r * src_pitch + b * 32 + 8 * part);
+            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+                v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+            }
+        } else {
+            const float *w = static_cast<const float *>(src) + r * src_pitch + b * 32 + 8 * part;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = w[j];
+        }
+        // the largest magnitude as bits: an infinity or NaN compares above
+        // every finite value
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t m = __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu;
+            amax = m > amax ? m : amax;
+        }
+        // quad_perm [1, 0, 3, 2], then [2, 3, 0, 1]
+        uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, true);
+        amax = o > amax ? o : amax;
+        o = (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, true);
+        amax = o > amax ? o : amax;
+        // the exponent field of amax is floor(log2 amax) + 127 (0 below 2^-126,
+        // where e would be under -127 anyway)
+        const uint32_t field = amax >> 23;
+        const bool bad = field == 255u;
+        const uint32_t se = field > 2u ? field - 2u : 0u;
+        const float scale = __builtin_bit_cast(float, se << 23);
+        uint32_t code = 0;
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[0], v[1], scale, 0);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[2], v[3], scale, 1);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[4], v[5], scale, 2);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[6], v[7], scale, 3);
+        code = bad ? 0u : code;
+        // nibble j of `code` is code 8 part + j; lanes 0, 1 take the matching
+        // nibbles of lanes 2, 3 (codes 16 further) as high nibbles
+        const uint32_t high = (uint32_t)__builtin_amdgcn_mov_dpp((int)code, 0x4E, 0xF, 0xF, true);
+        uint8_t *row = dst + r * dst_pitch;
+        if (part < 2) {
+            auto spread = [](uint32_t n) {          // nibbles 0..3 to the low halves of four bytes
+                n = (n | (n << 8)) & 0x00FF00FFu;
+                return (n | (n << 4)) & 0x0F0F0F0Fu;
+            };
+            const uint32_t w0 = spread(code & 0xFFFFu) | (spread(high & 0xFFFFu) << 4);
+            const uint32_t w1 = spread(code >> 16) | (spread(high >> 16) << 4);
+            *reinterpret_cast<uint2 *>(row + qoff + 16 * b + 8 * part) = make_uint2(w0, w1);
+        }
+        if (part == 0) row[b] = (uint8_t)(bad ? 255u : se);
+        if (b == 0 && part == 3)
+            for (int64_t p = nblk; p < qoff; ++p) row[p] = 0;
+    }
+}
+
+// W' = 2^e * value: two values of a byte per conversion, exact (a scale byte
+// of 255 gives NaN).  Four lanes per block, as above: lane `part` expands the
+// four code bytes 4 part .. 4 part + 3 into two runs of four floats.
+__global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(const uint8_t *__restrict__ src, uint64_t src_pitch,
+                                                               int64_t K, int64_t M, float *__restrict__ dst,
+                                                               uint64_t dst_pitch)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const int64_t nblk = K / 32;
+    const int64_t total = M * nblk * 4;
+    const int64_t qoff = quant_offset(K, 1);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t bi = i >> 2;
+        const int part = (int)(i & 3);
+        const int64_t r = bi / nblk;
+        const int64_t b = bi - r * nblk;
+        const uint8_t *row = src + r * src_pitch;
+        const float scale = __builtin_bit_cast(float, (uint32_t)row[b] << 23);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(row + qoff + 16 * b + 4 * part);
+        const f32x2 a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
+        const f32x2 a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
+        const f32x2 a2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
+        const f32x2 a3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+        float *out = dst + r * dst_pitch + b * 32 + 4 * part;
+        out[0] = a0.x;
+        out[1] = a1.x;
+        out[2] = a2.x;
+        out[3] = a3.x;
+        out[16] = a0.y;
+        out[17] = a1.y;
+        out[18] = a2.y;
+        out[19] = a3.y;
+    }
+}
+
 unsigned grid_for(int64_t items)
 {
     const int64_t blocks = (items + 255) / 256;
@@ -165,6 +287,17 @@ hipError_t launch_quantize(const float *src, uint64_t src_pitch_elems, int64_t K
                            uint8_t *dst, uint64_t dst_pitch, int type, hipStream_t stream,
                            bool q4_amax7, int scale_shift)
 {
+    if ((type & ~kSrcBf16) == W_MXFP4) {
+        const int64_t lanes = M * (K / 32) * 4;
+        if (lanes == 0) return hipSuccess;
+        if (type & kSrcBf16)
+            hipLaunchKernelGGL(quantize_mxfp4_kernel<true>, dim3(grid_for(lanes)), dim3(256), 0, stream,
+                               (const void *)src, src_pitch_elems, K, M, dst, dst_pitch);
+        else
+            hipLaunchKernelGGL(quantize_mxfp4_kernel<false>, dim3(grid_for(lanes)), dim3(256), 0, stream,
+                               (const void *)src, src_pitch_elems, K, M, dst, dst_pitch);
+        return hipGetLastError();
+    }
     const int64_t items = M * (K / (scale_shift ? 64 : 32));
     if (items == 0) return hipSuccess;
     const dim3 grid(grid_for(items)), block(256);
@@ -190,6 +323,13 @@ hipError_t launch_dequantize(const uint8_t *src, uint64_t src_pitch, int64_t K, 
     if (type == W_F16) {
         if (M * K == 0) return hipSuccess;
         hipLaunchKernelGGL(f16_to_f32_kernel, dim3(grid_for(M * K)), dim3(256), 0, stream,
+                           src, src_pitch, K, M, dst, dst_pitch_elems);
+        return hipGetLastError();
+    }
+    if (type == W_MXFP4) {
+        const int64_t lanes = M * (K / 32) * 4;
+        if (lanes == 0) return hipSuccess;
+        hipLaunchKernelGGL(dequantize_mxfp4_kernel, dim3(grid_for(lanes)), dim3(256), 0, stream,
                            src, src_pitch, K, M, dst, dst_pitch_elems);
         return hipGetLastError();
     }

@@ -1,0 +1,323 @@
+// row_tiles.h -- device parts shared by the kernels that stream packed weight
+// rows through the bf16 matrix cores against exactly represented binary32
+// activations: the MXFP4 GEMV (gemv_mx.hip) and the mixture-of-experts layer
+// (moe.hip).  Internal to the library.
+//
+// One matrix instruction, v_mfma_f32_16x16x32_bf16 (D 16 x 16 += A 16 x 32 *
+// B 32 x 16), takes 32 values of k of 16 weight rows (B) and of up to four
+// tokens (A).  The arithmetic is exact up to the binary32 accumulation:
+//
+//  * A, activations.  A binary32 value is cut into three bf16 parts of eight
+//    significant bits each, x = hi + mid + lo exactly (the top 16 bits, the
+//    top 16 bits of what is left, the rest); matrix row 4 t + p carries part p
+//    of token t (p = 3 is not used: such rows repeat part 2 and their sums
+//    are never read).  Products of two 8-bit significands are exact.
+//  * B, weights.  Row j of a tile is matrix column j.  A lane loads 16 bytes
+//    of its row, so the four lane groups g = lane / 16 cover one 64-byte
+//    unit of the row (four 32-blocks of 4-bit codes, or two of 8-bit ones)
+//    with one 128-bit load, and the unit is used up by four (or two) matrix
+//    instructions:
+//     - MXFP4: instruction i takes dword i of every lane: eight values of block
+//       4 u + g from lane group g.  Scale and value convert to bf16 together,
+//       exactly (v_cvt_scalef32_pk_bf16_fp4), so sums run through whole rows.
+//     - Q4_0, Q8_0: two cross-lane swaps regroup the dwords so that one
+//       instruction sees one block; the signed codes enter as exact bf16
+//       integers and the block's fp16 scale multiplies its sum in binary32.
+//  * D: lane (j, g) receives the three partial sums of row j and token g.
+//
+// What bounds these kernels is the weight stream; the activations' parts sit
+// in LDS in the order the matrix instructions read them (192 bytes per token
+// and 32-block), or come from memory in the same order.
+#pragma once
+
+#include "qmm_internal.h"
+
+namespace qmm {
+
+typedef __bf16 rt_bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 rt_bf16x2 __attribute__((ext_vector_type(2)));
+typedef float rt_f32x4 __attribute__((ext_vector_type(4)));
+typedef float rt_f32x2 __attribute__((ext_vector_type(2)));
+// four floats at any 4-byte aligned address
+typedef float rt_f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr int kTileCols = 16;          // weight rows per tile
+constexpr int kImageBytes = 192;       // activation parts of one token and 32-block
+
+// A row format: MF matrix instructions (32-blocks) per 64-byte unit and SPU
+// scale bytes per unit.
+template <int WT, int SS>
+struct RowFmt {
+    static constexpr int MF = WT == W_Q8_0 ? 2 : 4;
+    static constexpr int KPU = 32 * MF;
+    static constexpr int BB = 64 / MF;                   // code bytes of a block
+    static constexpr int SPU = WT == W_MXFP4 ? 4 : (2 * MF) >> SS;
+};
+
+// Where the activation parts of (block, quarter) lie, in units of 64-byte
+// (part, group) rows times the token count: the quarter q of a block is the
+// eight values one lane group feeds to one matrix instruction.  MXFP4: lane
+// group = block within the unit, instruction = quarter; otherwise the other
+// way round.
+template <int WT>
+__device__ inline int image_step(int block, int q)
+{
+    return WT == W_MXFP4 ? (block & ~3) + q : block;
+}
+template <int WT>
+__device__ inline int image_group(int block, int q)
+{
+    return WT == W_MXFP4 ? block & 3 : q;
+}
+// First elements (within the block) of the two runs of four that make up
+// quarter q, and whether the runs interleave (4-bit codes: byte s holds
+// elements 4 q + s and 16 + 4 q + s, values in that order; 8-bit codes: the
+// swap leaves codes 0.., 16.., 8.., 24.. in lane groups 0..3).
+template <int WT>
+__device__ inline int run0(int q)
+{
+    return WT == W_Q8_0 ? (q == 0 ? 0 : q == 1 ? 16 : q == 2 ? 8 : 24) : 4 * q;
+}
+template <int WT>
+__device__ inline int run1(int q)
+{
+    return WT == W_Q8_0 ? run0<WT>(q) + 4 : 16 + 4 * q;
+}
+
+// The exact three-way split of eight values (in matrix order) into bf16
+// parts.  An infinity keeps its value in the first part (the others zero), a
+// NaN stays one.
+__device__ inline void split_parts(const float (&v)[8], uint4 (&part)[3])
+{
+    uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v[i]);
+        const bool special = (u & 0x7F800000u) == 0x7F800000u;
+        const uint32_t h = (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : u & 0xFFFF0000u;
+        float r = v[i] - __builtin_bit_cast(float, u & 0xFFFF0000u);
+        r = special ? 0.0f : r;
+        const uint32_t m = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
+        hi[i] = h;
+        mid[i] = m;
+        lo[i] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, m));
+    }
+    // the upper halves of two dwords side by side
+    auto pk = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
+    part[0] = make_uint4(pk(hi[0], hi[1]), pk(hi[2], hi[3]), pk(hi[4], hi[5]), pk(hi[6], hi[7]));
+    part[1] = make_uint4(pk(mid[0], mid[1]), pk(mid[2], mid[3]), pk(mid[4], mid[5]), pk(mid[6], mid[7]));
+    part[2] = make_uint4(pk(lo[0], lo[1]), pk(lo[2], lo[3]), pk(lo[4], lo[5]), pk(lo[6], lo[7]));
+}
+
+// The two runs of four in matrix order.
+template <int WT>
+__device__ inline void matrix_order(const rt_f32x4 a, const rt_f32x4 b, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (WT == W_Q8_0) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        } else {
+            v[2 * i] = a[i];
+            v[2 * i + 1] = b[i];
+        }
+    }
+}
+
+// Fills the LDS image of blocks [b0, b0 + nblk) of `ntok` tokens with all
+// `threads` threads; blocks from nb on are zeros.  row(t) is token t's row.
+template <int WT, class Row>
+__device__ inline void build_image(uint8_t *img, int ntok, int b0, int nblk, int nb, int threads, Row row)
+{
+    const int per_tok = 4 * nblk;
+    for (int t = 0; t < ntok; ++t) {
+        const float *x = row(t);
+        for (int i = threadIdx.x; i < per_tok; i += threads) {
+            const int b = i >> 2, q = i & 3;
+            rt_f32x4 r0 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
+            if (b0 + b < nb) {
+                const float *p = x + (int64_t)(b0 + b) * 32;
+                r0 = *reinterpret_cast<const rt_f32x4u *>(p + run0<WT>(q));
+                r1 = *reinterpret_cast<const rt_f32x4u *>(p + run1<WT>(q));
+            }
+            float v[8];
+            matrix_order<WT>(r0, r1, v);
+            uint4 part[3];
+            split_parts(v, part);
+            uint8_t *dst = img + (image_step<WT>(b, q) * ntok + t) * kImageBytes + 16 * image_group<WT>(b, q);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(dst + 64 * p) = part[p];
+        }
+    }
+}
+
+// QU units of a tile's rows in registers: codes, and the scales of the
+// lane's row.
+template <int WT, int SS, int QU>
+struct Quantum {
+    static constexpr int SB = QU * RowFmt<WT, SS>::SPU;
+    uint4 q[QU];
+    uint32_t s[(SB + 3) / 4];
+};
+
+// Swap helpers: rows of 32 (or 16) lanes of two registers exchanged so that
+// a keeps the lower ones of both and b the upper ones.
+__device__ inline void rt_swap32(uint32_t &a, uint32_t &b)
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = p[0];
+    b = p[1];
+}
+__device__ inline void rt_swap16(uint32_t &a, uint32_t &b)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = p[0];
+    b = p[1];
+}
+
+typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
+
+// Loads quantum qi of the packed row at `row` (this lane's).  Every address
+// lies inside the row: code units past its end repeat its first bytes (their
+// activations are zeros and multiply_quantum zeroes their scales), and the
+// scale bytes of a quantum end at or before the row's end, because the row's
+// codes follow its scales.  The weights stream past the caches (kStreamLoad's
+// policy); the scales share cache lines with neighbouring quanta.
+template <int WT, int SS, int QU>
+__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int g)
+{
+    constexpr int SB = Quantum<WT, SS, QU>::SB;
+    const int c0 = 64 * QU * qi + 16 * g;
+    const uint8_t *codes = row + qoff;
+    auto load16 = [](const uint8_t *p) {
+        return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4 *>(p)));
+    };
+    if (64 * QU * (qi + 1) <= code_bytes) {                // uniform
+#pragma unroll
+        for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + c0 + 64 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + (c0 + 64 * i < code_bytes ? c0 + 64 * i : 0));
+    }
+    const uint8_t *s = row + SB * qi;
+    if constexpr (SB == 2) {
+        z.s[0] = *reinterpret_cast<const uint16_t *>(s);
+    } else if constexpr (SB == 4) {
+        z.s[0] = *reinterpret_cast<const uint32_t *>(s);
+    } else if constexpr (SB == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(s);
+        z.s[0] = v.x;
+        z.s[1] = v.y;
+    } else {
+        static_assert(SB % 16 == 0, "scale bytes of a quantum");
+#pragma unroll
+        for (int i = 0; i < SB / 16; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(s + 16 * i);
+            z.s[4 * i] = v.x;
+            z.s[4 * i + 1] = v.y;
+            z.s[4 * i + 2] = v.z;
+            z.s[4 * i + 3] = v.w;
+        }
+    }
+}
+
+// The sum of a lane's row and token over the instructions so far.  MXFP4 keeps
+// the matrix instruction's own accumulator (one per part, added at the end).
+template <int WT> struct RowAcc { rt_f32x4 c = {0, 0, 0, 0}; };
+template <int WT>
+__device__ inline float row_total(const RowAcc<WT> &a)
+{
+    return WT == W_MXFP4 ? a.c[0] + a.c[1] + a.c[2] : a.c[0];
+}
+
+// Byte E of w as a signed int8, converted to float (one SDWA conversion).
+template <int E>
+__device__ inline float rt_sbyte(uint32_t w) { return (float)(int8_t)(w >> (8 * E)); }
+__device__ inline uint32_t rt_pack(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(rt_f32x2{a, b}, rt_bf16x2));
+}
+
+// Multiplies quantum qi (in z) with the activation fragments frag(tg, step),
+// step = instruction index from the quantum's first one, for the token groups
+// tg < groups.  nb: blocks of the row (only the quantum that passes it masks
+// its scales).
+template <int WT, int SS, int QU, int TG, class Frag>
+__device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, int nb, int g, int groups,
+                                        RowAcc<WT> (&acc)[TG], Frag frag)
+{
+    using F = RowFmt<WT, SS>;
+    const int blk0 = qi * QU * F::MF;
+    const bool tail = blk0 + QU * F::MF > nb;              // uniform
+#pragma unroll
+    for (int i = 0; i < QU; ++i) {
+        uint32_t d[4] = {z.q[i].x, z.q[i].y, z.q[i].z, z.q[i].w};
+        if constexpr (WT == W_MXFP4) {
+            // lane group g holds block blk0 + 4 i + g: its scale byte as the
+            // exponent of a float (255 is NaN, 0 is 2^-127)
+            uint32_t e = (z.s[i] >> (8 * g)) & 0xFFu;
+            if (tail) e = blk0 + 4 * i + g < nb ? e : 0u;
+            const float f = __builtin_bit_cast(float, e << 23);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint4 bw = make_uint4(
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 3)));
+                const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
+#pragma unroll
+                for (int tg = 0; tg < TG; ++tg)
+                    if (tg < groups)
+                        acc[tg].c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 4 * i + t), b, acc[tg].c, 0, 0, 0);
+            }
+        } else {
+            rt_swap32(d[0], d[2]);
+            rt_swap32(d[1], d[3]);
+            if constexpr (WT == W_Q4_0) {
+                rt_swap16(d[0], d[1]);
+                rt_swap16(d[2], d[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < F::MF; ++t) {
+                uint4 bw;
+                if constexpr (WT == W_Q4_0) {
+                    // a nibble n at the top of a byte with its top bit flipped
+                    // is the int8 value 16 (n - 8); the scale absorbs the 16
+                    const uint32_t x = d[t] ^ 0x88888888u;
+                    const uint32_t lo = (x << 4) & 0xF0F0F0F0u, hi = x & 0xF0F0F0F0u;
+                    bw = make_uint4(rt_pack(rt_sbyte<0>(lo), rt_sbyte<0>(hi)), rt_pack(rt_sbyte<1>(lo), rt_sbyte<1>(hi)),
+                                    rt_pack(rt_sbyte<2>(lo), rt_sbyte<2>(hi)), rt_pack(rt_sbyte<3>(lo), rt_sbyte<3>(hi)));
+                } else {
+                    const uint32_t a = d[2 * t], c = d[2 * t + 1];
+                    bw = make_uint4(rt_pack(rt_sbyte<0>(a), rt_sbyte<1>(a)), rt_pack(rt_sbyte<2>(a), rt_sbyte<3>(a)),
+                                    rt_pack(rt_sbyte<0>(c), rt_sbyte<1>(c)), rt_pack(rt_sbyte<2>(c), rt_sbyte<3>(c)));
+                }
+                const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
+                const int blk = i * F::MF + t;                 // static
+                const int h = blk >> SS;                       // scale (half) index within the quantum
+                const uint32_t sb = (h & 1) ? z.s[h / 2] >> 16 : z.s[h / 2] & 0xFFFFu;
+                float f = (float)__builtin_bit_cast(_Float16, (uint16_t)sb);
+                if constexpr (WT == W_Q4_0) f *= 0.0625f;
+                if (tail) f = blk0 + blk < nb ? f : 0.0f;
+#pragma unroll
+                for (int tg = 0; tg < TG; ++tg)
+                    if (tg < groups) {
+                        const rt_f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, F::MF * i + t), b,
+                                                                                   rt_f32x4{0, 0, 0, 0}, 0, 0, 0);
+                        acc[tg].c[0] = fmaf(f, s[0] + (s[1] + s[2]), acc[tg].c[0]);
+                    }
+            }
+        }
+    }
+}
+
+// Swish(z) = z * sigma(z) = z / (1 + e^{-z}) in binary32; for z far below
+// zero e^{-z} overflows and the quotient is the limit -0.
+__device__ inline float rt_swish(float z)
+{
+    return z / (1.0f + expf(-z));
+}
+
+}  // namespace qmm
