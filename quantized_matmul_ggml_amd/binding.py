@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -42,6 +43,12 @@ class QmmTensor(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int32), ("n_dims", ctypes.c_int32),
                 ("ne", ctypes.c_int64 * 4), ("nb", ctypes.c_uint64 * 4),
                 ("data", ctypes.c_void_p)]
+
+
+_PACK = struct.Struct("=ii4q4QQ").pack      # the fields of QmmTensor
+_ELEM = {F32: 4, F16: 2, BF16: 2}
+_U64 = (1 << 64) - 1
+assert struct.calcsize("=ii4q4QQ") == ctypes.sizeof(QmmTensor)
 
 
 class QmmGemvItem(ctypes.Structure):
@@ -137,16 +144,11 @@ def row_size(type_: int, K: int) -> int:
 def make_desc(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int, n_dims: int = 2,
               nb0: int | None = None) -> QmmTensor:
     """A raw descriptor (used directly by the boundary tests)."""
-    t = QmmTensor()
-    t.type = type_
-    t.n_dims = n_dims
-    t.ne[0], t.ne[1], t.ne[2], t.ne[3] = ne0, ne1, 1, 1
     if nb0 is None:
-        nb0 = {F32: 4, F16: 2, BF16: 2}.get(type_, 0)
-    t.nb[0], t.nb[1] = nb0, nb1
-    t.nb[2] = t.nb[3] = nb1 * max(ne1, 1)
-    t.data = data_ptr
-    return t
+        nb0 = _ELEM.get(type_, 0)
+    nb2 = nb1 * (ne1 if ne1 > 1 else 1) & _U64
+    # one packed copy: filling the fields one by one costs several microseconds
+    return QmmTensor.from_buffer_copy(_PACK(type_, n_dims, ne0, ne1, 1, 1, nb0 & _U64, nb1 & _U64, nb2, nb2, data_ptr or 0))
 
 
 @dataclass
@@ -183,16 +185,26 @@ def _dense_desc(t: torch.Tensor, type_: int) -> QmmTensor:
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     es = t.element_size()
-    if t.numel() == 0:                  # empty: strides are meaningless
-        return make_desc(type_, t.shape[1], t.shape[0], t.shape[1] * es, t.data_ptr())
-    if t.stride(1) != 1:
+    rows, cols = t.shape
+    if rows == 0 or cols == 0:          # empty: strides are meaningless
+        return make_desc(type_, cols, rows, cols * es, t.data_ptr())
+    pitch, step = t.stride()
+    if step != 1:
         raise ValueError("rows must be contiguous (stride 1 along the last dimension)")
-    return make_desc(type_, t.shape[1], t.shape[0], t.stride(0) * es, t.data_ptr())
+    return make_desc(type_, cols, rows, pitch * es, t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+# The current stream's handle without building a Stream object (2.8 us less per
+# call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(status: int, where: str):
@@ -218,7 +230,7 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
         out[:, rs:].zero_()
     wt = Weight(out, type_, K, M)
     src, dst = _dense_desc(w, BF16 if w.dtype == torch.bfloat16 else F32), wt.desc()
-    _check(lib().qmm_quantize_rule(ctypes.byref(src), ctypes.byref(dst), rule, _stream(stream)),
+    _check(lib().qmm_quantize_rule(src, dst, rule, _stream(stream)),
            "qmm_quantize_rule")
     return wt
 
@@ -229,7 +241,7 @@ def dequantize(w: Weight, *, out: torch.Tensor | None = None, stream=None) -> to
     if out is None:
         out = torch.empty((w.M, w.K), dtype=torch.float32, device=w.data.device)
     src, dst = w.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_dequantize(ctypes.byref(src), ctypes.byref(dst), _stream(stream)),
+    _check(lib().qmm_dequantize(src, dst, _stream(stream)),
            "qmm_dequantize")
     return out
 
@@ -254,7 +266,7 @@ def gemv(w: Weight, x, *, out: torch.Tensor | None = None, stream=None) -> torch
     if out is None:
         out = torch.empty((n, w.M), dtype=torch.float32, device=dev)
     wd, yd = w.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_gemv(ctypes.byref(wd), ctypes.byref(xd), ctypes.byref(yd), _stream(stream)),
+    _check(lib().qmm_gemv(wd, xd, yd, _stream(stream)),
            "qmm_gemv")
     return out
 
@@ -296,7 +308,7 @@ def gemv_swiglu(w_gate: Weight, w_up: Weight, x, *, out: torch.Tensor | None = N
     if out is None:
         out = torch.empty((n, w_gate.M), dtype=torch.float32, device=dev)
     gd, ud, hd = w_gate.desc(), w_up.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_gemv_swiglu(ctypes.byref(gd), ctypes.byref(ud), ctypes.byref(xd), ctypes.byref(hd),
+    _check(lib().qmm_gemv_swiglu(gd, ud, xd, hd,
                                  _stream(stream)), "qmm_gemv_swiglu")
     return out
 
@@ -315,7 +327,7 @@ def records_to_rows(records: torch.Tensor, type_: int, K: int, M: int, *, pitch:
     out = torch.zeros((M, pitch), dtype=torch.uint8, device=records.device)
     wt = Weight(out, type_, K, M)
     d = wt.desc()
-    _check(lib().qmm_records_to_rows(ctypes.c_void_p(records.data_ptr()), ctypes.byref(d), _stream(stream)),
+    _check(lib().qmm_records_to_rows(records.data_ptr(), d, _stream(stream)),
            "qmm_records_to_rows")
     return wt
 
@@ -327,7 +339,7 @@ def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) 
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=w.data.device)
     d = w.desc()
-    _check(lib().qmm_rows_to_records(ctypes.byref(d), ctypes.c_void_p(out.data_ptr()), _stream(stream)),
+    _check(lib().qmm_rows_to_records(d, out.data_ptr(), _stream(stream)),
            "qmm_rows_to_records")
     return out
 
@@ -335,7 +347,7 @@ def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) 
 def gemm_workspace_size(w: Weight, x: torch.Tensor) -> int:
     """Bytes of workspace qmm_gemm_ws uses to split K for these shapes (0: no split)."""
     wd, xd = w.desc(), _dense_desc(x, BF16)
-    return int(lib().qmm_gemm_workspace_size(ctypes.byref(wd), ctypes.byref(xd)))
+    return int(lib().qmm_gemm_workspace_size(wd, xd))
 
 
 def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
@@ -358,19 +370,19 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
-        n = int(lib().qmm_gemm_workspace_size(ctypes.byref(wd), ctypes.byref(xd)))
+        n = int(lib().qmm_gemm_workspace_size(wd, xd))
         workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         if workspace is not None and stream is not None:
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
             workspace.record_stream(stream)
     if workspace is None:
-        _check(lib().qmm_gemm(ctypes.byref(wd), ctypes.byref(xd), ctypes.byref(yd), _stream(stream)),
+        _check(lib().qmm_gemm(wd, xd, yd, _stream(stream)),
                "qmm_gemm")
     else:
         _need_gpu(workspace)
-        _check(lib().qmm_gemm_ws(ctypes.byref(wd), ctypes.byref(xd), ctypes.byref(yd),
-                                 ctypes.c_void_p(workspace.data_ptr()),
+        _check(lib().qmm_gemm_ws(wd, xd, yd,
+                                 workspace.data_ptr(),
                                  workspace.numel() * workspace.element_size(), _stream(stream)),
                "qmm_gemm_ws")
     return out
@@ -384,8 +396,8 @@ def gemm_noalloc(w: Weight, x: torch.Tensor, out: torch.Tensor, *, workspace_byt
     _need_gpu(w.data, x, out)
     wd, xd, yd = w.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
     if workspace_bytes is None:
-        workspace_bytes = int(lib().qmm_gemm_workspace_size(ctypes.byref(wd), ctypes.byref(xd)))
-    _check(lib().qmm_gemm_noalloc(ctypes.byref(wd), ctypes.byref(xd), ctypes.byref(yd),
+        workspace_bytes = int(lib().qmm_gemm_workspace_size(wd, xd))
+    _check(lib().qmm_gemm_noalloc(wd, xd, yd,
                                   ctypes.c_size_t(workspace_bytes), _stream(stream)), "qmm_gemm_noalloc")
     return out
 
@@ -397,7 +409,7 @@ def gemm_swiglu(w_gate: Weight, w_up: Weight, x: torch.Tensor, *, out: torch.Ten
     if out is None:
         out = torch.empty((x.shape[0], w_gate.M), dtype=torch.float32, device=x.device)
     gd, ud, xd, hd = w_gate.desc(), w_up.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
-    _check(lib().qmm_gemm_swiglu(ctypes.byref(gd), ctypes.byref(ud), ctypes.byref(xd), ctypes.byref(hd),
+    _check(lib().qmm_gemm_swiglu(gd, ud, xd, hd,
                                  _stream(stream)), "qmm_gemm_swiglu")
     return out
 
@@ -458,15 +470,15 @@ def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, str
     ids = torch.empty((n, top_k), dtype=torch.int32, device=logits.device)
     weights = torch.empty((n, top_k), dtype=torch.float32, device=logits.device)
     ld = _dense_desc(logits, F32)
-    _check(lib().qmm_moe_route(ctypes.byref(ld), top_k, rule, ctypes.c_void_p(ids.data_ptr()),
-                               ctypes.c_void_p(weights.data_ptr()), _stream(stream)), "qmm_moe_route")
+    _check(lib().qmm_moe_route(ld, top_k, rule, ids.data_ptr(),
+                               weights.data_ptr(), _stream(stream)), "qmm_moe_route")
     return ids, weights
 
 
 def moe_workspace_size(w_gate: Experts, x: torch.Tensor, top_k: int) -> int:
     """Bytes of workspace qmm_moe_swiglu needs for these shapes."""
     gd, xd = w_gate.desc(), _dense_desc(x, F32)
-    return int(lib().qmm_moe_workspace_size(ctypes.byref(gd), ctypes.byref(xd), top_k))
+    return int(lib().qmm_moe_workspace_size(gd, xd, top_k))
 
 
 def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor, ids: torch.Tensor,
@@ -486,16 +498,16 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
         out = torch.empty((x.shape[0], w_down.M), dtype=torch.float32, device=x.device)
     gd, ud, dd, xd, yd = w_gate.desc(), w_up.desc(), w_down.desc(), _dense_desc(x, F32), _dense_desc(out, F32)
     if workspace is None:
-        n = int(lib().qmm_moe_workspace_size(ctypes.byref(gd), ctypes.byref(xd), top_k))
+        n = int(lib().qmm_moe_workspace_size(gd, xd, top_k))
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
         if stream is not None:
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
             workspace.record_stream(stream)
     _need_gpu(workspace)
-    _check(lib().qmm_moe_swiglu(ctypes.byref(gd), ctypes.byref(ud), ctypes.byref(dd), ctypes.byref(xd),
-                                ctypes.c_void_p(ids.data_ptr()), ctypes.c_void_p(weights.data_ptr()), top_k,
-                                ctypes.byref(yd), ctypes.c_void_p(workspace.data_ptr()),
+    _check(lib().qmm_moe_swiglu(gd, ud, dd, xd,
+                                ids.data_ptr(), weights.data_ptr(), top_k,
+                                yd, workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream(stream)), "qmm_moe_swiglu")
     return out
 

@@ -27,9 +27,8 @@
 namespace qmm {
 namespace {
 
-constexpr int kWaves = 16;
+constexpr int kWaves = 16;            // of moe_down_kernel's workgroups
 constexpr int kThreads = 64 * kWaves;
-constexpr int kImageMax = 96 * 1024;
 constexpr int kPairs = QMM_MOE_MAX_TOKENS * QMM_MOE_MAX_TOP_K;
 static_assert(kPairs == 128, "two pairs per lane of a wave");
 
@@ -125,18 +124,20 @@ struct MoeArgs {
     uint8_t *h;               // workspace: h_pair bytes per pair
     uint64_t h_pair;          // kImageBytes per 32-block of F, whole groups of four blocks
     int32_t E, N, k, F, M;    // M: output rows
-    int32_t nb1, qoff1, nq1;  // gate / up rows: blocks, code offset, quanta
-    int32_t nb2, qoff2, nq2;  // down rows
-    int32_t s_log2, pass_q;   // moe_up_kernel: waves per tile, quanta per pass
+    int32_t nb1, qoff1;       // gate / up rows: blocks, code offset
+    int32_t nb2, qoff2;       // down rows
+    int32_t steps1;           // moe_up_kernel: quanta per row, waves per tile,
+    int32_t s_log2;           //   LDS bytes of the image
+    int32_t image;
+    int32_t steps2;           // moe_down_kernel: quanta (or pairs) per row
 };
 
 template <int WT, int SS, int QU, int TG>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeArgs a)
+__global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
     constexpr int QB = QU * F::MF;
-    extern __shared__ __attribute__((aligned(16))) uint8_t img[];
-    __shared__ float red[kWaves][TG][64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ float pair_weight[kPairs];
     __shared__ float psum[8];
     __shared__ int slot_tok[8], slot_pair[8];
@@ -154,18 +155,22 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeArgs a)
     if (leader != pair) return;
 
     const int j = lane & 15, g = lane >> 4;
-    const int S = 1 << a.s_log2, T = kWaves >> a.s_log2;
+    const int threads = blockDim.x, waves = threads >> 6;
+    const int S = 1 << a.s_log2, T = waves >> a.s_log2;
     const int split = wave & (S - 1), tile_in = wave >> a.s_log2;
     const int grp = blockIdx.x;
+    float *const red = reinterpret_cast<float *>(lds);     // [waves][TG][64]
+    uint8_t *const img = lds + waves * TG * 64 * 4;
 
     // the first quantum is in flight while the tokens are set up
-    const bool second = j >= 8;
-    const uint8_t *const W = second ? a.up + (uint64_t)e * a.up_expert : a.gate + (uint64_t)e * a.gate_expert;
+    const bool upper = j >= 8;
+    const uint8_t *const W = upper ? a.up + (uint64_t)e * a.up_expert : a.gate + (uint64_t)e * a.gate_expert;
     const int r = (grp * T + tile_in) * 8 + (j & 7);
-    const uint8_t *const row = W + (uint64_t)(r < a.F ? r : a.F - 1) * (second ? a.up_pitch : a.gate_pitch);
+    const uint8_t *const row = W + (uint64_t)(r < a.F ? r : a.F - 1) * (upper ? a.up_pitch : a.gate_pitch);
     const int code_bytes = F::BB * a.nb1;
     Quantum<WT, SS, QU> cur, nxt;
-    if (split < a.nq1) load_quantum<WT, SS, QU>(cur, row, a.qoff1, code_bytes, split, g);
+    auto whole = [&](int q) { return (q + 1) * QB <= a.nb1; };
+    if (split < a.steps1) load_quantum<WT, SS, QU>(cur, row, a.qoff1, code_bytes, split, g, whole(split));
 
     // ---- the tokens: bit t of `toks`; thread t adds up the weights of token
     // t's slots in slot order (a token may name an expert twice) ----
@@ -208,35 +213,37 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeArgs a)
     const uint32_t step_bytes = (uint32_t)cnt * kImageBytes;
     const int groups = __builtin_amdgcn_readfirstlane(cnt > 4 ? 2 : 1);
 
-    RowAcc<WT> acc[TG];
-    for (int q0 = 0; q0 < a.nq1; q0 += a.pass_q) {
-        const int q1 = q0 + a.pass_q < a.nq1 ? q0 + a.pass_q : a.nq1;
+    RowAcc<WT, false> acc[TG];
+    const int pass = pass_steps(a.image, QB * kImageBytes, cnt, a.s_log2, a.steps1);
+    for (int q0 = 0; q0 < a.steps1; q0 += pass) {
+        const int q1 = q0 + pass < a.steps1 ? q0 + pass : a.steps1;
         if (q0 > 0) __syncthreads();
-        build_image<WT>(img, cnt, q0 * QB, (q1 - q0) * QB, a.nb1, kThreads,
+        build_image<WT>(img, cnt, q0 * QB, (q1 - q0) * QB, a.nb1, threads,
                         [&](int t) { return a.x + (uint64_t)slot_tok[t] * a.x_pitch; });
         __syncthreads();
         for (int q = q0 + split; q < q1; q += S) {
-            if (q + S < a.nq1) load_quantum<WT, SS, QU>(nxt, row, a.qoff1, code_bytes, q + S, g);
+            if (q + S < a.steps1) load_quantum<WT, SS, QU>(nxt, row, a.qoff1, code_bytes, q + S, g, whole(q + S));
             const uint8_t *base = img + (uint32_t)((q - q0) * QB) * step_bytes;
-            multiply_quantum<WT, SS, QU, TG>(cur, q, a.nb1, g, groups, acc, [&](int tg, int step) {
+            multiply_quantum<WT, SS, QU, TG, false>(cur, q, whole(q), a.nb1, g, upper, groups, acc, [&](int tg, int, int step) {
                 return *reinterpret_cast<const rt_bf16x8 *>(base + (uint32_t)step * step_bytes + frag_off[tg]);
             });
             cur = nxt;
         }
     }
 #pragma unroll
-    for (int tg = 0; tg < TG; ++tg) red[wave][tg][lane] = row_total(acc[tg]);
+    for (int tg = 0; tg < TG; ++tg) red[(wave * TG + tg) * 64 + lane] = row_total(acc[tg], upper);
     __syncthreads();
     // ---- h = Swish(gate) * up * weight, one thread per (row, token) ----
-    for (int i = threadIdx.x; i < T * cnt * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < T * cnt * 8; i += threads) {
         const int rr = i & 7, t = (i >> 3) / cnt, slot = (i >> 3) % cnt;
         const int f = (grp * T + t) * 8 + rr;
         if (f >= a.F) continue;
         const int tg = slot >> 2, l = 16 * (slot & 3) + rr;
         float s = 0.0f, u = 0.0f;
         for (int w = 0; w < S; ++w) {
-            s += red[t * S + w][tg][l];
-            u += red[t * S + w][tg][l + 8];
+            const float *part = red + ((t * S + w) * TG + tg) * 64 + l;
+            s += part[0];
+            u += part[8];
         }
         const float hv = rt_swish(s) * u * psum[slot];
         // its place among the parts: block f / 32, element f % 32
@@ -266,11 +273,12 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeArgs a)
     }
 }
 
-template <int WT, int SS, int QU, int TG>
+template <int WT, int SS, int QU, int TG, bool HALF>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
-    constexpr int QB = QU * F::MF;
+    constexpr int QB = QU * F::MF, H = HALF ? 2 : 1, SB = QB * H;
+    constexpr int ROWS = HALF ? 8 : 16;
     __shared__ float red[kWaves][TG][64];
     __shared__ __attribute__((aligned(16))) int ids[kPairs];
     __shared__ int lead_pos[kPairs];             // a leader pair's place in the list
@@ -323,92 +331,77 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
     __syncthreads();
 
     const int j = lane & 15, g = lane >> 4;
-    const int r = (int)blockIdx.x * 16 + j;
+    const bool upper = j >= 8;
+    const int r = (int)blockIdx.x * ROWS + (j & (ROWS - 1));
     const uint64_t row_off = (uint64_t)(r < a.M ? r : a.M - 1) * a.down_pitch;
     const int code_bytes = F::BB * a.nb2;
-    const int items = __builtin_amdgcn_readfirstlane(n_lead) * a.nq2;
+    const int items = __builtin_amdgcn_readfirstlane(n_lead) * a.steps2;
     const int part = (j & 3) < 2 ? (j & 3) : 2;
     const __amdgpu_buffer_rsrc_t hres = __builtin_amdgcn_make_buffer_rsrc(
         a.h, 0, (int)((uint32_t)P * (uint32_t)a.h_pair), BUFFER_FLAGS);
+    auto quantum = [&](int p) { return HALF ? 2 * p + (upper ? 1 : 0) : p; };
+    auto whole = [&](int p) { return (p + 1) * SB <= a.nb2; };
     auto load = [&](Quantum<WT, SS, QU> &z, int i) {
-        const int li = i / a.nq2, qi = i - li * a.nq2;
-        const uint8_t *w = a.down + (uint64_t)lead_id[li] * a.down_expert + row_off;
-        load_quantum<WT, SS, QU>(z, w, a.qoff2, code_bytes, qi, g);
+        const int li = i / a.steps2, p = i - li * a.steps2;
+        const uint8_t *w = a.down + (uint64_t)__builtin_amdgcn_readfirstlane(lead_id[li]) * a.down_expert + row_off;
+        load_quantum<WT, SS, QU>(z, w, a.qoff2, code_bytes, quantum(p), g, whole(p));
     };
-    RowAcc<WT> acc[TG];
+    RowAcc<WT, HALF> acc[TG];
     Quantum<WT, SS, QU> cur, nxt;
     if (wave < items) load(cur, wave);
     for (int i = wave; i < items; i += kWaves) {
         if (i + kWaves < items) load(nxt, i + kWaves);
-        const int li = i / a.nq2, qi = i - li * a.nq2;
-        uint32_t off[TG];
-        uint32_t any = 0;
+        const int li = i / a.steps2, p = i - li * a.steps2;
+        const int blk0 = p * SB;
+        // one token group after the other (only those with a token of this
+        // expert): its fragments, blocks past the row and tokens without this
+        // expert as zeros
 #pragma unroll
         for (int tg = 0; tg < TG; ++tg) {
-            const int t = 4 * tg + (j >> 2);
-            const int p = tok_pair[li][t];
-            off[tg] = p >= 0 ? (uint32_t)p * (uint32_t)a.h_pair + (uint32_t)(64 * part + 16 * g) : OUT_OF_RANGE;
-            if (__ballot(p >= 0)) any |= 1u << tg;
-        }
-        const int blk0 = qi * QB;
-        // fragments: blocks past the row read zeros
-        rt_bf16x8 fr[TG][QB];
+            const int pr = tok_pair[li][4 * tg + (j >> 2)];
+            if (__ballot(pr >= 0) == 0) continue;
+            const uint32_t off = (uint32_t)pr * (uint32_t)a.h_pair + (uint32_t)(64 * part + 16 * g);
+            rt_bf16x8 fr[SB];
 #pragma unroll
-        for (int tg = 0; tg < TG; ++tg)
-            if (any >> tg & 1) {
-#pragma unroll
-                for (int s = 0; s < QB; ++s) {
-                    // the block whose values this lane group feeds to instruction s
-                    const int b = WT == W_MXFP4 ? blk0 + (s & ~3) + g : blk0 + s;
-                    const uint32_t o = off[tg] != OUT_OF_RANGE && b < a.nb2 ? off[tg] + (uint32_t)(blk0 + s) * kImageBytes
-                                                                            : OUT_OF_RANGE;
-                    fr[tg][s] = __builtin_bit_cast(rt_bf16x8, __builtin_amdgcn_raw_buffer_load_b128(hres, o, 0, 0));
-                }
+            for (int s = 0; s < SB; ++s) {
+                // the block whose values this lane group feeds to instruction s
+                const int b = WT == W_MXFP4 ? blk0 + (s & ~3) + g : blk0 + s;
+                const uint32_t o = pr >= 0 && b < a.nb2 ? off + (uint32_t)(blk0 + s) * kImageBytes : OUT_OF_RANGE;
+                fr[s] = __builtin_bit_cast(rt_bf16x8, __builtin_amdgcn_raw_buffer_load_b128(hres, o, 0, 0));
             }
-        if constexpr (TG == 1) {
-            multiply_quantum<WT, SS, QU, 1>(cur, qi, a.nb2, g, 1, acc, [&](int, int s) { return fr[0][s]; });
-        } else {
-            // both token groups, or the one that has tokens of this expert
-            RowAcc<WT> one[1];
-            if (any == 3) {
-                multiply_quantum<WT, SS, QU, 2>(cur, qi, a.nb2, g, 2, acc, [&](int tg, int s) { return fr[tg][s]; });
-            } else if (any == 1) {
-                one[0] = acc[0];
-                multiply_quantum<WT, SS, QU, 1>(cur, qi, a.nb2, g, 1, one, [&](int, int s) { return fr[0][s]; });
-                acc[0] = one[0];
-            } else {
-                one[0] = acc[TG - 1];
-                multiply_quantum<WT, SS, QU, 1>(cur, qi, a.nb2, g, 1, one, [&](int, int s) { return fr[TG - 1][s]; });
-                acc[TG - 1] = one[0];
-            }
+            RowAcc<WT, HALF> one[1] = {acc[tg]};
+            multiply_quantum<WT, SS, QU, 1, HALF>(cur, quantum(p), whole(p), a.nb2, g, upper, 1, one,
+                                                  [&](int, int h, int s) { return fr[h * QB + s]; });
+            acc[tg] = one[0];
         }
         cur = nxt;
     }
 #pragma unroll
-    for (int tg = 0; tg < TG; ++tg) red[wave][tg][lane] = row_total(acc[tg]);
+    for (int tg = 0; tg < TG; ++tg) red[wave][tg][lane] = row_total(acc[tg], upper);
     __syncthreads();
     if (tid < TG * 64) {
-        const int l = tid & 63, tg = tid >> 6;
-        const int m = (int)blockIdx.x * 16 + (l & 15), t = 4 * tg + (l >> 4);
-        if (m < a.M && t < a.N) {
+        const int l = tid & 63, tg = tid >> 6, col = l & 15;
+        const int m = (int)blockIdx.x * ROWS + col, t = 4 * tg + (l >> 4);
+        if (col < ROWS && m < a.M && t < a.N) {
             float s = 0.0f;
-            for (int w = 0; w < kWaves; ++w) s += red[w][tg][l];
+            for (int w = 0; w < kWaves; ++w) s += HALF ? red[w][tg][l] + red[w][tg][l + 8] : red[w][tg][l];
             a.y[(uint64_t)t * a.y_pitch + m] = s;
         }
     }
 }
 
 typedef void (*Kernel)(MoeArgs);
-template <int WT, int SS>
-void pick(int qu, int tg, Kernel *up, Kernel *down)
+template <int WT, int SS, int TG>
+void pick(int qu, bool half, Kernel *up, Kernel *down)
 {
-    if (tg == 1) {
-        *up = qu == 4 ? moe_up_kernel<WT, SS, 4, 1> : qu == 2 ? moe_up_kernel<WT, SS, 2, 1> : moe_up_kernel<WT, SS, 1, 1>;
-        *down = moe_down_kernel<WT, SS, 2, 1>;
-    } else {
-        *up = qu == 4 ? moe_up_kernel<WT, SS, 4, 2> : qu == 2 ? moe_up_kernel<WT, SS, 2, 2> : moe_up_kernel<WT, SS, 1, 2>;
-        *down = moe_down_kernel<WT, SS, 2, 2>;
-    }
+    *up = qu == 4 ? moe_up_kernel<WT, SS, 4, TG> : qu == 2 ? moe_up_kernel<WT, SS, 2, TG> : moe_up_kernel<WT, SS, 1, TG>;
+    *down = half ? moe_down_kernel<WT, SS, 1, TG, true> : moe_down_kernel<WT, SS, 2, TG, false>;
+}
+template <int WT, int SS>
+void pick(int qu, int tg, bool half, Kernel *up, Kernel *down)
+{
+    if (tg == 1) pick<WT, SS, 1>(qu, half, up, down);
+    else pick<WT, SS, 2>(qu, half, up, down);
 }
 
 }  // namespace
@@ -470,48 +463,35 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
     a.nb2 = (int32_t)(F / 32);
     a.qoff2 = (int32_t)quant_offset(F, down.w.scale_shift);
     const int64_t units1 = (gate.w.K + kpu - 1) / kpu, units2 = (F + kpu - 1) / kpu;
-    // waves per tile and units per quantum of the first launch: K in as few
-    // pieces as still make a workgroup for every CU
-    int qu = 4, s_log2 = 0;
-    const int64_t tiles = (F + 7) / 8 * (N < 2 ? k : N * k / 2 + 1);
-    auto grow = [&] {
-        s_log2 = 0;
-        while (s_log2 < 4 && (2 << s_log2) <= (units1 + qu - 1) / qu) ++s_log2;
-    };
-    grow();
-    while (qu > 1 && tiles * (1 << s_log2) < 256 * kWaves && s_log2 < 4) {
-        qu /= 2;
-        grow();
-    }
-    while (((int64_t)qu << s_log2) * (kpu / 32) * kImageBytes * N > kImageMax) {
-        if (qu > 1) qu /= 2;
-        else --s_log2;
-    }
-    a.nq1 = (int32_t)((units1 + qu - 1) / qu);
-    a.nq2 = (int32_t)((units2 + 1) / 2);
-    a.s_log2 = s_log2;
-    const int S = 1 << s_log2, T = kWaves >> s_log2;
-    const int64_t q_bytes = (int64_t)qu * (kpu / 32) * kImageBytes * N;
-    const int64_t pass = kImageMax / q_bytes / S * S;
-    a.pass_q = (int32_t)(pass < a.nq1 ? pass : (a.nq1 > 0 ? a.nq1 : 1));
-    const int lds = (int)(a.pass_q * q_bytes);
+    // about how many experts several tokens choose between them
+    const int64_t experts = N < 2 ? k : N * k / 2 + 1 < gate.E ? N * k / 2 + 1 : gate.E;
+    const int tg = N > 4 ? 2 : 1;
+    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * experts, 0, (int)N);
+    a.steps1 = p.steps;
+    a.s_log2 = p.s_log2;
+    a.image = p.image;
+    const int T = p.waves >> p.s_log2;
+    const int lds = p.waves * tg * 64 * 4 + p.image;
+    // tiles of eight output rows while sixteen would leave CUs without one
+    const bool half = (M + 15) / 16 < 2 * (int64_t)device_cus();
+    a.steps2 = (int32_t)((units2 + 1) / 2);
 
     Kernel ku = nullptr, kd = nullptr;
-    const int tg = N > 4 ? 2 : 1;
-    if (type == W_MXFP4) pick<W_MXFP4, 0>(qu, tg, &ku, &kd);
-    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(qu, tg, &ku, &kd) : pick<W_Q4_0, 0>(qu, tg, &ku, &kd);
-    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(qu, tg, &ku, &kd) : pick<W_Q8_0, 0>(qu, tg, &ku, &kd);
+    if (type == W_MXFP4) pick<W_MXFP4, 0>(p.qu, tg, half, &ku, &kd);
+    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(p.qu, tg, half, &ku, &kd) : pick<W_Q4_0, 0>(p.qu, tg, half, &ku, &kd);
+    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(p.qu, tg, half, &ku, &kd) : pick<W_Q8_0, 0>(p.qu, tg, half, &ku, &kd);
     else return hipErrorInvalidValue;
     hipError_t e = hipSuccess;
     if (F > 0) {
-        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), kImageMax);
+        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), 128 * 1024);
         if (e != hipSuccess) return e;
         const unsigned groups = (unsigned)(((F + 7) / 8 + T - 1) / T);
-        hipLaunchKernelGGL(ku, dim3(groups, (unsigned)(N * k)), dim3(kThreads), (unsigned)lds, stream, a);
+        hipLaunchKernelGGL(ku, dim3(groups, (unsigned)(N * k)), dim3(64 * p.waves), (unsigned)lds, stream, a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kd, dim3((unsigned)((M + 15) / 16)), dim3(kThreads), 0, stream, a);
+    const unsigned tiles = (unsigned)(half ? (M + 7) / 8 : (M + 15) / 16);
+    hipLaunchKernelGGL(kd, dim3(tiles), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 

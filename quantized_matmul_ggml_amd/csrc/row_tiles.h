@@ -178,14 +178,18 @@ __device__ inline void rt_swap16(uint32_t &a, uint32_t &b)
 
 typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
 
-// Loads quantum qi of the packed row at `row` (this lane's).  Every address
-// lies inside the row: code units past its end repeat its first bytes (their
-// activations are zeros and multiply_quantum zeroes their scales), and the
-// scale bytes of a quantum end at or before the row's end, because the row's
-// codes follow its scales.  The weights stream past the caches (kStreamLoad's
-// policy); the scales share cache lines with neighbouring quanta.
+typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
+
+// Loads quantum qi of the packed row at `row` (both this lane's).  Every
+// address lies inside the row: what lies past its end repeats its first bytes
+// (the activations there are zeros and multiply_quantum zeroes the scales),
+// and the scale bytes of a quantum with any block of the row end at or before
+// the row's end, because the row's codes follow its scales.  whole: every
+// lane's quantum lies wholly in its row (uniform).  The weights stream past
+// the caches; the scales share cache lines with neighbouring quanta.
 template <int WT, int SS, int QU>
-__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int g)
+__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int g,
+                                    bool whole)
 {
     constexpr int SB = Quantum<WT, SS, QU>::SB;
     const int c0 = 64 * QU * qi + 16 * g;
@@ -193,14 +197,15 @@ __device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, 
     auto load16 = [](const uint8_t *p) {
         return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4 *>(p)));
     };
-    if (64 * QU * (qi + 1) <= code_bytes) {                // uniform
+    const uint8_t *s = row + SB * qi;
+    if (whole) {
 #pragma unroll
         for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + c0 + 64 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + (c0 + 64 * i < code_bytes ? c0 + 64 * i : 0));
+        s = 64 * QU * qi < code_bytes ? s : row;
     }
-    const uint8_t *s = row + SB * qi;
     if constexpr (SB == 2) {
         z.s[0] = *reinterpret_cast<const uint16_t *>(s);
     } else if constexpr (SB == 4) {
@@ -223,12 +228,23 @@ __device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, 
 }
 
 // The sum of a lane's row and token over the instructions so far.  MXFP4 keeps
-// the matrix instruction's own accumulator (one per part, added at the end).
-template <int WT> struct RowAcc { rt_f32x4 c = {0, 0, 0, 0}; };
-template <int WT>
-__device__ inline float row_total(const RowAcc<WT> &a)
+// the matrix instruction's own accumulators (one per part, added at the end;
+// with HALF one set for each half of the columns).
+template <int WT, bool HALF>
+struct RowAcc {
+    rt_f32x4 c[WT == W_MXFP4 && HALF ? 2 : 1] = {};
+};
+template <int WT, bool HALF>
+__device__ inline float row_total(const RowAcc<WT, HALF> &a, bool upper)
 {
-    return WT == W_MXFP4 ? a.c[0] + a.c[1] + a.c[2] : a.c[0];
+    if constexpr (WT == W_MXFP4 && HALF) {
+        const float lo = a.c[0][0] + a.c[0][1] + a.c[0][2], hi = a.c[1][0] + a.c[1][1] + a.c[1][2];
+        return upper ? hi : lo;
+    } else if constexpr (WT == W_MXFP4) {
+        return a.c[0][0] + a.c[0][1] + a.c[0][2];
+    } else {
+        return a.c[0][0];
+    }
 }
 
 // Byte E of w as a signed int8, converted to float (one SDWA conversion).
@@ -239,25 +255,30 @@ __device__ inline uint32_t rt_pack(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(rt_f32x2{a, b}, rt_bf16x2));
 }
 
-// Multiplies quantum qi (in z) with the activation fragments frag(tg, step),
-// step = instruction index from the quantum's first one, for the token groups
-// tg < groups.  nb: blocks of the row (only the quantum that passes it masks
-// its scales).
-template <int WT, int SS, int QU, int TG, class Frag>
-__device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, int nb, int g, int groups,
-                                        RowAcc<WT> (&acc)[TG], Frag frag)
+// Multiplies the quanta in z with the activation fragments of token groups
+// tg < groups.  frag(tg, half, step) is the fragment of instruction `step` of
+// the quantum that columns 8 half .. 8 half + 7 hold.  Without HALF all
+// sixteen columns are rows of the same quantum (half is 0); with it columns
+// 0 .. 7 are eight rows' quantum 2 q and columns 8 .. 15 the same rows' quantum
+// 2 q + 1, so that a tile of eight rows still loads sixteen columns at once:
+// each weight fragment meets both halves' activations, and each half of the
+// columns keeps its own product.  qi: this lane's quantum; whole: as in
+// load_quantum; nb: blocks of the row.
+template <int WT, int SS, int QU, int TG, bool HALF, class Frag>
+__device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool whole, int nb, int g, bool upper, int groups,
+                                        RowAcc<WT, HALF> (&acc)[TG], Frag frag)
 {
     using F = RowFmt<WT, SS>;
-    const int blk0 = qi * QU * F::MF;
-    const bool tail = blk0 + QU * F::MF > nb;              // uniform
+    constexpr int H = HALF ? 2 : 1;
+    const int left = whole ? QU * F::MF : nb - qi * QU * F::MF;      // blocks of this quantum in the row
 #pragma unroll
     for (int i = 0; i < QU; ++i) {
         uint32_t d[4] = {z.q[i].x, z.q[i].y, z.q[i].z, z.q[i].w};
         if constexpr (WT == W_MXFP4) {
-            // lane group g holds block blk0 + 4 i + g: its scale byte as the
-            // exponent of a float (255 is NaN, 0 is 2^-127)
+            // lane group g holds block 4 i + g of the quantum: its scale byte
+            // as the exponent of a float (255 is NaN, 0 is 2^-127)
             uint32_t e = (z.s[i] >> (8 * g)) & 0xFFu;
-            if (tail) e = blk0 + 4 * i + g < nb ? e : 0u;
+            if (!whole) e = 4 * i + g < left ? e : 0u;
             const float f = __builtin_bit_cast(float, e << 23);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -269,8 +290,11 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, int nb, 
                 const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
 #pragma unroll
                 for (int tg = 0; tg < TG; ++tg)
-                    if (tg < groups)
-                        acc[tg].c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 4 * i + t), b, acc[tg].c, 0, 0, 0);
+                    if (tg < groups) {
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            acc[tg].c[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, h, 4 * i + t), b, acc[tg].c[h], 0, 0, 0);
+                    }
             }
         } else {
             rt_swap32(d[0], d[2]);
@@ -296,17 +320,23 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, int nb, 
                 }
                 const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
                 const int blk = i * F::MF + t;                 // static
-                const int h = blk >> SS;                       // scale (half) index within the quantum
-                const uint32_t sb = (h & 1) ? z.s[h / 2] >> 16 : z.s[h / 2] & 0xFFFFu;
+                const int sh = blk >> SS;                      // the block's scale (a half) within the quantum
+                const uint32_t sb = (sh & 1) ? z.s[sh / 2] >> 16 : z.s[sh / 2] & 0xFFFFu;
                 float f = (float)__builtin_bit_cast(_Float16, (uint16_t)sb);
                 if constexpr (WT == W_Q4_0) f *= 0.0625f;
-                if (tail) f = blk0 + blk < nb ? f : 0.0f;
+                if (!whole) f = blk < left ? f : 0.0f;
 #pragma unroll
                 for (int tg = 0; tg < TG; ++tg)
                     if (tg < groups) {
-                        const rt_f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, F::MF * i + t), b,
-                                                                                   rt_f32x4{0, 0, 0, 0}, 0, 0, 0);
-                        acc[tg].c[0] = fmaf(f, s[0] + (s[1] + s[2]), acc[tg].c[0]);
+                        const rt_f32x4 zero = {0, 0, 0, 0};
+                        const rt_f32x4 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 0, blk), b, zero, 0, 0, 0);
+                        float sum = s0[0] + (s0[1] + s0[2]);
+                        if constexpr (HALF) {
+                            const rt_f32x4 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 1, blk), b, zero, 0, 0, 0);
+                            const float other = s1[0] + (s1[1] + s1[2]);
+                            sum = upper ? other : sum;
+                        }
+                        acc[tg].c[0][0] = fmaf(f, sum, acc[tg].c[0][0]);
                     }
             }
         }
@@ -318,6 +348,70 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, int nb, 
 __device__ inline float rt_swish(float z)
 {
     return z / (1.0f + expf(-z));
+}
+
+// ---- host: how a launch splits its rows ----
+struct RowPlan {
+    int qu;          // units per quantum (1, 2, 4)
+    int half;        // tiles of eight rows (HALF)
+    int s_log2;      // log2 of the waves that share a tile
+    int waves;       // per workgroup
+    int steps;       // quanta (or pairs of quanta) per row
+    int step_bytes;  // image bytes per step and token
+    int image;       // LDS bytes for the image
+};
+
+// units: 64-byte units per row, mf: blocks per unit; tiles: tiles of the
+// launch; half_tiles: their number with eight rows each (0: not available);
+// tokens: the most tokens one image holds.
+//
+// Sixteen waves on every CU keep enough loads in flight to stream at the
+// memory's rate, so a launch aims at that many (tile, wave) tasks, with as few
+// waves sharing a tile and as large quanta (one scale load per QU code loads)
+// as still give them.  Workgroups are small (four waves) while their image is,
+// so that several share a CU and one's loads run beside another's setup; with
+// more tokens a larger workgroup shares one image.
+inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens)
+{
+    const int64_t target = 16 * (int64_t)device_cus();
+    RowPlan p = {1, 0, 0, 4, 0, 0, 0};
+    auto steps_of = [&](int qu, int half) { return ((units + qu - 1) / qu + half) / (1 + half); };
+    int64_t best = -1;
+    for (int half = 0; half <= (half_tiles ? 1 : 0) && best < target; ++half) {
+        const int64_t t = half ? half_tiles : tiles;
+        for (int qu = 4; qu >= 1 && best < target; qu /= 2) {
+            int s = 0;
+            while (s < 4 && t << s < target && (2 << s) <= steps_of(qu, half)) ++s;
+            if (t << s > best) {
+                best = t << s;
+                p.qu = qu;
+                p.half = half;
+                p.s_log2 = s;
+            }
+        }
+    }
+    p.waves = tokens <= 2 ? 4 : tokens <= 4 ? 8 : 16;
+    if (p.waves < 1 << p.s_log2) p.waves = 1 << p.s_log2;
+    auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : 112 * 1024; };
+    // one step of every wave of a tile has to fit the image
+    for (;;) {
+        p.step_bytes = p.qu * (1 + p.half) * mf * kImageBytes;
+        if (((int64_t)p.step_bytes * tokens << p.s_log2) <= budget()) break;
+        if (p.waves < 16) p.waves *= 2;
+        else if (p.qu > 1) p.qu /= 2;
+        else --p.s_log2;
+    }
+    p.steps = (int)steps_of(p.qu, p.half);
+    const int64_t all = (int64_t)p.steps * p.step_bytes * tokens;
+    p.image = (int)(all < budget() ? all : budget());
+    return p;
+}
+// Steps per pass over K of an image for `tokens` tokens: all of them, or a
+// multiple of the waves per tile.
+__host__ __device__ inline int pass_steps(int image, int step_bytes, int tokens, int s_log2, int steps)
+{
+    const int n = image / (step_bytes * tokens);
+    return n < steps ? n >> s_log2 << s_log2 : steps > 0 ? steps : 1;
 }
 
 }  // namespace qmm
