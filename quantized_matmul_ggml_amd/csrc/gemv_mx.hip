@@ -10,10 +10,9 @@
 // waves sharing a tile's K in interleaved quanta of QU units (128 QU values of
 // k, 64 QU code bytes of each row); where that leaves the chip idle a tile has
 // eight rows and a wave takes two quanta of each at once (HALF, row_tiles.h).
-// The first quantum of every wave is in flight while the workgroup splits its
-// tokens into the LDS image; each wave's next quantum (of this tile or, at its
-// end, of the workgroup's next one) is loaded before the current one is
-// multiplied.  The S partial sums meet in LDS and are added in wave order.
+// The first quanta of every wave are in flight while the workgroup splits its
+// tokens into the LDS image, and those of its next tile while the S partial
+// sums of this one meet in LDS, where they are added in wave order.
 #include "row_tiles.h"
 
 namespace qmm {
@@ -46,7 +45,7 @@ struct MxArgs {
     MxItem item[QMM_GEMV_BATCH_MAX];
 };
 
-template <int QU, int TG, bool SW, bool HALF>
+template <int QU, int TG, bool SW, bool HALF, int D>
 __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
 {
     constexpr int WT = W_MXFP4, SS = 0;
@@ -75,16 +74,27 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
     float *const red = reinterpret_cast<float *>(lds);     // [2][waves][TG][64]
     uint8_t *const img = lds + 2 * waves * TG * 64 * 4;
 
-    // ---- the lane's row of a tile: a column of the gate or up matrix; rows
-    // past M repeat the last one and are not stored ----
-    const uint8_t *const Wl = SW && upper ? W2 : W;
-    const uint32_t pl = SW && upper ? pitch2 : pitch;
+    // ---- the rows of a tile: columns of the gate or up matrix; rows past M
+    // repeat the last one and are not stored ----
+    const int last_q = (nb - 1) / QB;
     auto quantum = [&](int p) { return HALF ? 2 * p + (upper ? 1 : 0) : p; };
     auto whole = [&](int p) { return (p + 1) * SB <= nb; };
-    auto load = [&](Quantum<WT, SS, QU> &z, int grp, int p) {
-        const int64_t r = (int64_t)(grp * T + tile_in) * ROWS + (j & (ROWS - 1));
-        load_quantum<WT, SS, QU>(z, Wl + (uint64_t)(r < M ? r : M - 1) * pl, qoff, 16 * nb, quantum(p), g, whole(p));
+    Quantum<WT, SS, QU> z[D];
+    // the wave's k-th quantum from step p0 of tile group grp on
+    auto load = [&](int grp, int p0) {
+        return [&, grp, p0](auto d, int k) {
+            // load_quantum's two rows: with one unit the lane's own (HALF:
+            // the row its half is of), with two rows j % 8 of both halves
+            auto at = [&](const uint8_t *base, uint32_t step, int64_t r) { return base + (uint64_t)(r < M ? r : M - 1) * step; };
+            const int64_t r = (int64_t)(grp * T + tile_in) * ROWS + (j & 7);
+            const bool own = QU == 1 && !HALF && upper;
+            const uint8_t *row0 = SW && own ? at(W2, pitch2, r) : at(W, pitch, !SW && own ? r + 8 : r);
+            const uint8_t *row1 = QU == 1 ? row0 : SW ? at(W2, pitch2, r) : at(W, pitch, r + 8);
+            load_quantum<WT, SS, QU>(z[d.value], row0, row1, qoff, 16 * nb, quantum(p0 + split + k * S), last_q, g, upper);
+        };
     };
+    // its quanta in [p0, p1)
+    auto share = [&](int p0, int p1) { return p0 + split < p1 ? (p1 - p0 - split + S - 1) >> s_log2 : 0; };
     // ---- activation fragments: matrix row 4 t + p is part p of token t ----
     uint32_t frag_off[TG];
 #pragma unroll
@@ -94,9 +104,15 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
     }
     const uint32_t block_bytes = (uint32_t)N * kImageBytes;
 
+    // ---- the first pass's activations, then the first weights ----
+    auto row = [&](int t) { return X + (uint64_t)t * x_pitch; };
     int grp = blockIdx.x;
-    Quantum<WT, SS, QU> cur, nxt;
-    if (split < steps) load(cur, grp, split);
+    ImageAhead ahead;
+    const int p_end = pass < steps ? pass : steps;
+    if (steps > 0) {
+        image_ahead<WT>(ahead, N, 0, p_end * SB, nb, threads, row);
+        stream_begin<0, 1>(share(0, p_end), load(grp, 0));
+    }
     int parity = 0;
     bool built = false;
     for (; grp < n_groups; grp += wgs, parity ^= 1) {
@@ -104,23 +120,26 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
         for (int p0 = 0; p0 < steps; p0 += pass) {
             const int p1 = p0 + pass < steps ? p0 + pass : steps;
             if (!built || pass < steps) {
-                if (built) __syncthreads();        // the last pass's image is no longer read
-                build_image<WT>(img, N, p0 * SB, (p1 - p0) * SB, nb, threads,
-                                [&](int t) { return X + (uint64_t)t * x_pitch; });
+                if (built) {
+                    __syncthreads();               // the last pass's image is no longer read
+                    build_image<WT, false>(img, N, p0 * SB, (p1 - p0) * SB, nb, threads, row, ahead);
+                } else {
+                    build_image<WT, true>(img, N, p0 * SB, (p1 - p0) * SB, nb, threads, row, ahead);
+                    stream_begin<1, D>(share(p0, p1), load(grp, p0));
+                }
                 built = true;
                 __syncthreads();
             }
-            for (int p = p0 + split; p < p1; p += S) {
-                const bool more = p + S < steps;
-                const int ngrp = more ? grp : grp + wgs;
-                if (ngrp < n_groups) load(nxt, ngrp, more ? p + S : split);
+            stream<D>(share(p0, p1), load(grp, p0), [&](auto d, int k) {
+                const int p = p0 + split + k * S;
                 const uint8_t *base = img + (uint32_t)((p - p0) * SB) * block_bytes;
-                multiply_quantum<WT, SS, QU, TG, HALF>(cur, quantum(p), whole(p), nb, g, upper, TG, acc,
+                multiply_quantum<WT, SS, QU, TG, HALF>(z[d.value], quantum(p), whole(p), nb, g, upper, TG, acc,
                                                        [&](int tg, int h, int step) {
                     return *reinterpret_cast<const rt_bf16x8 *>(base + (uint32_t)(h * QB + step) * block_bytes + frag_off[tg]);
                 });
-                cur = nxt;
-            }
+            });
+            const int next = p1 < steps ? p1 : 0, next_end = next + pass < steps ? next + pass : steps;
+            stream_begin<0, D>(share(next, next_end), load(p1 < steps ? grp : grp + wgs, next));
         }
         float *const mine = red + parity * waves * TG * 64;
 #pragma unroll
@@ -144,10 +163,19 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
 }
 
 typedef void (*Kernel)(MxArgs);
-template <int TG, bool SW, bool HALF>
-Kernel pick(int qu)
+// depth: quanta of one wave and pass over K; with one or two there is nothing to
+// load ahead.
+template <int QU, int TG, bool SW, bool HALF>
+Kernel pick_depth(int depth)
 {
-    return qu == 4 ? gemv_mx_kernel<4, TG, SW, HALF> : qu == 2 ? gemv_mx_kernel<2, TG, SW, HALF> : gemv_mx_kernel<1, TG, SW, HALF>;
+    constexpr int D = QU == 1 ? 4 : 3;
+    return depth >= 3 ? gemv_mx_kernel<QU, TG, SW, HALF, D>
+                      : depth == 2 ? gemv_mx_kernel<QU, TG, SW, HALF, 2> : gemv_mx_kernel<QU, TG, SW, HALF, 1>;
+}
+template <int TG, bool SW>
+Kernel pick(int qu, int depth)
+{
+    return qu == 2 ? pick_depth<2, TG, SW, false>(depth) : pick_depth<1, TG, SW, false>(depth);
 }
 
 hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStream_t stream)
@@ -160,7 +188,7 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
         half += (tasks[i].w.M + 7) / 8;
     }
     if (half == 0 || N == 0) return hipSuccess;
-    const RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N);
+    const RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N, (int)N);
     const int rows = sw || p.half ? 8 : 16, T = p.waves >> p.s_log2, tg = N > 4 ? 2 : 1;
     MxArgs a = {};
     a.N = (int32_t)N;
@@ -197,9 +225,10 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
         it.wgs = (int32_t)wgs;
         if (wgs > widest) widest = wgs;
     }
-    const Kernel k = sw     ? (tg == 1 ? pick<1, true, false>(p.qu) : pick<2, true, false>(p.qu))
-                     : p.half ? (tg == 1 ? pick<1, false, true>(p.qu) : pick<2, false, true>(p.qu))
-                              : (tg == 1 ? pick<1, false, false>(p.qu) : pick<2, false, false>(p.qu));
+    const int depth = (a.pass + (1 << p.s_log2) - 1) >> p.s_log2;
+    const Kernel k = p.half ? pick_depth<1, 1, false, true>(depth)
+                     : sw   ? (tg == 1 ? pick<1, true>(p.qu, depth) : pick<2, true>(p.qu, depth))
+                            : (tg == 1 ? pick<1, false>(p.qu, depth) : pick<2, false>(p.qu, depth));
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(k), 128 * 1024);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k, dim3((unsigned)widest, (unsigned)n), dim3(64 * p.waves), (unsigned)lds, stream, a);

@@ -18,10 +18,10 @@
 //    h = Swish(gate) * up, times the token's weight for the expert (so that
 //    the second launch only adds), goes to the workspace as the three bf16
 //    parts of row_tiles.h, in the order the matrix instructions read them.
-//  * moe_down_kernel: one workgroup per 16 output rows.  Its sixteen waves
-//    share the quanta of all leaders' down rows; since the weights are already
-//    in h, the experts' products add up in the same accumulators.  The waves'
-//    sums are added in wave order, so results do not depend on timing.
+//  * moe_down_kernel: one workgroup per 8 output rows.  Its sixteen waves share
+//    the quanta of all leaders' down rows; the weights are already in h, so the
+//    experts' products only add up, in a fixed order: results do not depend
+//    on timing.
 #include "row_tiles.h"
 
 namespace qmm {
@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kWaves = 16;            // of moe_down_kernel's workgroups
 constexpr int kThreads = 64 * kWaves;
+constexpr int kDownUnits = 1;         // units per quantum of moe_down_kernel (its pair of quanta is 128 bytes of a row)
 constexpr int kPairs = QMM_MOE_MAX_TOKENS * QMM_MOE_MAX_TOP_K;
 static_assert(kPairs == 128, "two pairs per lane of a wave");
 
@@ -132,276 +133,296 @@ struct MoeArgs {
     int32_t steps2;           // moe_down_kernel: quanta (or pairs) per row
 };
 
-template <int WT, int SS, int QU, int TG>
+// A workgroup takes T tiles of eight rows of one expert and one or two of its
+// pairs; an expert with more makes several, whose weights then come from the
+// caches (with four pairs a workgroup the few experts that have them needed
+// twice the LDS, took several passes over K, and finished last).
+template <int WT, int SS, int QU, int D>
 __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
     constexpr int QB = QU * F::MF;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ float pair_weight[kPairs];
-    __shared__ float psum[8];
-    __shared__ int slot_tok[8], slot_pair[8];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int P = a.N * a.k;
     const int pair = blockIdx.y;
-    const int e = a.ids[pair];
-    if (e < 0 || e >= a.E) return;                   // an empty slot
-    // every pair that names this expert; the first of them leads
+    // every pair's expert, pairs `lane` and `lane + 64`
     const int id0 = lane < P ? a.ids[lane] : -1, id1 = lane + 64 < P ? a.ids[lane + 64] : -1;
+    const int e = pair < 64 ? __builtin_amdgcn_readlane(id0, pair) : __builtin_amdgcn_readlane(id1, pair - 64);
+    if (e < 0 || e >= a.E) return;                   // an empty slot
+    // The pairs that name this expert, in order (a token that names an expert
+    // twice has two); every second one leads, the next one is its mate.
     const uint64_t m0 = __ballot(id0 == e), m1 = __ballot(id1 == e);
-    const int leader = m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1);
-    if (leader != pair) return;
+    const uint64_t from0 = pair < 63 ? ~0ull << (pair + 1) : 0, from1 = pair < 64 ? ~0ull : pair < 127 ? ~0ull << (pair - 63) : 0;
+    const int later = __builtin_popcountll(m0 & from0) + __builtin_popcountll(m1 & from1);
+    const int rank = __builtin_popcountll(m0) + __builtin_popcountll(m1) - 1 - later;
+    if (rank & 1) return;
+    const int now = later ? 2 : 1;
+    const int mate = m0 & from0 ? __builtin_ctzll(m0 & from0) : later ? 64 + __builtin_ctzll(m1 & from1) : pair;
 
     const int j = lane & 15, g = lane >> 4;
     const int threads = blockDim.x, waves = threads >> 6;
     const int S = 1 << a.s_log2, T = waves >> a.s_log2;
     const int split = wave & (S - 1), tile_in = wave >> a.s_log2;
     const int grp = blockIdx.x;
-    float *const red = reinterpret_cast<float *>(lds);     // [waves][TG][64]
-    uint8_t *const img = lds + waves * TG * 64 * 4;
+    float *const red = reinterpret_cast<float *>(lds);     // [waves][64]
+    uint8_t *const img = lds + waves * 64 * 4;
 
-    // the first quantum is in flight while the tokens are set up
+    // ---- the activations and the first quanta of weights ----
     const bool upper = j >= 8;
-    const uint8_t *const W = upper ? a.up + (uint64_t)e * a.up_expert : a.gate + (uint64_t)e * a.gate_expert;
-    const int r = (grp * T + tile_in) * 8 + (j & 7);
-    const uint8_t *const row = W + (uint64_t)(r < a.F ? r : a.F - 1) * (upper ? a.up_pitch : a.gate_pitch);
+    const int r = (grp * T + tile_in) * 8 + (j & 7), rc = r < a.F ? r : a.F - 1;
+    const uint8_t *const row_g = a.gate + (uint64_t)e * a.gate_expert + (uint64_t)rc * a.gate_pitch;
+    const uint8_t *const row_u = a.up + (uint64_t)e * a.up_expert + (uint64_t)rc * a.up_pitch;
+    const uint8_t *const row0 = QU == 1 && upper ? row_u : row_g;
     const int code_bytes = F::BB * a.nb1;
-    Quantum<WT, SS, QU> cur, nxt;
+    const int last_q = (a.nb1 - 1) / QB;
     auto whole = [&](int q) { return (q + 1) * QB <= a.nb1; };
-    if (split < a.steps1) load_quantum<WT, SS, QU>(cur, row, a.qoff1, code_bytes, split, g, whole(split));
-
-    // ---- the tokens: bit t of `toks`; thread t adds up the weights of token
-    // t's slots in slot order (a token may name an expert twice) ----
-    if (wave == 0) {
-        if (lane < P) pair_weight[lane] = id0 == e ? a.weights[lane] : 0.0f;
-        if (lane + 64 < P) pair_weight[lane + 64] = id1 == e ? a.weights[lane + 64] : 0.0f;
-    }
-    uint32_t toks = 0;
-    for (int t = 0; t < a.N; ++t) {                  // N <= 8
-        const int b = t * a.k, c = b + a.k;          // pairs b .. c - 1
-        auto bits = [&](uint64_t m, int base) -> uint64_t {
-            const int lo = b - base < 0 ? 0 : b - base, hi = c - base > 64 ? 64 : c - base;
-            if (lo >= hi) return 0;
-            return (m >> lo) & (hi - lo == 64 ? ~0ull : (1ull << (hi - lo)) - 1);
+    const int pass = pass_steps(a.image, QB * kImageBytes, now, a.s_log2, a.steps1);
+    const float *const x0 = a.x + (uint64_t)(pair / a.k) * a.x_pitch, *const x1 = a.x + (uint64_t)(mate / a.k) * a.x_pitch;
+    auto rows = [&](int place) { return place ? x1 : x0; };
+    ImageAhead ahead;
+    Quantum<WT, SS, QU> z[D];
+    // the wave's k-th quantum from step q0 of the row on, and their number in
+    // [q0, q1)
+    auto load = [&](int q0) {
+        return [&, q0](auto d, int k) {
+            load_quantum<WT, SS, QU>(z[d.value], row0, row_u, a.qoff1, code_bytes, q0 + split + k * S, last_q, g, upper);
         };
-        if (bits(m0, 0) | bits(m1, 64)) toks |= 1u << t;
+    };
+    auto share = [&](int q0, int q1) { return q0 + split < q1 ? (q1 - q0 - split + S - 1) >> a.s_log2 : 0; };
+    if (a.steps1 > 0) {
+        image_ahead<WT>(ahead, now, 0, pass * QB, a.nb1, threads, rows);
+        stream_begin<0, D - 1>(share(0, pass), load(0));
     }
-    const int cnt = __builtin_popcount(toks);
-    __syncthreads();
-    if (threadIdx.x < 8 && (toks >> threadIdx.x & 1)) {
-        const int t = threadIdx.x, slot = __builtin_popcount(toks & ((1u << t) - 1));
-        const int b = t * a.k;
-        float p = 0.0f;
-        for (int s = 0; s < a.k; ++s) p += pair_weight[b + s];
-        psum[slot] = p;
-        slot_tok[slot] = t;
-        // the token's first pair: the lowest set bit from b on
-        const uint64_t low = b < 64 ? m0 >> b : 0;
-        slot_pair[slot] = low ? b + __builtin_ctzll(low)
-                              : b > 64 ? b + __builtin_ctzll(m1 >> (b - 64)) : 64 + __builtin_ctzll(m1);
-    }
-    __syncthreads();
-
-    uint32_t frag_off[TG];
-#pragma unroll
-    for (int tg = 0; tg < TG; ++tg) {
-        const int tok = 4 * tg + (j >> 2), part = (j & 3) < 2 ? (j & 3) : 2;
-        frag_off[tg] = (uint32_t)((tok < cnt ? tok : cnt - 1) * kImageBytes + 64 * part + 16 * g);
-    }
-    const uint32_t step_bytes = (uint32_t)cnt * kImageBytes;
-    const int groups = __builtin_amdgcn_readfirstlane(cnt > 4 ? 2 : 1);
-
-    RowAcc<WT, false> acc[TG];
-    const int pass = pass_steps(a.image, QB * kImageBytes, cnt, a.s_log2, a.steps1);
+    // columns of the activations' operand: four each for two tokens, three
+    // parts and the last again; with one token it stands in both
+    const uint32_t step_bytes = (uint32_t)now * kImageBytes;
+    const uint32_t frag_off = (uint32_t)((j >> 2 & now - 1) * kImageBytes + ((j & 3) < 2 ? (j & 3) : 2) * 64 + 16 * g);
+    RowAcc<WT, false> acc[1];
     for (int q0 = 0; q0 < a.steps1; q0 += pass) {
         const int q1 = q0 + pass < a.steps1 ? q0 + pass : a.steps1;
-        if (q0 > 0) __syncthreads();
-        build_image<WT>(img, cnt, q0 * QB, (q1 - q0) * QB, a.nb1, threads,
-                        [&](int t) { return a.x + (uint64_t)slot_tok[t] * a.x_pitch; });
+        if (q0 == 0) {
+            build_image<WT, true>(img, now, 0, q1 * QB, a.nb1, threads, rows, ahead);
+            stream_begin<D - 1, D>(share(0, q1), load(0));
+        } else {
+            __syncthreads();                       // the last image is no longer read
+            stream_begin<0, D>(share(q0, q1), load(q0));
+            build_image<WT, false>(img, now, q0 * QB, (q1 - q0) * QB, a.nb1, threads, rows, ahead);
+        }
         __syncthreads();
-        for (int q = q0 + split; q < q1; q += S) {
-            if (q + S < a.steps1) load_quantum<WT, SS, QU>(nxt, row, a.qoff1, code_bytes, q + S, g, whole(q + S));
-            const uint8_t *base = img + (uint32_t)((q - q0) * QB) * step_bytes;
-            multiply_quantum<WT, SS, QU, TG, false>(cur, q, whole(q), a.nb1, g, upper, groups, acc, [&](int tg, int, int step) {
-                return *reinterpret_cast<const rt_bf16x8 *>(base + (uint32_t)step * step_bytes + frag_off[tg]);
+        stream<D>(share(q0, q1), load(q0), [&](auto d, int k) {
+            const int q = q0 + split + k * S;
+            const uint8_t *at = img + (uint32_t)((q - q0) * QB) * step_bytes + frag_off;
+            multiply_quantum<WT, SS, QU, 1, false>(z[d.value], q, whole(q), a.nb1, g, upper, 1, acc, [&](int, int, int step) {
+                return *reinterpret_cast<const rt_bf16x8 *>(at + (uint32_t)step * step_bytes);
             });
-            cur = nxt;
-        }
+        });
     }
-#pragma unroll
-    for (int tg = 0; tg < TG; ++tg) red[(wave * TG + tg) * 64 + lane] = row_total(acc[tg], upper);
+    red[wave * 64 + lane] = row_total(acc[0], upper);
     __syncthreads();
-    // ---- h = Swish(gate) * up * weight, one thread per (row, token) ----
-    for (int i = threadIdx.x; i < T * cnt * 8; i += threads) {
-        const int rr = i & 7, t = (i >> 3) / cnt, slot = (i >> 3) % cnt;
-        const int f = (grp * T + t) * 8 + rr;
-        if (f >= a.F) continue;
-        const int tg = slot >> 2, l = 16 * (slot & 3) + rr;
-        float s = 0.0f, u = 0.0f;
-        for (int w = 0; w < S; ++w) {
-            const float *part = red + ((t * S + w) * TG + tg) * 64 + l;
-            s += part[0];
-            u += part[8];
+    // ---- h = Swish(gate) * up * weight, one thread per (row, place); the last
+    // workgroup also clears the parts of the rows after F in the last group of
+    // four blocks, which moe_down_kernel reads ----
+    const int f_begin = grp * T * 8;
+    const int f_end = grp == (int)gridDim.x - 1 ? (a.F + 127) / 128 * 128 : f_begin + T * 8;
+    for (int i = threadIdx.x; i < (f_end - f_begin) * 2; i += threads) {
+        const int place = i & 1, ff = i >> 1, f = f_begin + ff;
+        if (place >= now) continue;
+        const int home = place ? mate : pair;
+        float hv = 0.0f;
+        if (f < a.F) {
+            const float *part = red + (ff >> 3) * S * 64 + 16 * place + (ff & 7);
+            float s = 0.0f, u = 0.0f;
+            for (int w = 0; w < S; ++w) {
+                s += part[64 * w];
+                u += part[64 * w + 8];
+            }
+            hv = rt_swish(s) * u * a.weights[home];
         }
-        const float hv = rt_swish(s) * u * psum[slot];
         // its place among the parts: block f / 32, element f % 32
         const int b = f >> 5, el = f & 31;
         int q, idx;
         if (WT == W_Q8_0) {
-            const int o = el >> 3;                   // octets 0, 1, 2, 3 sit in quarters 0, 2, 1, 3
+            const int o = el >> 3;         // octets 0, 1, 2, 3 sit in quarters 0, 2, 1, 3
             q = o == 1 ? 2 : o == 2 ? 1 : o;
             idx = el & 7;
         } else {
             q = (el & 15) >> 2;
             idx = 2 * (el & 3) + (el >> 4);
         }
-        const uint32_t hb = __builtin_bit_cast(uint32_t, hv);
-        const bool special = (hb & 0x7F800000u) == 0x7F800000u;
-        const uint32_t hi = (hb & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : hb & 0xFFFF0000u;
-        float r1 = hv - __builtin_bit_cast(float, hb & 0xFFFF0000u);
-        r1 = special ? 0.0f : r1;
-        const uint32_t mid = __builtin_bit_cast(uint32_t, r1) & 0xFFFF0000u;
-        const uint32_t lo = __builtin_bit_cast(uint32_t, r1 - __builtin_bit_cast(float, mid));
-        uint16_t *dst = reinterpret_cast<uint16_t *>(a.h + (uint64_t)slot_pair[slot] * a.h_pair +
+        // the three parts, as split_parts makes them
+        auto top = [](float x) { return __builtin_bit_cast(uint32_t, x) >> 16; };
+        auto rest = [&](float x) { return x - __builtin_bit_cast(float, top(x) << 16); };
+        const float mid = fabsf(hv) == INFINITY ? 0.0f : rest(hv);
+        uint16_t *dst = reinterpret_cast<uint16_t *>(a.h + (uint64_t)home * a.h_pair +
                                                      (uint64_t)image_step<WT>(b, q) * kImageBytes +
                                                      16 * image_group<WT>(b, q)) + idx;
-        dst[0] = (uint16_t)(hi >> 16);
-        dst[32] = (uint16_t)(mid >> 16);
-        dst[64] = (uint16_t)(lo >> 16);
+        dst[0] = (uint16_t)top(hv);
+        dst[32] = (uint16_t)top(mid);
+        dst[64] = (uint16_t)top(rest(mid));
     }
 }
 
-template <int WT, int SS, int QU, int TG, bool HALF>
+// A tile is eight rows: columns 0 .. 7 of the matrix instruction hold quantum
+// 2 p of the rows, columns 8 .. 15 quantum 2 p + 1, and likewise matrix rows
+// 0 .. 7 the parts of two tokens' activations of quantum 2 p and rows 8 .. 15
+// those of quantum 2 p + 1: the two diagonal quarters of D are the sums wanted.
+// An entry is an expert and one or two of its pairs (an expert with more
+// makes several, whose weights then come from the caches).  An item,
+// one entry's pair of quanta, is loaded while the item before is multiplied:
+// its weights, and its tokens' parts, which lie together in the workspace and
+// go through a piece of LDS of the wave's own to reach their lanes (loaded
+// fragment by fragment they were four times the load instructions, and the
+// texture-address unit was the bound).
+template <int WT, int SS, int QU>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
-    constexpr int QB = QU * F::MF, H = HALF ? 2 : 1, SB = QB * H;
-    constexpr int ROWS = HALF ? 8 : 16;
-    __shared__ float red[kWaves][TG][64];
+    constexpr int QB = QU * F::MF, SB = 2 * QB;
+    constexpr int CHUNK = SB * kImageBytes;      // a token's parts of one item
+    constexpr int HALF_LDS = CHUNK / 2 + 128, TOK_LDS = 2 * HALF_LDS + 64;   // strides that spread the banks
+    constexpr int NA = (2 * CHUNK + 1023) / 1024;          // 16-byte loads per lane for two tokens
+    __shared__ __attribute__((aligned(16))) uint8_t parts[kWaves][2 * TOK_LDS];
+    __shared__ float sums[kWaves][8][16];
     __shared__ __attribute__((aligned(16))) int ids[kPairs];
-    __shared__ int lead_pos[kPairs];             // a leader pair's place in the list
-    __shared__ int lead_id[kPairs];
-    __shared__ int16_t tok_pair[kPairs][8];      // the pair that holds (leader, token)'s h, or -1
-    __shared__ int n_lead;
+    __shared__ int4 entry[kPairs + 1];           // expert, its two pairs (-1: one only)
+    __shared__ int count[2];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int P = a.N * a.k;
-    // ---- the chosen experts, in the order of their first pair ----
     if (tid < kPairs) {
         const int v = tid < P ? a.ids[tid] : -1;
         ids[tid] = v >= 0 && v < a.E ? v : -1;
     }
-    reinterpret_cast<int *>(tok_pair)[tid & 511] = -1;      // 512 dwords
-    static_assert(sizeof(tok_pair) == 4 * 512 && kThreads >= 512, "cleared in one go");
+    for (int i = lane; i < 128; i += 64) (&sums[wave][0][0])[i] = 0.0f;
     __syncthreads();
-    int first = -1, first_tok = -1;
-    if (tid < P && ids[tid] >= 0) {
-        const int v = ids[tid], t0 = tid / a.k * a.k;
-        // from the last pair down, so that the lowest match stays
+    // ---- entries: every second pair of an expert starts one ----
+    int rank = 0, mate = kPairs;
+    const int mine_id = tid < P ? ids[tid] : -1;
+    if (wave < 2) {
 #pragma unroll 4
-        for (int c = (P - 1) >> 2; c >= 0; --c) {
+        for (int c = 0; c < (P + 3) >> 2; ++c) {
             const int4 w = reinterpret_cast<const int4 *>(ids)[c];
             const int m[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 3; i >= 0; --i)
-                if (m[i] == v) {
-                    first = 4 * c + i;
-                    if (4 * c + i >= t0) first_tok = 4 * c + i;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int p = 4 * c + i;
+                rank += m[i] == mine_id && p < tid ? 1 : 0;
+                mate = min(mate, m[i] == mine_id && p > tid ? p : kPairs);
+            }
         }
     }
-    if (wave < 2) {
-        const uint64_t lead = __ballot(tid < P && first == tid);
-        // wave 1 counts wave 0's leaders through LDS below
-        if (lane == 0) lead_id[kPairs - 1 - wave] = __builtin_popcountll(lead);
-        if (tid < P && first == tid) lead_pos[tid] = __builtin_popcountll(lead & ((1ull << lane) - 1));
-    }
+    const bool starts = mine_id >= 0 && (rank & 1) == 0;
+    const uint64_t starting = __ballot(starts);
+    if (wave < 2 && lane == 0) count[wave] = __builtin_popcountll(starting);
     __syncthreads();
-    const int c0 = lead_id[kPairs - 1], c1 = lead_id[kPairs - 2];
-    __syncthreads();
-    if (tid < P && first >= 0) {
-        const int pos = lead_pos[first] + (first >= 64 ? c0 : 0);
-        if (first == tid) lead_id[pos] = ids[tid];
-        if (first_tok == tid) tok_pair[pos][tid / a.k] = (int16_t)tid;
-    }
-    if (tid == 0) n_lead = c0 + c1;
+    if (starts)
+        entry[(wave ? count[0] : 0) + __builtin_popcountll(starting & ((1ull << lane) - 1))] =
+            make_int4(mine_id, tid, mate < kPairs ? mate : -1, tid / a.k | (mate < kPairs ? mate / a.k : 0) << 8);
+    const int entries = __builtin_amdgcn_readfirstlane(count[0] + count[1]);
     __syncthreads();
 
     const int j = lane & 15, g = lane >> 4;
     const bool upper = j >= 8;
-    const int r = (int)blockIdx.x * ROWS + (j & (ROWS - 1));
+    const int r = (int)blockIdx.x * 8 + (j & 7);
     const uint64_t row_off = (uint64_t)(r < a.M ? r : a.M - 1) * a.down_pitch;
     const int code_bytes = F::BB * a.nb2;
-    const int items = __builtin_amdgcn_readfirstlane(n_lead) * a.steps2;
-    const int part = (j & 3) < 2 ? (j & 3) : 2;
+    const int items = entries * a.steps2;
+    const int last_q = (a.nb2 - 1) / QB;
     const __amdgpu_buffer_rsrc_t hres = __builtin_amdgcn_make_buffer_rsrc(
         a.h, 0, (int)((uint32_t)P * (uint32_t)a.h_pair), BUFFER_FLAGS);
-    auto quantum = [&](int p) { return HALF ? 2 * p + (upper ? 1 : 0) : p; };
-    auto whole = [&](int p) { return (p + 1) * SB <= a.nb2; };
-    auto load = [&](Quantum<WT, SS, QU> &z, int i) {
-        const int li = i / a.steps2, p = i - li * a.steps2;
-        const uint8_t *w = a.down + (uint64_t)__builtin_amdgcn_readfirstlane(lead_id[li]) * a.down_expert + row_off;
-        load_quantum<WT, SS, QU>(z, w, a.qoff2, code_bytes, quantum(p), g, whole(p));
+    constexpr int D = 3;
+    uint4 part[D][NA];
+    Quantum<WT, SS, QU> z[D];
+    // The wave takes items wave, wave + 16, ...: entry n, step p.  Two cursors
+    // follow them, one for the loads and one for the products.
+    struct Cursor {
+        int n, p;
     };
-    RowAcc<WT, HALF> acc[TG];
-    Quantum<WT, SS, QU> cur, nxt;
-    if (wave < items) load(cur, wave);
-    for (int i = wave; i < items; i += kWaves) {
-        if (i + kWaves < items) load(nxt, i + kWaves);
-        const int li = i / a.steps2, p = i - li * a.steps2;
-        const int blk0 = p * SB;
-        // one token group after the other (only those with a token of this
-        // expert): its fragments, blocks past the row and tokens without this
-        // expert as zeros
-#pragma unroll
-        for (int tg = 0; tg < TG; ++tg) {
-            const int pr = tok_pair[li][4 * tg + (j >> 2)];
-            if (__ballot(pr >= 0) == 0) continue;
-            const uint32_t off = (uint32_t)pr * (uint32_t)a.h_pair + (uint32_t)(64 * part + 16 * g);
-            rt_bf16x8 fr[SB];
-#pragma unroll
-            for (int s = 0; s < SB; ++s) {
-                // the block whose values this lane group feeds to instruction s
-                const int b = WT == W_MXFP4 ? blk0 + (s & ~3) + g : blk0 + s;
-                const uint32_t o = pr >= 0 && b < a.nb2 ? off + (uint32_t)(blk0 + s) * kImageBytes : OUT_OF_RANGE;
-                fr[s] = __builtin_bit_cast(rt_bf16x8, __builtin_amdgcn_raw_buffer_load_b128(hres, o, 0, 0));
-            }
-            RowAcc<WT, HALF> one[1] = {acc[tg]};
-            multiply_quantum<WT, SS, QU, 1, HALF>(cur, quantum(p), whole(p), a.nb2, g, upper, 1, one,
-                                                  [&](int, int h, int s) { return fr[h * QB + s]; });
-            acc[tg] = one[0];
+    const int steps2 = a.steps2 > 0 ? a.steps2 : 1;
+    const Cursor stride = {kWaves / steps2, kWaves % steps2};
+    auto advance = [&](Cursor &c) {
+        c.n += stride.n;
+        c.p += stride.p;
+        if (c.p >= steps2) {
+            c.p -= steps2;
+            ++c.n;
         }
-        cur = nxt;
-    }
+    };
+    Cursor loads = {wave / steps2, wave % steps2}, products = loads;
+    // the wave's next item: its activations, then its weights, both in flight
+    // (past the last item the last entry again, unused)
+    auto load = [&](auto d, int) {
+        const int n = loads.n < entries ? loads.n : entries - 1, p = loads.p;
+        advance(loads);
+        const int4 en = entry[n];
 #pragma unroll
-    for (int tg = 0; tg < TG; ++tg) red[wave][tg][lane] = row_total(acc[tg], upper);
+        for (int k = 0; k < NA; ++k) {
+            const int at = 1024 * k + 16 * lane;             // within the two tokens' chunks
+            const int tok = at >= CHUNK ? 1 : 0;
+            const uint32_t off = (uint32_t)(p * CHUNK + at - tok * CHUNK);
+            const int pr = tok ? en.z : en.y;
+            const bool in = pr >= 0 && at < 2 * CHUNK && off < (uint32_t)a.h_pair;
+            part[d.value][k] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                hres, in ? (uint32_t)pr * (uint32_t)a.h_pair + off : OUT_OF_RANGE, 0, 0));
+        }
+        const uint8_t *w = a.down + (uint64_t)__builtin_amdgcn_readfirstlane(en.x) * a.down_expert + row_off;
+        load_quantum<WT, SS, QU>(z[d.value], w, w, a.qoff2, code_bytes, 2 * p + (upper ? 1 : 0), last_q, g, upper);
+    };
+    const uint32_t frag_off = (uint32_t)((j >> 2 & 1) * TOK_LDS + (j >> 3) * HALF_LDS + ((j & 3) < 2 ? (j & 3) : 2) * 64 + 16 * g);
+    uint8_t *const mine = parts[wave];
+    const int share = wave < items ? (items - wave + kWaves - 1) / kWaves : 0;
+    if (items > 0) stream_begin<0, D>(share, load);
+    stream<D>(share, load, [&](auto d, int) {
+        // this item's parts to their lanes (the wave's own LDS: its reads and
+        // writes stay in order)
+#pragma unroll
+        for (int k = 0; k < NA; ++k) {
+            const int at = 1024 * k + 16 * lane, tok = at >= CHUNK ? 1 : 0, in = at - tok * CHUNK;
+            if (2 * CHUNK % 1024 == 0 || at < 2 * CHUNK)
+                *reinterpret_cast<uint4 *>(mine + tok * TOK_LDS + (in >= CHUNK / 2 ? HALF_LDS - CHUNK / 2 : 0) + in) = part[d.value][k];
+        }
+        const int p = products.p;
+        const int4 en = entry[products.n];
+        advance(products);
+        __builtin_amdgcn_wave_barrier();
+        RowAcc<WT, false> acc[1];
+        multiply_quantum<WT, SS, QU, 1, false>(z[d.value], 2 * p + (upper ? 1 : 0), (p + 1) * SB <= a.nb2, a.nb2, g, upper, 1, acc,
+                                               [&](int, int, int s) {
+            return *reinterpret_cast<const rt_bf16x8 *>(mine + (uint32_t)s * kImageBytes + frag_off);
+        });
+        __builtin_amdgcn_wave_barrier();
+        // D's diagonal quarters: pair g & 1, half g >> 1.  One pair after the
+        // other: both may be of one token.
+        const float total = row_total(acc[0], upper);
+        const bool mine_now = (g >> 1) == (j >> 3);
+        if (mine_now && (g & 1) == 0) sums[wave][en.w & 255][j] += total;
+        __builtin_amdgcn_wave_barrier();
+        if (mine_now && (g & 1) == 1 && en.z >= 0) sums[wave][en.w >> 8][j] += total;
+        __builtin_amdgcn_wave_barrier();
+    });
     __syncthreads();
-    if (tid < TG * 64) {
-        const int l = tid & 63, tg = tid >> 6, col = l & 15;
-        const int m = (int)blockIdx.x * ROWS + col, t = 4 * tg + (l >> 4);
-        if (col < ROWS && m < a.M && t < a.N) {
+    if (tid < 64) {
+        const int m = (int)blockIdx.x * 8 + (tid & 7), t = tid >> 3;
+        if (m < a.M && t < a.N) {
             float s = 0.0f;
-            for (int w = 0; w < kWaves; ++w) s += HALF ? red[w][tg][l] + red[w][tg][l + 8] : red[w][tg][l];
+            for (int w = 0; w < kWaves; ++w) s += sums[w][t][tid & 7] + sums[w][t][8 + (tid & 7)];
             a.y[(uint64_t)t * a.y_pitch + m] = s;
         }
     }
 }
 
 typedef void (*Kernel)(MoeArgs);
-template <int WT, int SS, int TG>
-void pick(int qu, bool half, Kernel *up, Kernel *down)
-{
-    *up = qu == 4 ? moe_up_kernel<WT, SS, 4, TG> : qu == 2 ? moe_up_kernel<WT, SS, 2, TG> : moe_up_kernel<WT, SS, 1, TG>;
-    *down = half ? moe_down_kernel<WT, SS, 1, TG, true> : moe_down_kernel<WT, SS, 2, TG, false>;
-}
 template <int WT, int SS>
-void pick(int qu, int tg, bool half, Kernel *up, Kernel *down)
+void pick(int qu, int depth, Kernel *up, Kernel *down)
 {
-    if (tg == 1) pick<WT, SS, 1>(qu, half, up, down);
-    else pick<WT, SS, 2>(qu, half, up, down);
+    // (with one or two quanta of a wave and pass there is nothing to load ahead)
+    *up = qu == 2 ? (depth >= 3 ? moe_up_kernel<WT, SS, 2, 3> : moe_up_kernel<WT, SS, 2, 2>)
+                  : (depth >= 3 ? moe_up_kernel<WT, SS, 1, 4> : moe_up_kernel<WT, SS, 1, 2>);
+    *down = moe_down_kernel<WT, SS, kDownUnits>;
 }
 
 }  // namespace
@@ -463,23 +484,23 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
     a.nb2 = (int32_t)(F / 32);
     a.qoff2 = (int32_t)quant_offset(F, down.w.scale_shift);
     const int64_t units1 = (gate.w.K + kpu - 1) / kpu, units2 = (F + kpu - 1) / kpu;
-    // about how many experts several tokens choose between them
-    const int64_t experts = N < 2 ? k : N * k / 2 + 1 < gate.E ? N * k / 2 + 1 : gate.E;
-    const int tg = N > 4 ? 2 : 1;
-    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * experts, 0, (int)N);
+    // about how many experts the tokens choose between them, each k of E
+    double untouched = 1.0;
+    for (int64_t n = 0; n < N; ++n) untouched *= k < gate.E ? 1.0 - (double)k / (double)gate.E : 0.0;
+    const int64_t experts = (int64_t)((double)gate.E * (1.0 - untouched) + 1.0);
+    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * experts, 0, (int)(N * k < 2 ? 1 : 2), 1);
     a.steps1 = p.steps;
     a.s_log2 = p.s_log2;
     a.image = p.image;
     const int T = p.waves >> p.s_log2;
-    const int lds = p.waves * tg * 64 * 4 + p.image;
-    // tiles of eight output rows while sixteen would leave CUs without one
-    const bool half = (M + 15) / 16 < 2 * (int64_t)device_cus();
-    a.steps2 = (int32_t)((units2 + 1) / 2);
+    const int lds = p.waves * 64 * 4 + p.image;
+    a.steps2 = (int32_t)((units2 + 2 * kDownUnits - 1) / (2 * kDownUnits));
 
+    const int depth = (p.steps + (1 << p.s_log2) - 1) >> p.s_log2;
     Kernel ku = nullptr, kd = nullptr;
-    if (type == W_MXFP4) pick<W_MXFP4, 0>(p.qu, tg, half, &ku, &kd);
-    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(p.qu, tg, half, &ku, &kd) : pick<W_Q4_0, 0>(p.qu, tg, half, &ku, &kd);
-    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(p.qu, tg, half, &ku, &kd) : pick<W_Q8_0, 0>(p.qu, tg, half, &ku, &kd);
+    if (type == W_MXFP4) pick<W_MXFP4, 0>(p.qu, depth, &ku, &kd);
+    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(p.qu, depth, &ku, &kd) : pick<W_Q4_0, 0>(p.qu, depth, &ku, &kd);
+    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(p.qu, depth, &ku, &kd) : pick<W_Q8_0, 0>(p.qu, depth, &ku, &kd);
     else return hipErrorInvalidValue;
     hipError_t e = hipSuccess;
     if (F > 0) {
@@ -490,8 +511,7 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const unsigned tiles = (unsigned)(half ? (M + 7) / 8 : (M + 15) / 16);
-    hipLaunchKernelGGL(kd, dim3(tiles), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(kd, dim3((unsigned)((M + 7) / 8)), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -12,11 +12,11 @@
 //    top 16 bits of what is left, the rest); matrix row 4 t + p carries part p
 //    of token t (p = 3 is not used: such rows repeat part 2 and their sums
 //    are never read).  Products of two 8-bit significands are exact.
-//  * B, weights.  Row j of a tile is matrix column j.  A lane loads 16 bytes
+//  * B, weights.  Row j of a tile is matrix column j.  A lane holds 16 bytes
 //    of its row, so the four lane groups g = lane / 16 cover one 64-byte
 //    unit of the row (four 32-blocks of 4-bit codes, or two of 8-bit ones)
-//    with one 128-bit load, and the unit is used up by four (or two) matrix
-//    instructions:
+//    in one 128-bit register each, and the unit is used up by four (or two)
+//    matrix instructions:
 //     - MXFP4: instruction i takes dword i of every lane: eight values of block
 //       4 u + g from lane group g.  Scale and value convert to bf16 together,
 //       exactly (v_cvt_scalef32_pk_bf16_fp4), so sums run through whole rows.
@@ -32,6 +32,8 @@
 
 #include "qmm_internal.h"
 
+#include <type_traits>
+
 namespace qmm {
 
 typedef __bf16 rt_bf16x8 __attribute__((ext_vector_type(8)));
@@ -40,6 +42,16 @@ typedef float rt_f32x4 __attribute__((ext_vector_type(4)));
 typedef float rt_f32x2 __attribute__((ext_vector_type(2)));
 // four floats at any 4-byte aligned address
 typedef float rt_f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// Calls f(std::integral_constant<int, 0>{}) .. f(std::integral_constant<int, N-1>{}).
+template <int N, int I = 0, class F>
+__device__ inline void static_steps(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_steps<N, I + 1>(f);
+    }
+}
 
 constexpr int kTileCols = 16;          // weight rows per tile
 constexpr int kImageBytes = 192;       // activation parts of one token and 32-block
@@ -85,26 +97,23 @@ __device__ inline int run1(int q)
 }
 
 // The exact three-way split of eight values (in matrix order) into bf16
-// parts.  An infinity keeps its value in the first part (the others zero), a
-// NaN stays one.
+// parts: the upper 16 bits, the upper 16 bits of the remainder, and the rest
+// (eight significant bits each).  An infinity is its own first part; a NaN's
+// remainder is a NaN.
 __device__ inline void split_parts(const float (&v)[8], uint4 (&part)[3])
 {
-    uint32_t hi[8], mid[8], lo[8];
+    // the upper halves of two dwords side by side
+    auto pk = [](float a, float b) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    };
+    auto upper = [](float x) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u); };
+    float mid[8], lo[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __builtin_bit_cast(uint32_t, v[i]);
-        const bool special = (u & 0x7F800000u) == 0x7F800000u;
-        const uint32_t h = (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x7FC00000u : u & 0xFFFF0000u;
-        float r = v[i] - __builtin_bit_cast(float, u & 0xFFFF0000u);
-        r = special ? 0.0f : r;
-        const uint32_t m = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
-        hi[i] = h;
-        mid[i] = m;
-        lo[i] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, m));
+        mid[i] = fabsf(v[i]) == INFINITY ? 0.0f : v[i] - upper(v[i]);
+        lo[i] = mid[i] - upper(mid[i]);
     }
-    // the upper halves of two dwords side by side
-    auto pk = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
-    part[0] = make_uint4(pk(hi[0], hi[1]), pk(hi[2], hi[3]), pk(hi[4], hi[5]), pk(hi[6], hi[7]));
+    part[0] = make_uint4(pk(v[0], v[1]), pk(v[2], v[3]), pk(v[4], v[5]), pk(v[6], v[7]));
     part[1] = make_uint4(pk(mid[0], mid[1]), pk(mid[2], mid[3]), pk(mid[4], mid[5]), pk(mid[6], mid[7]));
     part[2] = make_uint4(pk(lo[0], lo[1]), pk(lo[2], lo[3]), pk(lo[4], lo[5]), pk(lo[6], lo[7]));
 }
@@ -125,30 +134,82 @@ __device__ inline void matrix_order(const rt_f32x4 a, const rt_f32x4 b, float (&
     }
 }
 
-// Fills the LDS image of blocks [b0, b0 + nblk) of `ntok` tokens with all
-// `threads` threads; blocks from nb on are zeros.  row(t) is token t's row.
-template <int WT, class Row>
-__device__ inline void build_image(uint8_t *img, int ntok, int b0, int nblk, int nb, int threads, Row row)
-{
-    const int per_tok = 4 * nblk;
-    for (int t = 0; t < ntok; ++t) {
-        const float *x = row(t);
-        for (int i = threadIdx.x; i < per_tok; i += threads) {
-            const int b = i >> 2, q = i & 3;
-            rt_f32x4 r0 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
-            if (b0 + b < nb) {
-                const float *p = x + (int64_t)(b0 + b) * 32;
-                r0 = *reinterpret_cast<const rt_f32x4u *>(p + run0<WT>(q));
-                r1 = *reinterpret_cast<const rt_f32x4u *>(p + run1<WT>(q));
-            }
-            float v[8];
-            matrix_order<WT>(r0, r1, v);
-            uint4 part[3];
-            split_parts(v, part);
-            uint8_t *dst = img + (image_step<WT>(b, q) * ntok + t) * kImageBytes + 16 * image_group<WT>(b, q);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(dst + 64 * p) = part[p];
+// The LDS image of blocks [b0, b0 + nblk) of `ntok` tokens, filled by all
+// `threads` threads in pieces of eight values; blocks from nb on are zeros.
+// row(t) is token t's row.  A thread's first two pieces are loaded ahead of the
+// workgroup's first weights (AHEAD: image_ahead, then build_image), since loads
+// complete in order; the weights that follow the first quantum are asked for
+// after the conversion, because the memory takes them only as fast as it
+// delivers, and a wave waiting to issue loads converts nothing.
+struct ImageAhead {
+    rt_f32x4 r[2][2];
+};
+// Piece i as (token, piece of the token): tokens are few, so no division.
+struct ImagePiece {
+    int t, i;
+    __device__ inline void settle(int per_tok)
+    {
+#pragma nounroll
+        while (i >= per_tok) {
+            i -= per_tok;
+            ++t;
         }
+    }
+};
+template <int WT, class Row>
+__device__ inline void image_load(const ImagePiece &p, int ntok, int b0, int nb, Row row, rt_f32x4 &r0, rt_f32x4 &r1)
+{
+    const int b = b0 + (p.i >> 2), q = p.i & 3;
+    r0 = r1 = rt_f32x4{0, 0, 0, 0};
+    if (p.t < ntok && b < nb) {
+        const float *x = row(p.t) + (int64_t)b * 32;
+        r0 = *reinterpret_cast<const rt_f32x4u *>(x + run0<WT>(q));
+        r1 = *reinterpret_cast<const rt_f32x4u *>(x + run1<WT>(q));
+    }
+}
+template <int WT, class Row>
+__device__ inline void image_ahead(ImageAhead &a, int ntok, int b0, int nblk, int nb, int threads, Row row)
+{
+    ImagePiece p = {0, (int)threadIdx.x};
+#pragma unroll
+    for (int n = 0; n < 2; ++n, p.i += threads) {
+        p.settle(4 * nblk);
+        image_load<WT>(p, ntok, b0, nb, row, a.r[n][0], a.r[n][1]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int WT, bool AHEAD, class Row>
+__device__ inline void build_image(uint8_t *img, int ntok, int b0, int nblk, int nb, int threads, Row row,
+                                   const ImageAhead &ahead)
+{
+    auto put = [&](const ImagePiece &p, const rt_f32x4 r0, const rt_f32x4 r1) {
+        const int b = p.i >> 2, q = p.i & 3;
+        float v[8];
+        matrix_order<WT>(r0, r1, v);
+        uint4 part[3];
+        split_parts(v, part);
+        uint8_t *dst = img + (image_step<WT>(b, q) * ntok + p.t) * kImageBytes + 16 * image_group<WT>(b, q);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(dst + 64 * k) = part[k];
+    };
+    ImagePiece p = {0, (int)threadIdx.x};
+    p.settle(4 * nblk);
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (p.t < ntok) put(p, ahead.r[n][0], ahead.r[n][1]);
+            __builtin_amdgcn_sched_barrier(0);     // one after the other: fewer registers
+            p.i += threads;
+            p.settle(4 * nblk);
+        }
+    }
+#pragma nounroll
+    while (p.t < ntok) {
+        rt_f32x4 r0, r1;
+        image_load<WT>(p, ntok, b0, nb, row, r0, r1);
+        put(p, r0, r1);
+        p.i += threads;
+        p.settle(4 * nblk);
     }
 }
 
@@ -180,32 +241,34 @@ typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
 
 typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
 
-// Loads quantum qi of the packed row at `row` (both this lane's).  Every
-// address lies inside the row: what lies past its end repeats its first bytes
-// (the activations there are zeros and multiply_quantum zeroes the scales),
-// and the scale bytes of a quantum with any block of the row end at or before
-// the row's end, because the row's codes follow its scales.  whole: every
-// lane's quantum lies wholly in its row (uniform).  The weights stream past
-// the caches; the scales share cache lines with neighbouring quanta.
+// Loads quantum qi.  With one unit a lane reads 16 bytes of its own row, `row0`
+// (64 bytes of each row per load).  With two, the first load takes both units
+// (128 bytes, the cache line's size) of the tile's first eight rows and the
+// second those of the other eight: columns j and j + 8 read the halves of one
+// row, row0 in the first load and row1 in the second, and pair_units hands each
+// lane its own row afterwards.  (Sixteen rows 64 bytes at a time leave half of
+// each cache line's fill to a later load, and the L1 holds few enough lines
+// for that to halve the bytes in flight.)
+//
+// Always the same loads in the same order, whatever the row's length: a
+// branch around a load would make the compiler wait for every load in flight,
+// the next quantum's among them.  Every address lies inside the row: units
+// past its end repeat its last 16 bytes and a quantum past it the scales of
+// its last (last_q; the activations there are zeros and multiply_quantum
+// zeroes the scales), and the scale bytes of a quantum with any block of the
+// row end at or before the row's end, because the row's codes follow its
+// scales.
 template <int WT, int SS, int QU>
-__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int g,
-                                    bool whole)
+__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row0, const uint8_t *row1, int qoff, int code_bytes,
+                                    int qi, int last_q, int g, bool upper)
 {
+    static_assert(QU == 1 || QU == 2, "one or two units");
     constexpr int SB = Quantum<WT, SS, QU>::SB;
-    const int c0 = 64 * QU * qi + 16 * g;
-    const uint8_t *codes = row + qoff;
-    auto load16 = [](const uint8_t *p) {
-        return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const rt_u32x4 *>(p)));
-    };
-    const uint8_t *s = row + SB * qi;
-    if (whole) {
-#pragma unroll
-        for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + c0 + 64 * i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < QU; ++i) z.q[i] = load16(codes + (c0 + 64 * i < code_bytes ? c0 + 64 * i : 0));
-        s = 64 * QU * qi < code_bytes ? s : row;
-    }
+    const int c = 64 * QU * qi + (QU == 2 && upper ? 64 : 0) + 16 * g, top = code_bytes - 16;
+    const uint32_t at = (uint32_t)(qoff + (c < top ? c : top));
+    z.q[0] = *reinterpret_cast<const uint4 *>(row0 + at);
+    if constexpr (QU == 2) z.q[1] = *reinterpret_cast<const uint4 *>(row1 + at);
+    const uint8_t *s = (QU == 2 && upper ? row1 : row0) + (uint32_t)(SB * (qi < last_q ? qi : last_q));
     if constexpr (SB == 2) {
         z.s[0] = *reinterpret_cast<const uint16_t *>(s);
     } else if constexpr (SB == 4) {
@@ -225,6 +288,24 @@ __device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row, 
             z.s[4 * i + 3] = v.w;
         }
     }
+}
+
+// The units of a lane's own row from the two loads of load_quantum: columns
+// 8 .. 15 of the first and 0 .. 7 of the second hold each other's (one DPP
+// rotation by eight lanes per dword, written to half the columns).
+template <int WT, int SS>
+__device__ inline void pair_units(Quantum<WT, SS, 2> &z)
+{
+    uint32_t a[4] = {z.q[0].x, z.q[0].y, z.q[0].z, z.q[0].w}, b[4] = {z.q[1].x, z.q[1].y, z.q[1].z, z.q[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int lo = __builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);
+        const int hi = __builtin_amdgcn_update_dpp((int)b[i], (int)a[i], 0x128, 0xF, 0x3, false);
+        a[i] = (uint32_t)lo;
+        b[i] = (uint32_t)hi;
+    }
+    z.q[0] = make_uint4(a[0], a[1], a[2], a[3]);
+    z.q[1] = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // The sum of a lane's row and token over the instructions so far.  MXFP4 keeps
@@ -270,9 +351,29 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool who
 {
     using F = RowFmt<WT, SS>;
     constexpr int H = HALF ? 2 : 1;
+    if constexpr (QU == 2) pair_units<WT, SS>(z);
     const int left = whole ? QU * F::MF : nb - qi * QU * F::MF;      // blocks of this quantum in the row
+    // A unit's fragments are read while the unit before is multiplied (with
+    // two token groups, at its start: the registers hold one unit's).
+    constexpr int NF = F::MF * TG * H;
+    constexpr int BUFS = NF <= 4 && QU > 1 ? 2 : 1;
+    rt_bf16x8 fr[BUFS][TG][H][F::MF];
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int t = 0; t < F::MF; ++t)
+#pragma unroll
+            for (int tg = 0; tg < TG; ++tg)
+                if (tg < groups) {
+#pragma unroll
+                    for (int h = 0; h < H; ++h) fr[i % BUFS][tg][h][t] = frag(tg, h, F::MF * i + t);
+                }
+    };
+    if constexpr (BUFS == 2) fetch(0);
 #pragma unroll
     for (int i = 0; i < QU; ++i) {
+        if constexpr (BUFS == 1) fetch(i);
+        else if (i + 1 < QU) fetch(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
         uint32_t d[4] = {z.q[i].x, z.q[i].y, z.q[i].z, z.q[i].w};
         if constexpr (WT == W_MXFP4) {
             // lane group g holds block 4 i + g of the quantum: its scale byte
@@ -293,7 +394,7 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool who
                     if (tg < groups) {
 #pragma unroll
                         for (int h = 0; h < H; ++h)
-                            acc[tg].c[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, h, 4 * i + t), b, acc[tg].c[h], 0, 0, 0);
+                            acc[tg].c[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][h][t], b, acc[tg].c[h], 0, 0, 0);
                     }
             }
         } else {
@@ -329,10 +430,10 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool who
                 for (int tg = 0; tg < TG; ++tg)
                     if (tg < groups) {
                         const rt_f32x4 zero = {0, 0, 0, 0};
-                        const rt_f32x4 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 0, blk), b, zero, 0, 0, 0);
+                        const rt_f32x4 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][0][t], b, zero, 0, 0, 0);
                         float sum = s0[0] + (s0[1] + s0[2]);
                         if constexpr (HALF) {
-                            const rt_f32x4 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(tg, 1, blk), b, zero, 0, 0, 0);
+                            const rt_f32x4 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][1][t], b, zero, 0, 0, 0);
                             const float other = s1[0] + (s1[1] + s1[2]);
                             sum = upper ? other : sum;
                         }
@@ -343,6 +444,39 @@ __device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool who
     }
 }
 
+// A wave's run over its n quanta (or items) 0 .. n - 1 with D of them in
+// registers: `stream_begin` loads the first D, `stream` multiplies each and
+// loads the one D later into its place.  The places are fixed at compile time:
+// moving a loaded register would wait for its load, so that only one quantum
+// were ever in flight.  load(d, i)
+// fills place d; use(d, i) consumes it.  Past the end the last one is loaded
+// again (from the caches), so that every load is unconditional: a place loaded
+// on one of two paths would be copied where they meet, and waited for there.
+template <int FROM, int TO, class Load>
+__device__ inline void stream_begin(int n, Load load)
+{
+    static_steps<TO - FROM>([&](auto i) {
+        constexpr int d = FROM + decltype(i)::value;
+        load(std::integral_constant<int, d>{}, d < n ? d : n > 0 ? n - 1 : 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int D, class Load, class Use>
+__device__ inline void stream(int n, Load load, Use use)
+{
+    int i = 0;
+    for (; n - i > D; i += D)
+        static_steps<D>([&](auto d) {
+            const int k = i + (int)d.value;
+            use(d, k);
+            __builtin_amdgcn_sched_barrier(0);
+            load(d, k + D < n ? k + D : n - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    static_steps<D>([&](auto d) {
+        if (i + (int)d.value < n) use(d, i + (int)d.value);
+    });
+}
 // Swish(z) = z * sigma(z) = z / (1 + e^{-z}) in binary32; for z far below
 // zero e^{-z} overflows and the quotient is the limit -0.
 __device__ inline float rt_swish(float z)
@@ -352,7 +486,7 @@ __device__ inline float rt_swish(float z)
 
 // ---- host: how a launch splits its rows ----
 struct RowPlan {
-    int qu;          // units per quantum (1, 2, 4)
+    int qu;          // units per quantum (1, 2)
     int half;        // tiles of eight rows (HALF)
     int s_log2;      // log2 of the waves that share a tile
     int waves;       // per workgroup
@@ -363,23 +497,27 @@ struct RowPlan {
 
 // units: 64-byte units per row, mf: blocks per unit; tiles: tiles of the
 // launch; half_tiles: their number with eight rows each (0: not available);
-// tokens: the most tokens one image holds.
+// tokens: the most tokens one image holds at once; likely: how many it will hold
+// as a rule.
 //
-// Sixteen waves on every CU keep enough loads in flight to stream at the
-// memory's rate, so a launch aims at that many (tile, wave) tasks, with as few
-// waves sharing a tile and as large quanta (one scale load per QU code loads)
-// as still give them.  Workgroups are small (four waves) while their image is,
-// so that several share a CU and one's loads run beside another's setup; with
-// more tokens a larger workgroup shares one image.
-inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens)
+// About ten waves on every CU, each with three or four quanta in flight, stream
+// at the memory's rate, so a launch aims at that many (tile, wave) tasks, with
+// as few waves sharing a tile and as large quanta (one scale load per QU code
+// loads) as still give them (two of eight Q4_0 experts of 5632 x 2048: 20.0 us
+// with two waves a tile, 22 with one or four).  Workgroups are small (four
+// waves) while their image is, so that several share a CU and one's loads run
+// beside another's setup; with more tokens a larger workgroup shares one
+// image.  (Eight-row tiles with larger quanta or two token groups need more
+// registers than sixteen waves a CU leave.)
+inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens, int likely)
 {
-    const int64_t target = 16 * (int64_t)device_cus();
+    const int64_t target = 10 * (int64_t)device_cus();
     RowPlan p = {1, 0, 0, 4, 0, 0, 0};
     auto steps_of = [&](int qu, int half) { return ((units + qu - 1) / qu + half) / (1 + half); };
     int64_t best = -1;
-    for (int half = 0; half <= (half_tiles ? 1 : 0) && best < target; ++half) {
+    for (int half = 0; half <= (half_tiles && tokens <= 4 ? 1 : 0) && best < target; ++half) {
         const int64_t t = half ? half_tiles : tiles;
-        for (int qu = 4; qu >= 1 && best < target; qu /= 2) {
+        for (int qu = half ? 1 : 2; qu >= 1 && best < target; qu /= 2) {
             int s = 0;
             while (s < 4 && t << s < target && (2 << s) <= steps_of(qu, half)) ++s;
             if (t << s > best) {
@@ -390,7 +528,7 @@ inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tile
             }
         }
     }
-    p.waves = tokens <= 2 ? 4 : tokens <= 4 ? 8 : 16;
+    p.waves = likely <= 2 ? 4 : likely <= 4 ? 8 : 16;
     if (p.waves < 1 << p.s_log2) p.waves = 1 << p.s_log2;
     auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : 112 * 1024; };
     // one step of every wave of a tile has to fit the image
