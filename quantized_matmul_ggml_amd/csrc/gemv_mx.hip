@@ -7,12 +7,14 @@
 // product is exact and only the binary32 accumulation rounds.
 //
 // Work split: a workgroup of W waves covers W / S tiles of 16 weight rows, S
-// waves sharing a tile's K in interleaved quanta of QU units (128 QU values of
-// k, 64 QU code bytes of each row); where that leaves the chip idle a tile has
-// eight rows and a wave takes two quanta of each at once (HALF, row_tiles.h).
-// The first quanta of every wave are in flight while the workgroup splits its
-// tokens into the LDS image, and those of its next tile while the S partial
-// sums of this one meet in LDS, where they are added in wave order.
+// waves sharing a tile's K, one run of 64-byte units each; where that leaves
+// the chip idle a tile has eight rows and a wave takes two units of each at
+// once (HALF, row_tiles.h).  The first units of every wave are in flight while
+// the workgroup splits its tokens into the LDS image, and those of its next
+// tile while the S partial sums of this one meet in LDS, where they are added
+// in wave order.
+//
+// 32000 x 2048, one token: 8.3 us for 34.8 MB (a bare read of them: 7.7).
 #include "row_tiles.h"
 
 namespace qmm {
@@ -38,18 +40,18 @@ struct MxArgs {
     int32_t N;
     int32_t nb;               // 32-blocks per row
     int32_t qoff;
-    int32_t steps;            // quanta (HALF: pairs of quanta) per row
+    int32_t steps;            // units (HALF: pairs of units) per row
     int32_t s_log2;           // waves per tile
     int32_t pass;             // steps per pass over K (a multiple of S, or all)
     int32_t pad[10];
     MxItem item[QMM_GEMV_BATCH_MAX];
 };
 
-template <int QU, int TG, bool SW, bool HALF, int D>
+template <int TG, bool SW, bool HALF, int D>
 __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
 {
     constexpr int WT = W_MXFP4, SS = 0;
-    constexpr int QB = QU * RowFmt<WT, SS>::MF;            // blocks (and instructions) per quantum
+    constexpr int QB = RowFmt<WT, SS>::MF;                 // blocks (and instructions) per unit
     constexpr int SB = QB * (HALF ? 2 : 1);                // per step
     constexpr int ROWS = SW || HALF ? 8 : 16;              // row indices per tile
     static_assert(!(SW && HALF), "a fused tile has its two matrices in the halves");
@@ -72,29 +74,36 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
     const int S = 1 << s_log2, T = waves >> s_log2;
     const int split = wave & (S - 1), tile_in = wave >> s_log2;
     float *const red = reinterpret_cast<float *>(lds);     // [2][waves][TG][64]
-    uint8_t *const img = lds + 2 * waves * TG * 64 * 4;
+    uint8_t *const scales = lds + 2 * waves * TG * 64 * 4 + wave * kScaleLds;
+    uint8_t *const img = lds + waves * (2 * TG * 64 * 4 + kScaleLds);
 
     // ---- the rows of a tile: columns of the gate or up matrix; rows past M
     // repeat the last one and are not stored ----
-    const int last_q = (nb - 1) / QB;
-    auto quantum = [&](int p) { return HALF ? 2 * p + (upper ? 1 : 0) : p; };
+    auto unit = [&](int p) { return HALF ? 2 * p + (upper ? 1 : 0) : p; };
     auto whole = [&](int p) { return (p + 1) * SB <= nb; };
-    Quantum<WT, SS, QU> z[D];
-    // the wave's k-th quantum from step p0 of tile group grp on
-    auto load = [&](int grp, int p0) {
-        return [&, grp, p0](auto d, int k) {
-            // load_quantum's two rows: with one unit the lane's own (HALF:
-            // the row its half is of), with two rows j % 8 of both halves
-            auto at = [&](const uint8_t *base, uint32_t step, int64_t r) { return base + (uint64_t)(r < M ? r : M - 1) * step; };
-            const int64_t r = (int64_t)(grp * T + tile_in) * ROWS + (j & 7);
-            const bool own = QU == 1 && !HALF && upper;
-            const uint8_t *row0 = SW && own ? at(W2, pitch2, r) : at(W, pitch, !SW && own ? r + 8 : r);
-            const uint8_t *row1 = QU == 1 ? row0 : SW ? at(W2, pitch2, r) : at(W, pitch, r + 8);
-            load_quantum<WT, SS, QU>(z[d.value], row0, row1, qoff, 16 * nb, quantum(p0 + split + k * S), last_q, g, upper);
-        };
+    Unit<WT, SS> z[D];
+    ScaleWindow<WT, SS, HALF, D> window;
+    // The wave's run of steps in a pass of len steps from p0 on: its first, and
+    // their number.
+    auto per_wave = [&](int len) { return (len + S - 1) >> s_log2; };
+    auto first = [&](int p0, int len) { return p0 + split * per_wave(len); };
+    auto share = [&](int len) {
+        const int left = len - split * per_wave(len);
+        return left < 0 ? 0 : left < per_wave(len) ? left : per_wave(len);
     };
-    // its quanta in [p0, p1)
-    auto share = [&](int p0, int p1) { return p0 + split < p1 ? (p1 - p0 - split + S - 1) >> s_log2 : 0; };
+    auto pass_len = [&](int p0) { return p0 + pass < steps ? pass : steps - p0; };
+    // the lane's row of a tile (HALF: columns j and j + 8 are halves of one)
+    auto tile_row = [&](int grp) {
+        const int64_t r = (int64_t)(grp * T + tile_in) * ROWS + (ROWS == 8 ? j & 7 : j);
+        return (SW && upper ? W2 : W) + (uint64_t)(r < M ? r : M - 1) * (SW && upper ? pitch2 : pitch);
+    };
+    auto load = [&](const uint8_t *r, int from) {
+        return [&, r, from](auto d, int k) { load_codes<WT, SS>(z[d.value], r, qoff, 16 * nb, unit(from + k), g); };
+    };
+    auto load_scales = [&](const uint8_t *r, int p) {
+        window.load(r, qoff + 16 * nb, p, g, upper);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     // ---- activation fragments: matrix row 4 t + p is part p of token t ----
     uint32_t frag_off[TG];
 #pragma unroll
@@ -108,38 +117,47 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
     auto row = [&](int t) { return X + (uint64_t)t * x_pitch; };
     int grp = blockIdx.x;
     ImageAhead ahead;
-    const int p_end = pass < steps ? pass : steps;
     if (steps > 0) {
-        image_ahead<WT>(ahead, N, 0, p_end * SB, nb, threads, row);
-        stream_begin<0, 1>(share(0, p_end), load(grp, 0));
+        const int len = pass_len(0), from = first(0, len);
+        const uint8_t *const r = tile_row(grp);
+        image_ahead<WT>(ahead, N, 0, len * SB, nb, threads, row);
+        load_scales(r, from);
+        stream_begin<0, 1>(share(len), load(r, from));
+        build_image<WT, true>(img, N, 0, len * SB, nb, threads, row, ahead);
+        stream_begin<1, D>(share(len), load(r, from));
+        __syncthreads();
     }
     int parity = 0;
-    bool built = false;
-    for (; grp < n_groups; grp += wgs, parity ^= 1) {
+    for (const int grp0 = grp; grp < n_groups; grp += wgs, parity ^= 1) {
         RowAcc<WT, HALF> acc[TG];
-        for (int p0 = 0; p0 < steps; p0 += pass) {
-            const int p1 = p0 + pass < steps ? p0 + pass : steps;
-            if (!built || pass < steps) {
-                if (built) {
-                    __syncthreads();               // the last pass's image is no longer read
-                    build_image<WT, false>(img, N, p0 * SB, (p1 - p0) * SB, nb, threads, row, ahead);
-                } else {
-                    build_image<WT, true>(img, N, p0 * SB, (p1 - p0) * SB, nb, threads, row, ahead);
-                    stream_begin<1, D>(share(p0, p1), load(grp, p0));
-                }
-                built = true;
+        for (int p0 = 0, p1; p0 < steps; p0 = p1) {
+            const int len = pass_len(p0), from = first(p0, len);
+            p1 = p0 + len;
+            if (pass < steps && (grp > grp0 || p0 > 0)) {
+                __syncthreads();                   // the last pass's image is no longer read
+                build_image<WT, false>(img, N, p0 * SB, len * SB, nb, threads, row, ahead);
                 __syncthreads();
             }
-            stream<D>(share(p0, p1), load(grp, p0), [&](auto d, int k) {
-                const int p = p0 + split + k * S;
+            const uint8_t *const r = tile_row(grp);
+            stream<D>(share(len), [&](auto more, int i) {
+                window.put(scales, j, g);
+                if constexpr (more.value) load_scales(r, from + i);
+            }, load(r, from), [&](auto d, int k) {
+                const int p = from + k;
                 const uint8_t *base = img + (uint32_t)((p - p0) * SB) * block_bytes;
-                multiply_quantum<WT, SS, QU, TG, HALF>(z[d.value], quantum(p), whole(p), nb, g, upper, TG, acc,
+                window.get(z[d.value], scales, d.value, j);
+                multiply_unit<WT, SS, TG, HALF>(z[d.value], unit(p), whole(p), nb, g, upper, TG, acc,
                                                        [&](int tg, int h, int step) {
                     return *reinterpret_cast<const rt_bf16x8 *>(base + (uint32_t)(h * QB + step) * block_bytes + frag_off[tg]);
                 });
             });
-            const int next = p1 < steps ? p1 : 0, next_end = next + pass < steps ? next + pass : steps;
-            stream_begin<0, D>(share(next, next_end), load(p1 < steps ? grp : grp + wgs, next));
+            const bool same = p1 < steps;
+            if (same || grp + wgs < n_groups) {
+                const int p = same ? p1 : 0, next_len = pass_len(p), next = first(p, next_len);
+                const uint8_t *const n = tile_row(same ? grp : grp + wgs);
+                load_scales(n, next);
+                stream_begin<0, D>(share(next_len), load(n, next));
+            }
         }
         float *const mine = red + parity * waves * TG * 64;
 #pragma unroll
@@ -163,19 +181,17 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
 }
 
 typedef void (*Kernel)(MxArgs);
-// depth: quanta of one wave and pass over K; with one or two there is nothing to
+// depth: units of one wave and pass over K; with one or two there is nothing to
 // load ahead.
-template <int QU, int TG, bool SW, bool HALF>
-Kernel pick_depth(int depth)
+template <int TG, bool SW, bool HALF>
+Kernel pick(int depth)
 {
-    constexpr int D = QU == 1 ? 4 : 3;
-    return depth >= 3 ? gemv_mx_kernel<QU, TG, SW, HALF, D>
-                      : depth == 2 ? gemv_mx_kernel<QU, TG, SW, HALF, 2> : gemv_mx_kernel<QU, TG, SW, HALF, 1>;
-}
-template <int TG, bool SW>
-Kernel pick(int qu, int depth)
-{
-    return qu == 2 ? pick_depth<2, TG, SW, false>(depth) : pick_depth<1, TG, SW, false>(depth);
+    if (depth <= 1) return gemv_mx_kernel<TG, SW, HALF, 1>;
+    if (depth == 2) return gemv_mx_kernel<TG, SW, HALF, 2>;
+    if constexpr (!HALF) {
+        if (depth > 4) return gemv_mx_kernel<TG, SW, HALF, 8>;
+    }
+    return gemv_mx_kernel<TG, SW, HALF, 4>;
 }
 
 hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStream_t stream)
@@ -197,7 +213,7 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
     a.steps = p.steps;
     a.s_log2 = p.s_log2;
     a.pass = pass_steps(p.image, p.step_bytes, (int)N, p.s_log2, p.steps);
-    const int lds = 2 * p.waves * tg * 64 * 4 + p.image;
+    const int lds = p.waves * (2 * tg * 64 * 4 + kScaleLds) + p.image;
     // as many workgroups as the CUs hold at once stream the tiles between them
     const int per_cu = 16 / p.waves;
     const int64_t cap = (int64_t)per_cu * device_cus();
@@ -226,10 +242,10 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
         if (wgs > widest) widest = wgs;
     }
     const int depth = (a.pass + (1 << p.s_log2) - 1) >> p.s_log2;
-    const Kernel k = p.half ? pick_depth<1, 1, false, true>(depth)
-                     : sw   ? (tg == 1 ? pick<1, true>(p.qu, depth) : pick<2, true>(p.qu, depth))
-                            : (tg == 1 ? pick<1, false>(p.qu, depth) : pick<2, false>(p.qu, depth));
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(k), 128 * 1024);
+    const Kernel k = p.half ? pick<1, false, true>(depth)
+                     : sw   ? (tg == 1 ? pick<1, true, false>(depth) : pick<2, true, false>(depth))
+                            : (tg == 1 ? pick<1, false, false>(depth) : pick<2, false, false>(depth));
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(k), 160 * 1024);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k, dim3((unsigned)widest, (unsigned)n), dim3(64 * p.waves), (unsigned)lds, stream, a);
     return hipGetLastError();

@@ -9,17 +9,18 @@
 //
 // For one to eight tokens the run time is the time to stream the chosen
 // experts' weights (A Complete Guide to llama.cpp and Customization with C++,
-// §2.1), so each chosen expert is read once, whatever the number of tokens
-// that share it, in two launches with the arithmetic of row_tiles.h:
+// §2.1), so tokens that share an expert share its reads, in two launches with
+// the arithmetic of row_tiles.h.  A pair is a (token, slot); an entry is an
+// expert and one or two of the pairs that name it.
 //
-//  * moe_up_kernel: grid (tile groups, pairs).  A pair is a (token, slot);
-//    the first pair that names an expert is its leader and does the work of
-//    all tokens that chose it, the workgroups of the others leave at once.
+//  * moe_up_kernel: grid (tile groups, pairs).  The first, third, ... pair that
+//    names an expert does the work of its entry, the workgroups of the others
+//    leave at once.
 //    h = Swish(gate) * up, times the token's weight for the expert (so that
 //    the second launch only adds), goes to the workspace as the three bf16
 //    parts of row_tiles.h, in the order the matrix instructions read them.
 //  * moe_down_kernel: one workgroup per 8 output rows.  Its sixteen waves share
-//    the quanta of all leaders' down rows; the weights are already in h, so the
+//    the units of all entries' down rows; the weights are already in h, so the
 //    experts' products only add up, in a fixed order: results do not depend
 //    on timing.
 #include "row_tiles.h"
@@ -29,7 +30,6 @@ namespace {
 
 constexpr int kWaves = 16;            // of moe_down_kernel's workgroups
 constexpr int kThreads = 64 * kWaves;
-constexpr int kDownUnits = 1;         // units per quantum of moe_down_kernel (its pair of quanta is 128 bytes of a row)
 constexpr int kPairs = QMM_MOE_MAX_TOKENS * QMM_MOE_MAX_TOP_K;
 static_assert(kPairs == 128, "two pairs per lane of a wave");
 
@@ -127,21 +127,21 @@ struct MoeArgs {
     int32_t E, N, k, F, M;    // M: output rows
     int32_t nb1, qoff1;       // gate / up rows: blocks, code offset
     int32_t nb2, qoff2;       // down rows
-    int32_t steps1;           // moe_up_kernel: quanta per row, waves per tile,
+    int32_t steps1;           // moe_up_kernel: units per row, waves per tile,
     int32_t s_log2;           //   LDS bytes of the image
     int32_t image;
-    int32_t steps2;           // moe_down_kernel: quanta (or pairs) per row
+    int32_t steps2;           // moe_down_kernel: pairs of units per row
 };
 
 // A workgroup takes T tiles of eight rows of one expert and one or two of its
 // pairs; an expert with more makes several, whose weights then come from the
 // caches (with four pairs a workgroup the few experts that have them needed
 // twice the LDS, took several passes over K, and finished last).
-template <int WT, int SS, int QU, int D>
+template <int WT, int SS, int D>
 __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
-    constexpr int QB = QU * F::MF;
+    constexpr int QB = F::MF;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const int lane = threadIdx.x & 63;
@@ -168,33 +168,47 @@ __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
     const int split = wave & (S - 1), tile_in = wave >> a.s_log2;
     const int grp = blockIdx.x;
     float *const red = reinterpret_cast<float *>(lds);     // [waves][64]
-    uint8_t *const img = lds + waves * 64 * 4;
+    uint8_t *const scales = lds + waves * 64 * 4 + wave * kScaleLds;
+    uint8_t *const img = lds + waves * (64 * 4 + kScaleLds);
 
-    // ---- the activations and the first quanta of weights ----
+    // ---- the activations and the first units of weights ----
     const bool upper = j >= 8;
     const int r = (grp * T + tile_in) * 8 + (j & 7), rc = r < a.F ? r : a.F - 1;
-    const uint8_t *const row_g = a.gate + (uint64_t)e * a.gate_expert + (uint64_t)rc * a.gate_pitch;
-    const uint8_t *const row_u = a.up + (uint64_t)e * a.up_expert + (uint64_t)rc * a.up_pitch;
-    const uint8_t *const row0 = QU == 1 && upper ? row_u : row_g;
+    const uint8_t *const row = upper ? a.up + (uint64_t)e * a.up_expert + (uint64_t)rc * a.up_pitch
+                                     : a.gate + (uint64_t)e * a.gate_expert + (uint64_t)rc * a.gate_pitch;
     const int code_bytes = F::BB * a.nb1;
-    const int last_q = (a.nb1 - 1) / QB;
     auto whole = [&](int q) { return (q + 1) * QB <= a.nb1; };
     const int pass = pass_steps(a.image, QB * kImageBytes, now, a.s_log2, a.steps1);
     const float *const x0 = a.x + (uint64_t)(pair / a.k) * a.x_pitch, *const x1 = a.x + (uint64_t)(mate / a.k) * a.x_pitch;
+    const float w0 = a.weights[pair], w1 = a.weights[mate];
     auto rows = [&](int place) { return place ? x1 : x0; };
     ImageAhead ahead;
-    Quantum<WT, SS, QU> z[D];
-    // the wave's k-th quantum from step q0 of the row on, and their number in
-    // [q0, q1)
-    auto load = [&](int q0) {
-        return [&, q0](auto d, int k) {
-            load_quantum<WT, SS, QU>(z[d.value], row0, row_u, a.qoff1, code_bytes, q0 + split + k * S, last_q, g, upper);
-        };
+    Unit<WT, SS> z[D];
+    ScaleWindow<WT, SS, false, D> window;
+    // The wave's run of units in a pass of len steps from q0 on: its first, and
+    // their number.
+    auto per_wave = [&](int len) { return (len + S - 1) >> a.s_log2; };
+    auto first = [&](int q0, int len) { return q0 + split * per_wave(len); };
+    auto share = [&](int len) {
+        const int left = len - split * per_wave(len);
+        return left < 0 ? 0 : left < per_wave(len) ? left : per_wave(len);
     };
-    auto share = [&](int q0, int q1) { return q0 + split < q1 ? (q1 - q0 - split + S - 1) >> a.s_log2 : 0; };
+    auto pass_len = [&](int q0) { return q0 + pass < a.steps1 ? pass : a.steps1 - q0; };
+    auto load = [&](int from) {
+        return [&, from](auto d, int k) { load_codes<WT, SS>(z[d.value], row, a.qoff1, code_bytes, from + k, g); };
+    };
+    auto load_scales = [&](int p) {
+        window.load(row, a.qoff1 + code_bytes, p, g, upper);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     if (a.steps1 > 0) {
-        image_ahead<WT>(ahead, now, 0, pass * QB, a.nb1, threads, rows);
-        stream_begin<0, D - 1>(share(0, pass), load(0));
+        const int len = pass_len(0), from = first(0, len);
+        image_ahead<WT>(ahead, now, 0, len * QB, a.nb1, threads, rows);
+        load_scales(from);
+        stream_begin<0, D - 1>(share(len), load(from));
+        build_image<WT, true>(img, now, 0, len * QB, a.nb1, threads, rows, ahead);
+        stream_begin<D - 1, D>(share(len), load(from));
+        __syncthreads();
     }
     // columns of the activations' operand: four each for two tokens, three
     // parts and the last again; with one token it stands in both
@@ -202,23 +216,28 @@ __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
     const uint32_t frag_off = (uint32_t)((j >> 2 & now - 1) * kImageBytes + ((j & 3) < 2 ? (j & 3) : 2) * 64 + 16 * g);
     RowAcc<WT, false> acc[1];
     for (int q0 = 0; q0 < a.steps1; q0 += pass) {
-        const int q1 = q0 + pass < a.steps1 ? q0 + pass : a.steps1;
-        if (q0 == 0) {
-            build_image<WT, true>(img, now, 0, q1 * QB, a.nb1, threads, rows, ahead);
-            stream_begin<D - 1, D>(share(0, q1), load(0));
-        } else {
+        const int len = pass_len(q0), from = first(q0, len);
+        if (q0 > 0) {
             __syncthreads();                       // the last image is no longer read
-            stream_begin<0, D>(share(q0, q1), load(q0));
-            build_image<WT, false>(img, now, q0 * QB, (q1 - q0) * QB, a.nb1, threads, rows, ahead);
+            build_image<WT, false>(img, now, q0 * QB, len * QB, a.nb1, threads, rows, ahead);
+            __syncthreads();
         }
-        __syncthreads();
-        stream<D>(share(q0, q1), load(q0), [&](auto d, int k) {
-            const int q = q0 + split + k * S;
+        stream<D>(share(len), [&](auto more, int i) {
+            window.put(scales, j, g);
+            if constexpr (more.value) load_scales(from + i);
+        }, load(from), [&](auto d, int k) {
+            const int q = from + k;
             const uint8_t *at = img + (uint32_t)((q - q0) * QB) * step_bytes + frag_off;
-            multiply_quantum<WT, SS, QU, 1, false>(z[d.value], q, whole(q), a.nb1, g, upper, 1, acc, [&](int, int, int step) {
+            window.get(z[d.value], scales, d.value, j);
+            multiply_unit<WT, SS, 1, false>(z[d.value], q, whole(q), a.nb1, g, upper, 1, acc, [&](int, int, int step) {
                 return *reinterpret_cast<const rt_bf16x8 *>(at + (uint32_t)step * step_bytes);
             });
         });
+        if (q0 + pass < a.steps1) {
+            const int next_len = pass_len(q0 + pass), next = first(q0 + pass, next_len);
+            load_scales(next);
+            stream_begin<0, D>(share(next_len), load(next));
+        }
     }
     red[wave * 64 + lane] = row_total(acc[0], upper);
     __syncthreads();
@@ -239,7 +258,7 @@ __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
                 s += part[64 * w];
                 u += part[64 * w + 8];
             }
-            hv = rt_swish(s) * u * a.weights[home];
+            hv = rt_swish(s) * u * (place ? w1 : w0);
         }
         // its place among the parts: block f / 32, element f % 32
         const int b = f >> 5, el = f & 31;
@@ -265,22 +284,23 @@ __global__ __launch_bounds__(1024) void moe_up_kernel(const MoeArgs a)
     }
 }
 
-// A tile is eight rows: columns 0 .. 7 of the matrix instruction hold quantum
-// 2 p of the rows, columns 8 .. 15 quantum 2 p + 1, and likewise matrix rows
-// 0 .. 7 the parts of two tokens' activations of quantum 2 p and rows 8 .. 15
-// those of quantum 2 p + 1: the two diagonal quarters of D are the sums wanted.
+
+// A tile is eight rows: columns 0 .. 7 of the matrix instruction hold unit
+// 2 p of the rows, columns 8 .. 15 unit 2 p + 1, and likewise matrix rows
+// 0 .. 7 the parts of two tokens' activations of unit 2 p and rows 8 .. 15
+// those of unit 2 p + 1: the two diagonal quarters of D are the sums wanted.
 // An entry is an expert and one or two of its pairs (an expert with more
 // makes several, whose weights then come from the caches).  An item,
-// one entry's pair of quanta, is loaded while the item before is multiplied:
+// one entry's pair of units, is loaded while the item before is multiplied:
 // its weights, and its tokens' parts, which lie together in the workspace and
 // go through a piece of LDS of the wave's own to reach their lanes (loaded
 // fragment by fragment they were four times the load instructions, and the
 // texture-address unit was the bound).
-template <int WT, int SS, int QU>
+template <int WT, int SS>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
 {
     using F = RowFmt<WT, SS>;
-    constexpr int QB = QU * F::MF, SB = 2 * QB;
+    constexpr int QB = F::MF, SB = 2 * QB;
     constexpr int CHUNK = SB * kImageBytes;      // a token's parts of one item
     constexpr int HALF_LDS = CHUNK / 2 + 128, TOK_LDS = 2 * HALF_LDS + 64;   // strides that spread the banks
     constexpr int NA = (2 * CHUNK + 1023) / 1024;          // 16-byte loads per lane for two tokens
@@ -336,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
         a.h, 0, (int)((uint32_t)P * (uint32_t)a.h_pair), BUFFER_FLAGS);
     constexpr int D = 3;
     uint4 part[D][NA];
-    Quantum<WT, SS, QU> z[D];
+    Unit<WT, SS> z[D];
     // The wave takes items wave, wave + 16, ...: entry n, step p.  Two cursors
     // follow them, one for the loads and one for the products.
     struct Cursor {
@@ -370,13 +390,13 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
                 hres, in ? (uint32_t)pr * (uint32_t)a.h_pair + off : OUT_OF_RANGE, 0, 0));
         }
         const uint8_t *w = a.down + (uint64_t)__builtin_amdgcn_readfirstlane(en.x) * a.down_expert + row_off;
-        load_quantum<WT, SS, QU>(z[d.value], w, w, a.qoff2, code_bytes, 2 * p + (upper ? 1 : 0), last_q, g, upper);
+        load_unit<WT, SS>(z[d.value], w, a.qoff2, code_bytes, 2 * p + (upper ? 1 : 0), last_q, g);
     };
     const uint32_t frag_off = (uint32_t)((j >> 2 & 1) * TOK_LDS + (j >> 3) * HALF_LDS + ((j & 3) < 2 ? (j & 3) : 2) * 64 + 16 * g);
     uint8_t *const mine = parts[wave];
     const int share = wave < items ? (items - wave + kWaves - 1) / kWaves : 0;
     if (items > 0) stream_begin<0, D>(share, load);
-    stream<D>(share, load, [&](auto d, int) {
+    stream<D>(share, [](auto, int) {}, load, [&](auto d, int) {
         // this item's parts to their lanes (the wave's own LDS: its reads and
         // writes stay in order)
 #pragma unroll
@@ -390,7 +410,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
         advance(products);
         __builtin_amdgcn_wave_barrier();
         RowAcc<WT, false> acc[1];
-        multiply_quantum<WT, SS, QU, 1, false>(z[d.value], 2 * p + (upper ? 1 : 0), (p + 1) * SB <= a.nb2, a.nb2, g, upper, 1, acc,
+        multiply_unit<WT, SS, 1, false>(z[d.value], 2 * p + (upper ? 1 : 0), (p + 1) * SB <= a.nb2, a.nb2, g, upper, 1, acc,
                                                [&](int, int, int s) {
             return *reinterpret_cast<const rt_bf16x8 *>(mine + (uint32_t)s * kImageBytes + frag_off);
         });
@@ -417,12 +437,11 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
 
 typedef void (*Kernel)(MoeArgs);
 template <int WT, int SS>
-void pick(int qu, int depth, Kernel *up, Kernel *down)
+void pick(int depth, Kernel *up, Kernel *down)
 {
-    // (with one or two quanta of a wave and pass there is nothing to load ahead)
-    *up = qu == 2 ? (depth >= 3 ? moe_up_kernel<WT, SS, 2, 3> : moe_up_kernel<WT, SS, 2, 2>)
-                  : (depth >= 3 ? moe_up_kernel<WT, SS, 1, 4> : moe_up_kernel<WT, SS, 1, 2>);
-    *down = moe_down_kernel<WT, SS, kDownUnits>;
+    // (with one or two units of a wave and pass there is nothing to load ahead)
+    *up = depth > 4 ? moe_up_kernel<WT, SS, 8> : depth > 2 ? moe_up_kernel<WT, SS, 4> : moe_up_kernel<WT, SS, 2>;
+    *down = moe_down_kernel<WT, SS>;
 }
 
 }  // namespace
@@ -484,27 +503,31 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
     a.nb2 = (int32_t)(F / 32);
     a.qoff2 = (int32_t)quant_offset(F, down.w.scale_shift);
     const int64_t units1 = (gate.w.K + kpu - 1) / kpu, units2 = (F + kpu - 1) / kpu;
-    // about how many experts the tokens choose between them, each k of E
-    double untouched = 1.0;
-    for (int64_t n = 0; n < N; ++n) untouched *= k < gate.E ? 1.0 - (double)k / (double)gate.E : 0.0;
-    const int64_t experts = (int64_t)((double)gate.E * (1.0 - untouched) + 1.0);
-    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * experts, 0, (int)(N * k < 2 ? 1 : 2), 1);
+    // About how many entries the tokens make: a token chooses k of E experts, so
+    // an expert has c pairs of N trials with chance k / E each, and ceil(c / 2)
+    // entries: the mean of c plus the chance that it is odd, halved.
+    const double chance = k < gate.E ? (double)k / (double)gate.E : 1.0;
+    double even = 1.0;
+    for (int64_t n = 0; n < N; ++n) even *= 1.0 - 2.0 * chance;
+    const double mean = (double)gate.E * ((double)N * chance + (1.0 - even) / 2.0) / 2.0;
+    const int64_t entries = mean < 1.0 ? 1 : (int64_t)(mean + 0.5);
+    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * entries, 0, (int)(N * k < 2 ? 1 : 2), 1);
     a.steps1 = p.steps;
     a.s_log2 = p.s_log2;
     a.image = p.image;
     const int T = p.waves >> p.s_log2;
-    const int lds = p.waves * 64 * 4 + p.image;
-    a.steps2 = (int32_t)((units2 + 2 * kDownUnits - 1) / (2 * kDownUnits));
+    const int lds = p.waves * (64 * 4 + kScaleLds) + p.image;
+    a.steps2 = (int32_t)((units2 + 1) / 2);
 
     const int depth = (p.steps + (1 << p.s_log2) - 1) >> p.s_log2;
     Kernel ku = nullptr, kd = nullptr;
-    if (type == W_MXFP4) pick<W_MXFP4, 0>(p.qu, depth, &ku, &kd);
-    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(p.qu, depth, &ku, &kd) : pick<W_Q4_0, 0>(p.qu, depth, &ku, &kd);
-    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(p.qu, depth, &ku, &kd) : pick<W_Q8_0, 0>(p.qu, depth, &ku, &kd);
+    if (type == W_MXFP4) pick<W_MXFP4, 0>(depth, &ku, &kd);
+    else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(depth, &ku, &kd) : pick<W_Q4_0, 0>(depth, &ku, &kd);
+    else if (type == W_Q8_0) ss ? pick<W_Q8_0, 1>(depth, &ku, &kd) : pick<W_Q8_0, 0>(depth, &ku, &kd);
     else return hipErrorInvalidValue;
     hipError_t e = hipSuccess;
     if (F > 0) {
-        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), 128 * 1024);
+        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), 160 * 1024);
         if (e != hipSuccess) return e;
         const unsigned groups = (unsigned)(((F + 7) / 8 + T - 1) / T);
         hipLaunchKernelGGL(ku, dim3(groups, (unsigned)(N * k)), dim3(64 * p.waves), (unsigned)lds, stream, a);

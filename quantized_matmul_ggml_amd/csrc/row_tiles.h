@@ -138,7 +138,7 @@ __device__ inline void matrix_order(const rt_f32x4 a, const rt_f32x4 b, float (&
 // `threads` threads in pieces of eight values; blocks from nb on are zeros.
 // row(t) is token t's row.  A thread's first two pieces are loaded ahead of the
 // workgroup's first weights (AHEAD: image_ahead, then build_image), since loads
-// complete in order; the weights that follow the first quantum are asked for
+// complete in order; the weights that follow the first unit are asked for
 // after the conversion, because the memory takes them only as fast as it
 // delivers, and a wave waiting to issue loads converts nothing.
 struct ImageAhead {
@@ -213,12 +213,12 @@ __device__ inline void build_image(uint8_t *img, int ntok, int b0, int nblk, int
     }
 }
 
-// QU units of a tile's rows in registers: codes, and the scales of the
-// lane's row.
-template <int WT, int SS, int QU>
-struct Quantum {
-    static constexpr int SB = QU * RowFmt<WT, SS>::SPU;
-    uint4 q[QU];
+// One unit of a tile's rows in registers: codes, and the scales of the lane's
+// row.
+template <int WT, int SS>
+struct Unit {
+    static constexpr int SB = RowFmt<WT, SS>::SPU;
+    uint4 q;
     uint32_t s[(SB + 3) / 4];
 };
 
@@ -239,74 +239,88 @@ __device__ inline void rt_swap16(uint32_t &a, uint32_t &b)
 
 typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
 
-typedef uint32_t rt_u32x4 __attribute__((ext_vector_type(4)));
-
-// Loads quantum qi.  With one unit a lane reads 16 bytes of its own row, `row0`
-// (64 bytes of each row per load).  With two, the first load takes both units
-// (128 bytes, the cache line's size) of the tile's first eight rows and the
-// second those of the other eight: columns j and j + 8 read the halves of one
-// row, row0 in the first load and row1 in the second, and pair_units hands each
-// lane its own row afterwards.  (Sixteen rows 64 bytes at a time leave half of
-// each cache line's fill to a later load, and the L1 holds few enough lines
-// for that to halve the bytes in flight.)
+// The codes of unit qi of the lane's row: 16 bytes of it each, 64 bytes of
+// sixteen rows per load.  (Two units of eight rows, whole cache lines, streamed
+// no faster, and handing each lane its own row afterwards took registers that
+// hold units in flight now.)
 //
 // Always the same loads in the same order, whatever the row's length: a
 // branch around a load would make the compiler wait for every load in flight,
-// the next quantum's among them.  Every address lies inside the row: units
-// past its end repeat its last 16 bytes and a quantum past it the scales of
-// its last (last_q; the activations there are zeros and multiply_quantum
-// zeroes the scales), and the scale bytes of a quantum with any block of the
-// row end at or before the row's end, because the row's codes follow its
-// scales.
-template <int WT, int SS, int QU>
-__device__ inline void load_quantum(Quantum<WT, SS, QU> &z, const uint8_t *row0, const uint8_t *row1, int qoff, int code_bytes,
-                                    int qi, int last_q, int g, bool upper)
+// the next unit's among them.  Every address lies inside the row: units past
+// its end repeat its last 16 bytes (the activations there are zeros and
+// multiply_unit zeroes the scales).
+template <int WT, int SS>
+__device__ inline void load_codes(Unit<WT, SS> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int g)
 {
-    static_assert(QU == 1 || QU == 2, "one or two units");
-    constexpr int SB = Quantum<WT, SS, QU>::SB;
-    const int c = 64 * QU * qi + (QU == 2 && upper ? 64 : 0) + 16 * g, top = code_bytes - 16;
-    const uint32_t at = (uint32_t)(qoff + (c < top ? c : top));
-    z.q[0] = *reinterpret_cast<const uint4 *>(row0 + at);
-    if constexpr (QU == 2) z.q[1] = *reinterpret_cast<const uint4 *>(row1 + at);
-    const uint8_t *s = (QU == 2 && upper ? row1 : row0) + (uint32_t)(SB * (qi < last_q ? qi : last_q));
+    const int c = 64 * qi + 16 * g, top = code_bytes - 16;
+    z.q = *reinterpret_cast<const uint4 *>(row + (uint32_t)(qoff + (c < top ? c : top)));
+}
+
+// SB bytes at an address aligned to SB.
+template <int SB>
+__device__ inline void scale_words(const uint8_t *s, uint32_t (&out)[(SB + 3) / 4])
+{
     if constexpr (SB == 2) {
-        z.s[0] = *reinterpret_cast<const uint16_t *>(s);
+        out[0] = *reinterpret_cast<const uint16_t *>(s);
     } else if constexpr (SB == 4) {
-        z.s[0] = *reinterpret_cast<const uint32_t *>(s);
-    } else if constexpr (SB == 8) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(s);
-        z.s[0] = v.x;
-        z.s[1] = v.y;
+        out[0] = *reinterpret_cast<const uint32_t *>(s);
     } else {
-        static_assert(SB % 16 == 0, "scale bytes of a quantum");
-#pragma unroll
-        for (int i = 0; i < SB / 16; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(s + 16 * i);
-            z.s[4 * i] = v.x;
-            z.s[4 * i + 1] = v.y;
-            z.s[4 * i + 2] = v.z;
-            z.s[4 * i + 3] = v.w;
-        }
+        static_assert(SB == 8, "scale bytes of a unit");
+        const uint2 v = *reinterpret_cast<const uint2 *>(s);
+        out[0] = v.x;
+        out[1] = v.y;
     }
 }
 
-// The units of a lane's own row from the two loads of load_quantum: columns
-// 8 .. 15 of the first and 0 .. 7 of the second hold each other's (one DPP
-// rotation by eight lanes per dword, written to half the columns).
+// Codes and scales of one unit.  A unit past the row's end (last_q) has the
+// scales of its last; the scale bytes of a unit with any block of the row end
+// at or before the row's end, because the row's codes follow its scales.
 template <int WT, int SS>
-__device__ inline void pair_units(Quantum<WT, SS, 2> &z)
+__device__ inline void load_unit(Unit<WT, SS> &z, const uint8_t *row, int qoff, int code_bytes, int qi, int last_q, int g)
 {
-    uint32_t a[4] = {z.q[0].x, z.q[0].y, z.q[0].z, z.q[0].w}, b[4] = {z.q[1].x, z.q[1].y, z.q[1].z, z.q[1].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int lo = __builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);
-        const int hi = __builtin_amdgcn_update_dpp((int)b[i], (int)a[i], 0x128, 0xF, 0x3, false);
-        a[i] = (uint32_t)lo;
-        b[i] = (uint32_t)hi;
-    }
-    z.q[0] = make_uint4(a[0], a[1], a[2], a[3]);
-    z.q[1] = make_uint4(b[0], b[1], b[2], b[3]);
+    constexpr int SB = Unit<WT, SS>::SB;
+    load_codes<WT, SS>(z, row, qoff, code_bytes, qi, g);
+    scale_words<SB>(row + (uint32_t)(SB * (qi < last_q ? qi : last_q)), z.s);
 }
+
+// The scales of D consecutive steps of a wave's rows, in one load: lane group
+// g takes the g-th 16 bytes of its row (with HALF the eight lanes of a row one
+// piece each), and a piece of LDS of the wave's own hands every lane the
+// scales it multiplies by.  One load per unit for its scales, four lanes
+// reading the same bytes, takes the texture units as long as 1 KB of codes:
+// streaming 94 MB of MXFP4 rows took 21.9 us with it, 18.8 with one load per
+// row, 18.4 with no scales at all.
+template <int WT, int SS, bool HALF, int D>
+struct ScaleWindow {
+    static constexpr int SB = RowFmt<WT, SS>::SPU;
+    static constexpr int STEP = SB * (HALF ? 2 : 1), PIECES = (D * STEP + 15) / 16;
+    static constexpr int STRIDE = HALF ? 144 : 80;         // rows on different banks
+    static_assert(PIECES <= (HALF ? 8 : 4), "one piece per lane");
+    typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+    words next;
+
+    // Steps p .. p + D - 1 of the lane's row of row_bytes bytes, clamped so that
+    // every address lies in the row: its last 16 bytes are codes.
+    __device__ inline void load(const uint8_t *row, int row_bytes, int p, int g, bool upper)
+    {
+        const int piece = HALF && upper ? 4 + g : g;
+        const int at = STEP * p + 16 * (piece < PIECES ? piece : PIECES - 1), top = row_bytes - 16;
+        next = *reinterpret_cast<const words *>(row + (uint32_t)(at < top ? at : top));
+    }
+    __device__ inline void put(uint8_t *lds, int j, int g) const
+    {
+        const int row = HALF ? j & 7 : j, piece = HALF && j >= 8 ? 4 + g : g;
+        __builtin_amdgcn_wave_barrier();
+        *reinterpret_cast<uint4 *>(lds + row * STRIDE + 16 * piece) = make_uint4(next.x, next.y, next.z, next.w);
+        __builtin_amdgcn_wave_barrier();
+    }
+    __device__ inline void get(Unit<WT, SS> &z, const uint8_t *lds, int d, int j) const
+    {
+        const int row = HALF ? j & 7 : j;
+        scale_words<SB>(lds + row * STRIDE + (HALF ? 2 * d + (j >= 8 ? 1 : 0) : d) * SB, z.s);
+    }
+};
+constexpr int kScaleLds = 16 * 80;                         // a wave's LDS for it
 
 // The sum of a lane's row and token over the instructions so far.  MXFP4 keeps
 // the matrix instruction's own accumulators (one per part, added at the end;
@@ -336,136 +350,127 @@ __device__ inline uint32_t rt_pack(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(rt_f32x2{a, b}, rt_bf16x2));
 }
 
-// Multiplies the quanta in z with the activation fragments of token groups
+// Multiplies the units in z with the activation fragments of token groups
 // tg < groups.  frag(tg, half, step) is the fragment of instruction `step` of
-// the quantum that columns 8 half .. 8 half + 7 hold.  Without HALF all
-// sixteen columns are rows of the same quantum (half is 0); with it columns
-// 0 .. 7 are eight rows' quantum 2 q and columns 8 .. 15 the same rows' quantum
+// the unit that columns 8 half .. 8 half + 7 hold.  Without HALF all
+// sixteen columns are rows of the same unit (half is 0); with it columns
+// 0 .. 7 are eight rows' unit 2 q and columns 8 .. 15 the same rows' unit
 // 2 q + 1, so that a tile of eight rows still loads sixteen columns at once:
 // each weight fragment meets both halves' activations, and each half of the
-// columns keeps its own product.  qi: this lane's quantum; whole: as in
-// load_quantum; nb: blocks of the row.
-template <int WT, int SS, int QU, int TG, bool HALF, class Frag>
-__device__ inline void multiply_quantum(Quantum<WT, SS, QU> &z, int qi, bool whole, int nb, int g, bool upper, int groups,
+// columns keeps its own product.  qi: this lane's unit; whole: as in
+// load_unit; nb: blocks of the row.
+template <int WT, int SS, int TG, bool HALF, class Frag>
+__device__ inline void multiply_unit(const Unit<WT, SS> &z, int qi, bool whole, int nb, int g, bool upper, int groups,
                                         RowAcc<WT, HALF> (&acc)[TG], Frag frag)
 {
     using F = RowFmt<WT, SS>;
     constexpr int H = HALF ? 2 : 1;
-    if constexpr (QU == 2) pair_units<WT, SS>(z);
-    const int left = whole ? QU * F::MF : nb - qi * QU * F::MF;      // blocks of this quantum in the row
-    // A unit's fragments are read while the unit before is multiplied (with
-    // two token groups, at its start: the registers hold one unit's).
-    constexpr int NF = F::MF * TG * H;
-    constexpr int BUFS = NF <= 4 && QU > 1 ? 2 : 1;
-    rt_bf16x8 fr[BUFS][TG][H][F::MF];
-    auto fetch = [&](int i) {
+    const int left = whole ? F::MF : nb - qi * F::MF;      // blocks of this unit in the row
+    rt_bf16x8 fr[TG][H][F::MF];
 #pragma unroll
-        for (int t = 0; t < F::MF; ++t)
+    for (int t = 0; t < F::MF; ++t)
+#pragma unroll
+        for (int tg = 0; tg < TG; ++tg)
+            if (tg < groups) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) fr[tg][h][t] = frag(tg, h, t);
+            }
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t d[4] = {z.q.x, z.q.y, z.q.z, z.q.w};
+    if constexpr (WT == W_MXFP4) {
+        // lane group g holds block g of the unit: its scale byte
+        // as the exponent of a float (255 is NaN, 0 is 2^-127)
+        uint32_t e = (z.s[0] >> (8 * g)) & 0xFFu;
+        if (!whole) e = g < left ? e : 0u;
+        const float f = __builtin_bit_cast(float, e << 23);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint4 bw = make_uint4(
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 0)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 1)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 2)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 3)));
+            const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
 #pragma unroll
             for (int tg = 0; tg < TG; ++tg)
                 if (tg < groups) {
 #pragma unroll
-                    for (int h = 0; h < H; ++h) fr[i % BUFS][tg][h][t] = frag(tg, h, F::MF * i + t);
+                    for (int h = 0; h < H; ++h)
+                        acc[tg].c[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[tg][h][t], b, acc[tg].c[h], 0, 0, 0);
                 }
-    };
-    if constexpr (BUFS == 2) fetch(0);
+        }
+    } else {
+        rt_swap32(d[0], d[2]);
+        rt_swap32(d[1], d[3]);
+        if constexpr (WT == W_Q4_0) {
+            rt_swap16(d[0], d[1]);
+            rt_swap16(d[2], d[3]);
+        }
 #pragma unroll
-    for (int i = 0; i < QU; ++i) {
-        if constexpr (BUFS == 1) fetch(i);
-        else if (i + 1 < QU) fetch(i + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        uint32_t d[4] = {z.q[i].x, z.q[i].y, z.q[i].z, z.q[i].w};
-        if constexpr (WT == W_MXFP4) {
-            // lane group g holds block 4 i + g of the quantum: its scale byte
-            // as the exponent of a float (255 is NaN, 0 is 2^-127)
-            uint32_t e = (z.s[i] >> (8 * g)) & 0xFFu;
-            if (!whole) e = 4 * i + g < left ? e : 0u;
-            const float f = __builtin_bit_cast(float, e << 23);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint4 bw = make_uint4(
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 0)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 1)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 2)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 3)));
-                const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
-#pragma unroll
-                for (int tg = 0; tg < TG; ++tg)
-                    if (tg < groups) {
-#pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            acc[tg].c[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][h][t], b, acc[tg].c[h], 0, 0, 0);
-                    }
-            }
-        } else {
-            rt_swap32(d[0], d[2]);
-            rt_swap32(d[1], d[3]);
+        for (int t = 0; t < F::MF; ++t) {
+            uint4 bw;
             if constexpr (WT == W_Q4_0) {
-                rt_swap16(d[0], d[1]);
-                rt_swap16(d[2], d[3]);
+                // a nibble n at the top of a byte with its top bit flipped
+                // is the int8 value 16 (n - 8); the scale absorbs the 16
+                const uint32_t x = d[t] ^ 0x88888888u;
+                const uint32_t lo = (x << 4) & 0xF0F0F0F0u, hi = x & 0xF0F0F0F0u;
+                bw = make_uint4(rt_pack(rt_sbyte<0>(lo), rt_sbyte<0>(hi)), rt_pack(rt_sbyte<1>(lo), rt_sbyte<1>(hi)),
+                                rt_pack(rt_sbyte<2>(lo), rt_sbyte<2>(hi)), rt_pack(rt_sbyte<3>(lo), rt_sbyte<3>(hi)));
+            } else {
+                const uint32_t a = d[2 * t], c = d[2 * t + 1];
+                bw = make_uint4(rt_pack(rt_sbyte<0>(a), rt_sbyte<1>(a)), rt_pack(rt_sbyte<2>(a), rt_sbyte<3>(a)),
+                                rt_pack(rt_sbyte<0>(c), rt_sbyte<1>(c)), rt_pack(rt_sbyte<2>(c), rt_sbyte<3>(c)));
             }
+            const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
+            const int sh = t >> SS;                        // the block's scale (a half) within the unit
+            const uint32_t sb = (sh & 1) ? z.s[sh / 2] >> 16 : z.s[sh / 2] & 0xFFFFu;
+            float f = (float)__builtin_bit_cast(_Float16, (uint16_t)sb);
+            if constexpr (WT == W_Q4_0) f *= 0.0625f;
+            if (!whole) f = t < left ? f : 0.0f;
 #pragma unroll
-            for (int t = 0; t < F::MF; ++t) {
-                uint4 bw;
-                if constexpr (WT == W_Q4_0) {
-                    // a nibble n at the top of a byte with its top bit flipped
-                    // is the int8 value 16 (n - 8); the scale absorbs the 16
-                    const uint32_t x = d[t] ^ 0x88888888u;
-                    const uint32_t lo = (x << 4) & 0xF0F0F0F0u, hi = x & 0xF0F0F0F0u;
-                    bw = make_uint4(rt_pack(rt_sbyte<0>(lo), rt_sbyte<0>(hi)), rt_pack(rt_sbyte<1>(lo), rt_sbyte<1>(hi)),
-                                    rt_pack(rt_sbyte<2>(lo), rt_sbyte<2>(hi)), rt_pack(rt_sbyte<3>(lo), rt_sbyte<3>(hi)));
-                } else {
-                    const uint32_t a = d[2 * t], c = d[2 * t + 1];
-                    bw = make_uint4(rt_pack(rt_sbyte<0>(a), rt_sbyte<1>(a)), rt_pack(rt_sbyte<2>(a), rt_sbyte<3>(a)),
-                                    rt_pack(rt_sbyte<0>(c), rt_sbyte<1>(c)), rt_pack(rt_sbyte<2>(c), rt_sbyte<3>(c)));
-                }
-                const rt_bf16x8 b = __builtin_bit_cast(rt_bf16x8, bw);
-                const int blk = i * F::MF + t;                 // static
-                const int sh = blk >> SS;                      // the block's scale (a half) within the quantum
-                const uint32_t sb = (sh & 1) ? z.s[sh / 2] >> 16 : z.s[sh / 2] & 0xFFFFu;
-                float f = (float)__builtin_bit_cast(_Float16, (uint16_t)sb);
-                if constexpr (WT == W_Q4_0) f *= 0.0625f;
-                if (!whole) f = blk < left ? f : 0.0f;
-#pragma unroll
-                for (int tg = 0; tg < TG; ++tg)
-                    if (tg < groups) {
-                        const rt_f32x4 zero = {0, 0, 0, 0};
-                        const rt_f32x4 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][0][t], b, zero, 0, 0, 0);
-                        float sum = s0[0] + (s0[1] + s0[2]);
-                        if constexpr (HALF) {
-                            const rt_f32x4 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[i % BUFS][tg][1][t], b, zero, 0, 0, 0);
-                            const float other = s1[0] + (s1[1] + s1[2]);
-                            sum = upper ? other : sum;
-                        }
-                        acc[tg].c[0][0] = fmaf(f, sum, acc[tg].c[0][0]);
+            for (int tg = 0; tg < TG; ++tg)
+                if (tg < groups) {
+                    const rt_f32x4 zero = {0, 0, 0, 0};
+                    const rt_f32x4 s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[tg][0][t], b, zero, 0, 0, 0);
+                    float sum = s0[0] + (s0[1] + s0[2]);
+                    if constexpr (HALF) {
+                        const rt_f32x4 s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[tg][1][t], b, zero, 0, 0, 0);
+                        const float other = s1[0] + (s1[1] + s1[2]);
+                        sum = upper ? other : sum;
                     }
-            }
+                    acc[tg].c[0][0] = fmaf(f, sum, acc[tg].c[0][0]);
+                }
         }
     }
 }
 
-// A wave's run over its n quanta (or items) 0 .. n - 1 with D of them in
+// A wave's run over its n units (or items) 0 .. n - 1 with D of them in
 // registers: `stream_begin` loads the first D, `stream` multiplies each and
 // loads the one D later into its place.  The places are fixed at compile time:
-// moving a loaded register would wait for its load, so that only one quantum
-// were ever in flight.  load(d, i)
-// fills place d; use(d, i) consumes it.  Past the end the last one is loaded
-// again (from the caches), so that every load is unconditional: a place loaded
-// on one of two paths would be copied where they meet, and waited for there.
+// moving a loaded register would wait for its load, so that only one unit
+// were ever in flight.  load(d, i) fills place d; use(d, i) consumes it;
+// head(more, i) is called before each D of them with the index of the next D
+// and whether there are any.  Past the end the last one is loaded again (from
+// the caches), so that every load is unconditional: a place loaded on one of
+// two paths would be copied where they meet, and waited for there.  Every path
+// into `stream` has to issue the loads in this order too, since the compiler
+// waits for the fewest loads that may have followed on any of them.
 template <int FROM, int TO, class Load>
 __device__ inline void stream_begin(int n, Load load)
 {
     static_steps<TO - FROM>([&](auto i) {
         constexpr int d = FROM + decltype(i)::value;
         load(std::integral_constant<int, d>{}, d < n ? d : n > 0 ? n - 1 : 0);
+        __builtin_amdgcn_sched_barrier(0);
     });
-    __builtin_amdgcn_sched_barrier(0);
 }
-template <int D, class Load, class Use>
-__device__ inline void stream(int n, Load load, Use use)
+template <int D, class Head, class Load, class Use>
+__device__ inline void stream(int n, Head head, Load load, Use use)
 {
     int i = 0;
-    for (; n - i > D; i += D)
+    for (; n - i > D; i += D) {
+        head(std::true_type{}, i + D);
+        __builtin_amdgcn_sched_barrier(0);
         static_steps<D>([&](auto d) {
             const int k = i + (int)d.value;
             use(d, k);
@@ -473,10 +478,13 @@ __device__ inline void stream(int n, Load load, Use use)
             load(d, k + D < n ? k + D : n - 1);
             __builtin_amdgcn_sched_barrier(0);
         });
+    }
+    head(std::false_type{}, 0);
     static_steps<D>([&](auto d) {
         if (i + (int)d.value < n) use(d, i + (int)d.value);
     });
 }
+
 // Swish(z) = z * sigma(z) = z / (1 + e^{-z}) in binary32; for z far below
 // zero e^{-z} overflows and the quotient is the limit -0.
 __device__ inline float rt_swish(float z)
@@ -486,11 +494,10 @@ __device__ inline float rt_swish(float z)
 
 // ---- host: how a launch splits its rows ----
 struct RowPlan {
-    int qu;          // units per quantum (1, 2)
     int half;        // tiles of eight rows (HALF)
     int s_log2;      // log2 of the waves that share a tile
     int waves;       // per workgroup
-    int steps;       // quanta (or pairs of quanta) per row
+    int steps;       // units (HALF: pairs of units) per row
     int step_bytes;  // image bytes per step and token
     int image;       // LDS bytes for the image
 };
@@ -500,46 +507,44 @@ struct RowPlan {
 // tokens: the most tokens one image holds at once; likely: how many it will hold
 // as a rule.
 //
-// About ten waves on every CU, each with three or four quanta in flight, stream
-// at the memory's rate, so a launch aims at that many (tile, wave) tasks, with
-// as few waves sharing a tile and as large quanta (one scale load per QU code
-// loads) as still give them (two of eight Q4_0 experts of 5632 x 2048: 20.0 us
-// with two waves a tile, 22 with one or four).  Workgroups are small (four
-// waves) while their image is, so that several share a CU and one's loads run
-// beside another's setup; with more tokens a larger workgroup shares one
-// image.  (Eight-row tiles with larger quanta or two token groups need more
-// registers than sixteen waves a CU leave.)
+// The memory streams at its rate with about sixteen waves on every CU and four
+// or more units of each in flight, so waves share tiles until there are that
+// many (tile, wave) tasks or four units left to a wave (three Q8_0 tokens
+// choosing four of sixteen experts of 1408 x 2048: 25.2 us with four waves a
+// tile, 27.0 with two, 29.4 with one).  With two token groups a unit is twice
+// the work and two units will do (5632 x 2048 for eight tokens: 6.0 us with
+// eight waves a tile, 6.8 with four).  Where a launch has so few tiles that most
+// of the chip idles even so, tiles of eight rows and pairs of units double
+// them (2048 x 5632 for one token: 4.4 us against 4.9; 5632 x 2048, whose 352
+// tiles are enough, 5.0 against 4.4).  Workgroups are small (four waves) while
+// their image is, so that several share a CU and one's loads run beside
+// another's setup; with more tokens a larger workgroup shares one image.
 inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens, int likely)
 {
-    const int64_t target = 10 * (int64_t)device_cus();
-    RowPlan p = {1, 0, 0, 4, 0, 0, 0};
-    auto steps_of = [&](int qu, int half) { return ((units + qu - 1) / qu + half) / (1 + half); };
-    int64_t best = -1;
-    for (int half = 0; half <= (half_tiles && tokens <= 4 ? 1 : 0) && best < target; ++half) {
-        const int64_t t = half ? half_tiles : tiles;
-        for (int qu = half ? 1 : 2; qu >= 1 && best < target; qu /= 2) {
-            int s = 0;
-            while (s < 4 && t << s < target && (2 << s) <= steps_of(qu, half)) ++s;
-            if (t << s > best) {
-                best = t << s;
-                p.qu = qu;
-                p.half = half;
-                p.s_log2 = s;
-            }
-        }
+    const int64_t cus = device_cus();
+    RowPlan p = {0, 0, 4, 0, 0, 0};
+    auto steps_of = [&](int half) { return (units + half) / (1 + half); };
+    auto share = [&](int64_t t, int64_t steps, int least) {
+        int s = 0;
+        while (s < 4 && t << s < 16 * cus && steps >> (s + 1) >= least) ++s;
+        return s;
+    };
+    p.s_log2 = share(tiles, steps_of(0), tokens > 4 ? 2 : 4);
+    if (half_tiles && tokens <= 4 && tiles << p.s_log2 < 5 * cus) {
+        p.half = 1;
+        p.s_log2 = share(half_tiles, steps_of(1), 2);
     }
     p.waves = likely <= 2 ? 4 : likely <= 4 ? 8 : 16;
     if (p.waves < 1 << p.s_log2) p.waves = 1 << p.s_log2;
     auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : 112 * 1024; };
     // one step of every wave of a tile has to fit the image
     for (;;) {
-        p.step_bytes = p.qu * (1 + p.half) * mf * kImageBytes;
+        p.step_bytes = (1 + p.half) * mf * kImageBytes;
         if (((int64_t)p.step_bytes * tokens << p.s_log2) <= budget()) break;
         if (p.waves < 16) p.waves *= 2;
-        else if (p.qu > 1) p.qu /= 2;
         else --p.s_log2;
     }
-    p.steps = (int)steps_of(p.qu, p.half);
+    p.steps = (int)steps_of(p.half);
     const int64_t all = (int64_t)p.steps * p.step_bytes * tokens;
     p.image = (int)(all < budget() ? all : budget());
     return p;
