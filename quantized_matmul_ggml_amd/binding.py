@@ -81,7 +81,8 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m quantized_matmul_ggml_amd.build` "
                 "(hipcc, gfx950); there is no fallback implementation")
         h = ctypes.CDLL(LIB_PATH)
-        P = ctypes.POINTER(QmmTensor)
+        # descriptors: packed bytes (_PACK), or ctypes.byref of a QmmTensor
+        P = ctypes.c_void_p
         h.qmm_row_size.argtypes = [ctypes.c_int32, ctypes.c_int64]
         h.qmm_row_size.restype = ctypes.c_size_t
         h.qmm_quantize.argtypes = [P, P, ctypes.c_void_p]
@@ -151,6 +152,13 @@ def make_desc(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int, n_dims: i
     return QmmTensor.from_buffer_copy(_PACK(type_, n_dims, ne0, ne1, 1, 1, nb0 & _U64, nb1 & _U64, nb2, nb2, data_ptr or 0))
 
 
+def _packed(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int) -> bytes:
+    """make_desc's bytes, which the entry points take as they are (building a
+    structure from them costs as much again)."""
+    nb2 = nb1 * (ne1 if ne1 > 1 else 1)
+    return _PACK(type_, 2, ne0, ne1, 1, 1, _ELEM.get(type_, 0), nb1, nb2, nb2, data_ptr)
+
+
 @dataclass
 class Weight:
     """A weight matrix W (ne = [K, M]): M rows of K weights on the GPU.
@@ -169,29 +177,44 @@ class Weight:
     def desc(self) -> QmmTensor:
         return make_desc(self.type, self.K, self.M, self.pitch, self.data.data_ptr())
 
+    def _desc(self) -> bytes:
+        d = self.data
+        return _packed(self.type, self.K, self.M, d.stride(0) * d.element_size(), d.data_ptr())
+
     def rows(self, r0: int, r1: int) -> "Weight":
         """Row-range view [r0, r1): no copy, same pitch."""
         return Weight(self.data[r0:r1], self.type, self.K, r1 - r0)
 
 
-def _need_gpu(*ts: torch.Tensor):
+def _need_gpu(*ts: torch.Tensor) -> int:
+    """The one GPU the tensors are on."""
+    dev = ts[0].get_device()
     for t in ts:
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("libqmm operates on GPU tensors only")
+        if d != dev:
+            raise ValueError("the tensors of a call must be on one GPU")
+    return dev
 
 
 def _dense_desc(t: torch.Tensor, type_: int) -> QmmTensor:
     """2-D row-major torch tensor (rows, cols) -> ne = [cols, rows]."""
+    return QmmTensor.from_buffer_copy(_dense(t, type_))
+
+
+def _dense(t: torch.Tensor, type_: int) -> bytes:
+    """_dense_desc's bytes."""
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     es = t.element_size()
     rows, cols = t.shape
     if rows == 0 or cols == 0:          # empty: strides are meaningless
-        return make_desc(type_, cols, rows, cols * es, t.data_ptr())
+        return _packed(type_, cols, rows, cols * es, t.data_ptr())
     pitch, step = t.stride()
     if step != 1:
         raise ValueError("rows must be contiguous (stride 1 along the last dimension)")
-    return make_desc(type_, cols, rows, pitch * es, t.data_ptr())
+    return _packed(type_, cols, rows, pitch * es, t.data_ptr())
 
 
 # The current stream's handle without building a Stream object (2.8 us less per
@@ -205,6 +228,23 @@ def _stream(stream) -> int:
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _launch(dev: int, stream, name: str, *args):
+    """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
+    stream; raises what it refuses."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, name, *args)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    status = getattr(_lib or lib(), name)(*args, handle)
+    if status != OK:
+        raise QmmError(status, name)
 
 
 def _check(status: int, where: str):
@@ -221,28 +261,23 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
     64-weight-block variants Q8_B64 / Q4_B64 (rule: QUANT_DEFAULT, or
     QUANT_Q4_AMAX7 for the symmetric amax/7 Q4 rule), or MXFP4 rows (fp32 or
     bf16 w)."""
-    _need_gpu(w)
+    dev = _need_gpu(w)
     M, K = w.shape
     rs = row_size(type_, K)
     pitch = rs if pitch is None else pitch
-    out = torch.empty((M, pitch), dtype=torch.uint8, device=w.device)
+    out = torch.empty(M, pitch, dtype=torch.uint8, device=w.device)
     if pitch > rs:
         out[:, rs:].zero_()
     wt = Weight(out, type_, K, M)
-    src, dst = _dense_desc(w, BF16 if w.dtype == torch.bfloat16 else F32), wt.desc()
-    _check(lib().qmm_quantize_rule(src, dst, rule, _stream(stream)),
-           "qmm_quantize_rule")
+    _launch(dev, stream, "qmm_quantize_rule", _dense(w, BF16 if w.dtype == torch.bfloat16 else F32), wt._desc(), rule)
     return wt
 
 
 def dequantize(w: Weight, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """W' as fp32 (M, K)."""
-    _need_gpu(w.data)
     if out is None:
-        out = torch.empty((w.M, w.K), dtype=torch.float32, device=w.data.device)
-    src, dst = w.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_dequantize(src, dst, _stream(stream)),
-           "qmm_dequantize")
+        out = torch.empty(w.M, w.K, dtype=torch.float32, device=w.data.device)
+    _launch(_need_gpu(w.data, out), stream, "qmm_dequantize", w._desc(), _dense(out, F32))
     return out
 
 
@@ -257,17 +292,10 @@ def gemv(w: Weight, x, *, out: torch.Tensor | None = None, stream=None) -> torch
     """y (N, M) fp32 = x (N, K) times W'^T; 1 <= N <= 8.  x is fp32 (N, K), or
     a Q8_0 Weight of N rows (activations quantized with quantize()) for the
     integer-activation path."""
-    if isinstance(x, Weight):
-        _need_gpu(w.data, x.data)
-        n, dev, xd = x.M, x.data.device, x.desc()
-    else:
-        _need_gpu(w.data, x)
-        n, dev, xd = x.shape[0], x.device, _dense_desc(x, F32)
+    xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, F32))
     if out is None:
-        out = torch.empty((n, w.M), dtype=torch.float32, device=dev)
-    wd, yd = w.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_gemv(wd, xd, yd, _stream(stream)),
-           "qmm_gemv")
+        out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+    _launch(_need_gpu(w.data, xt, out), stream, "qmm_gemv", w._desc(), xd, _dense(out, F32))
     return out
 
 
@@ -276,22 +304,21 @@ def gemv_batch(items, *, stream=None) -> list:
     sharing the weight type, K and N; x is fp32 (N, K) in every item, or a
     Q8_0 Weight of N rows in every item (the integer-activation path).
     Returns the outputs."""
-    descs, keep, outs = [], [], []
+    descs, keep, outs, tensors = [], [], [], []
     for w, x, out in items:
-        if isinstance(x, Weight):
-            _need_gpu(w.data, x.data)
-            n, dev, xd = x.M, x.data.device, x.desc()
-        else:
-            _need_gpu(w.data, x)
-            n, dev, xd = x.shape[0], x.device, _dense_desc(x, F32)
+        xt, n, xd = (x.data, x.M, x.desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense_desc(x, F32))
         if out is None:
-            out = torch.empty((n, w.M), dtype=torch.float32, device=dev)
+            out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+        tensors += [w.data, xt, out]
         wd, yd = w.desc(), _dense_desc(out, F32)
         keep += [wd, xd, yd]
         descs.append(QmmGemvItem(ctypes.pointer(wd), ctypes.pointer(xd), ctypes.pointer(yd)))
         outs.append(out)
     arr = (QmmGemvItem * max(1, len(descs)))(*descs)
-    _check(lib().qmm_gemv_batch(arr, len(descs), _stream(stream)), "qmm_gemv_batch")
+    if tensors:
+        _launch(_need_gpu(*tensors), stream, "qmm_gemv_batch", arr, len(descs))
+    else:
+        _check(lib().qmm_gemv_batch(arr, 0, _stream(stream)), "qmm_gemv_batch")
     return outs
 
 
@@ -299,17 +326,11 @@ def gemv_swiglu(w_gate: Weight, w_up: Weight, x, *, out: torch.Tensor | None = N
                 stream=None) -> torch.Tensor:
     """h (N, M) fp32 = Swish(x W_gate'^T) * (x W_up'^T), one fused launch; 1 <= N <= 8.
     x is fp32 (N, K), or a Q8_0 Weight of N rows for the integer-activation path."""
-    if isinstance(x, Weight):
-        _need_gpu(w_gate.data, w_up.data, x.data)
-        n, dev, xd = x.M, x.data.device, x.desc()
-    else:
-        _need_gpu(w_gate.data, w_up.data, x)
-        n, dev, xd = x.shape[0], x.device, _dense_desc(x, F32)
+    xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, F32))
     if out is None:
-        out = torch.empty((n, w_gate.M), dtype=torch.float32, device=dev)
-    gd, ud, hd = w_gate.desc(), w_up.desc(), _dense_desc(out, F32)
-    _check(lib().qmm_gemv_swiglu(gd, ud, xd, hd,
-                                 _stream(stream)), "qmm_gemv_swiglu")
+        out = torch.empty(n, w_gate.M, dtype=torch.float32, device=xt.device)
+    _launch(_need_gpu(w_gate.data, w_up.data, xt, out), stream, "qmm_gemv_swiglu", w_gate._desc(), w_up._desc(), xd,
+            _dense(out, F32))
     return out
 
 
@@ -321,33 +342,27 @@ def record_size(type_: int) -> int:
 def records_to_rows(records: torch.Tensor, type_: int, K: int, M: int, *, pitch: int | None = None,
                     stream=None) -> Weight:
     """Packed rows (a Weight) from M * K/32 block records (uint8 device tensor)."""
-    _need_gpu(records)
+    dev = _need_gpu(records)
     rs = row_size(type_, K)
     pitch = rs if pitch is None else pitch
     out = torch.zeros((M, pitch), dtype=torch.uint8, device=records.device)
     wt = Weight(out, type_, K, M)
-    d = wt.desc()
-    _check(lib().qmm_records_to_rows(records.data_ptr(), d, _stream(stream)),
-           "qmm_records_to_rows")
+    _launch(dev, stream, "qmm_records_to_rows", records.data_ptr(), wt._desc())
     return wt
 
 
 def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The M * K/32 block records of a quantized Weight (uint8 device tensor)."""
-    _need_gpu(w.data)
     n = w.M * (w.K // 32) * record_size(w.type)
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=w.data.device)
-    d = w.desc()
-    _check(lib().qmm_rows_to_records(d, out.data_ptr(), _stream(stream)),
-           "qmm_rows_to_records")
+    _launch(_need_gpu(w.data, out), stream, "qmm_rows_to_records", w._desc(), out.data_ptr())
     return out
 
 
 def gemm_workspace_size(w: Weight, x: torch.Tensor) -> int:
     """Bytes of workspace qmm_gemm_ws uses to split K for these shapes (0: no split)."""
-    wd, xd = w.desc(), _dense_desc(x, BF16)
-    return int(lib().qmm_gemm_workspace_size(wd, xd))
+    return int(lib().qmm_gemm_workspace_size(w._desc(), _dense(x, BF16)))
 
 
 def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
@@ -358,33 +373,24 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
     workspace: "auto" allocates the split-K workspace the shapes call for (a
     torch allocation, so it is graph-capture safe), None runs without one
     (qmm_gemm), or a uint8 device tensor to use as is."""
-    if isinstance(x, Weight):
-        _need_gpu(w.data, x.data)
-        n, dev, xd = x.M, x.data.device, x.desc()
-    else:
-        _need_gpu(w.data, x)
-        n, dev, xd = x.shape[0], x.device, _dense_desc(x, BF16)
+    xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, BF16))
     if out is None:
-        out = torch.empty((n, w.M), dtype=torch.float32, device=dev)
-    wd, yd = w.desc(), _dense_desc(out, F32)
+        out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+    dev, wd, yd = _need_gpu(w.data, xt, out), w._desc(), _dense(out, F32)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         n = int(lib().qmm_gemm_workspace_size(wd, xd))
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        workspace = torch.empty(n, dtype=torch.uint8, device=xt.device) if n else None
         if workspace is not None and stream is not None:
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
             workspace.record_stream(stream)
     if workspace is None:
-        _check(lib().qmm_gemm(wd, xd, yd, _stream(stream)),
-               "qmm_gemm")
+        _launch(dev, stream, "qmm_gemm", wd, xd, yd)
     else:
-        _need_gpu(workspace)
-        _check(lib().qmm_gemm_ws(wd, xd, yd,
-                                 workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)),
-               "qmm_gemm_ws")
+        _need_gpu(out, workspace)
+        _launch(dev, stream, "qmm_gemm_ws", wd, xd, yd, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -393,41 +399,40 @@ def gemm_noalloc(w: Weight, x: torch.Tensor, out: torch.Tensor, *, workspace_byt
     """qmm_gemm_noalloc: the GEMM with its split-K partial sums in the
     library's static scratch array (no allocation in the call; `out` is the
     caller's).  workspace_bytes defaults to the full split of these shapes."""
-    _need_gpu(w.data, x, out)
-    wd, xd, yd = w.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
+    dev, wd, xd = _need_gpu(w.data, x, out), w._desc(), _dense(x, BF16)
     if workspace_bytes is None:
         workspace_bytes = int(lib().qmm_gemm_workspace_size(wd, xd))
-    _check(lib().qmm_gemm_noalloc(wd, xd, yd,
-                                  ctypes.c_size_t(workspace_bytes), _stream(stream)), "qmm_gemm_noalloc")
+    _launch(dev, stream, "qmm_gemm_noalloc", wd, xd, _dense(out, F32), workspace_bytes)
     return out
 
 
 def gemm_swiglu(w_gate: Weight, w_up: Weight, x: torch.Tensor, *, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """h (N, M) fp32 = Swish(x W_gate'^T) * (x W_up'^T) for bf16 x (N, K), one fused launch."""
-    _need_gpu(w_gate.data, w_up.data, x)
     if out is None:
-        out = torch.empty((x.shape[0], w_gate.M), dtype=torch.float32, device=x.device)
-    gd, ud, xd, hd = w_gate.desc(), w_up.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
-    _check(lib().qmm_gemm_swiglu(gd, ud, xd, hd,
-                                 _stream(stream)), "qmm_gemm_swiglu")
+        out = torch.empty(x.shape[0], w_gate.M, dtype=torch.float32, device=x.device)
+    _launch(_need_gpu(w_gate.data, w_up.data, x, out), stream, "qmm_gemm_swiglu", w_gate._desc(), w_up._desc(),
+            _dense(x, BF16), _dense(out, F32))
     return out
 
 
 def gemm_batch(items, *, stream=None) -> list:
     """Several prefill GEMMs in one launch: items = [(Weight, x (N, K) bf16, out or None), ...]
     sharing the weight type, K and N.  Returns the outputs."""
-    descs, keep, outs = [], [], []
+    descs, keep, outs, tensors = [], [], [], []
     for w, x, out in items:
-        _need_gpu(w.data, x)
         if out is None:
-            out = torch.empty((x.shape[0], w.M), dtype=torch.float32, device=x.device)
+            out = torch.empty(x.shape[0], w.M, dtype=torch.float32, device=x.device)
+        tensors += [w.data, x, out]
         wd, xd, yd = w.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
         keep += [wd, xd, yd]
         descs.append(QmmGemmItem(ctypes.pointer(wd), ctypes.pointer(xd), ctypes.pointer(yd)))
         outs.append(out)
     arr = (QmmGemmItem * max(1, len(descs)))(*descs)
-    _check(lib().qmm_gemm_batch(arr, len(descs), _stream(stream)), "qmm_gemm_batch")
+    if tensors:
+        _launch(_need_gpu(*tensors), stream, "qmm_gemm_batch", arr, len(descs))
+    else:
+        _check(lib().qmm_gemm_batch(arr, 0, _stream(stream)), "qmm_gemm_batch")
     return outs
 
 
@@ -445,6 +450,12 @@ class Experts:
                       n_dims=3)
         t.ne[2], t.nb[2] = self.data.shape[0], self.data.stride(0) * self.data.element_size()
         return t
+
+    def _desc(self) -> bytes:
+        d = self.data
+        es, E = d.element_size(), d.shape[0]
+        nb2 = d.stride(0) * es
+        return _PACK(self.type, 3, self.K, self.M, E, 1, 0, d.stride(1) * es, nb2, nb2 * E, d.data_ptr())
 
     def expert(self, e: int) -> Weight:
         """Expert e's matrix: no copy."""
@@ -465,20 +476,16 @@ def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, str
     its logits (N, E) fp32, largest first, with softmax weights over all
     experts (ROUTE_ALL) or over the chosen ones (ROUTE_CHOSEN).  Experts
     masked by -inf are never chosen; empty slots hold id -1 and weight 0."""
-    _need_gpu(logits)
-    n = logits.shape[0]
-    ids = torch.empty((n, top_k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((n, top_k), dtype=torch.float32, device=logits.device)
-    ld = _dense_desc(logits, F32)
-    _check(lib().qmm_moe_route(ld, top_k, rule, ids.data_ptr(),
-                               weights.data_ptr(), _stream(stream)), "qmm_moe_route")
+    dev, n = _need_gpu(logits), logits.shape[0]
+    ids = torch.empty(n, top_k, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(n, top_k, dtype=torch.float32, device=logits.device)
+    _launch(dev, stream, "qmm_moe_route", _dense(logits, F32), top_k, rule, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
 def moe_workspace_size(w_gate: Experts, x: torch.Tensor, top_k: int) -> int:
     """Bytes of workspace qmm_moe_swiglu needs for these shapes."""
-    gd, xd = w_gate.desc(), _dense_desc(x, F32)
-    return int(lib().qmm_moe_workspace_size(gd, xd, top_k))
+    return int(lib().qmm_moe_workspace_size(w_gate._desc(), _dense(x, F32), top_k))
 
 
 def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor, ids: torch.Tensor,
@@ -488,15 +495,14 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
     SwiGLU block of expert ids (int32), both (N, top_k) and contiguous;
     x (N, K) fp32, N <= 8.  workspace: a uint8 device tensor of at least
     moe_workspace_size bytes, or None to allocate one (graph-capture safe)."""
-    _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights)
     top_k = ids.shape[1]
     if ids.dtype != torch.int32 or weights.dtype != torch.float32:
         raise ValueError("ids must be int32 and weights float32")
     if ids.shape != weights.shape or ids.shape[0] != x.shape[0] or not (ids.is_contiguous() and weights.is_contiguous()):
         raise ValueError("ids and weights must be contiguous and (N, top_k)")
     if out is None:
-        out = torch.empty((x.shape[0], w_down.M), dtype=torch.float32, device=x.device)
-    gd, ud, dd, xd, yd = w_gate.desc(), w_up.desc(), w_down.desc(), _dense_desc(x, F32), _dense_desc(out, F32)
+        out = torch.empty(x.shape[0], w_down.M, dtype=torch.float32, device=x.device)
+    gd, xd = w_gate._desc(), _dense(x, F32)
     if workspace is None:
         n = int(lib().qmm_moe_workspace_size(gd, xd, top_k))
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
@@ -504,11 +510,9 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
             workspace.record_stream(stream)
-    _need_gpu(workspace)
-    _check(lib().qmm_moe_swiglu(gd, ud, dd, xd,
-                                ids.data_ptr(), weights.data_ptr(), top_k,
-                                yd, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(stream)), "qmm_moe_swiglu")
+    dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)
+    _launch(dev, stream, "qmm_moe_swiglu", gd, w_up._desc(), w_down._desc(), xd, ids.data_ptr(), weights.data_ptr(), top_k,
+            _dense(out, F32), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 

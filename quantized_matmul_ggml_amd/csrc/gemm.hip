@@ -243,22 +243,30 @@ hipError_t launch_gemm_batch(const WeightView *w, const ActView *x, const OutVie
     return launch_items(w, x, y, count, plan, nullptr, stream);
 }
 
-// Raise a kernel's dynamic-LDS limit once (the attribute persists for the
-// process); later launches, including those recorded into graphs, reuse it.
+// Raise a kernel's dynamic-LDS limit once per device (the attribute persists
+// for the process); later launches, including those recorded into graphs,
+// reuse it.
 hipError_t allow_dynamic_lds(const void *fn, int bytes)
 {
+    struct Granted {
+        const void *fn;
+        int dev, bytes;
+    };
     static std::mutex mu;
-    static const void *fns[64];
-    static int granted[64];
+    static Granted granted[512];
     static int n = 0;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (fns[i] == fn && granted[i] >= bytes) return hipSuccess;
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
-    for (int i = 0; i < n; ++i)
-        if (fns[i] == fn) { granted[i] = bytes; return hipSuccess; }
-    if (n < 64) { fns[n] = fn; granted[n] = bytes; ++n; }
+    std::lock_guard<std::mutex> lock(mu);
+    Granted *known = nullptr;
+    for (int i = 0; i < n && !known; ++i)
+        if (granted[i].fn == fn && granted[i].dev == dev) known = &granted[i];
+    if (known && known->bytes >= bytes) return hipSuccess;
+    e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    if (known) known->bytes = bytes;
+    else if (n < 512) granted[n++] = {fn, dev, bytes};
     return hipSuccess;
 }
 
