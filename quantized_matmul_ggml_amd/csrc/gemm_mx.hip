@@ -9,15 +9,28 @@
 // instruction multiplies the codes, scales by 2^(s_w + s_x - 254) and adds in
 // binary32.  The order of the codes within a block does not matter, since both
 // operands have the same one, so nothing is unpacked.  Four times the bf16
-// rate per instruction, so what bounds large products is feeding it.
+// rate per instruction: 9.9 PFLOP/s of zeros and 6.0 of random codes, for which
+// the clock falls to 1.5 GHz (all CUs, registers only).
 //
 // Work split: a workgroup of WR x WC waves computes BM weight rows x BN tokens,
 // each wave TM x TN tiles of 32 x 32, so that a fragment read from LDS feeds TM
-// or TN instructions.  K advances 256 (128 code bytes and 8 scale bytes of each
-// row) per step.  Codes and scales go from memory to LDS with direct-to-LDS
-// loads, NST - 1 steps ahead, into a ring of NST stages; one barrier per step.
-// Every 16-byte unit of a row is placed by an XOR of its index with bits of the
-// row, so that the rows read together fall in different banks.
+// or TN instructions.  K advances 256 (128 code bytes, whole cache lines, and 8
+// scale bytes of each row) per step.  Codes and scales go from memory to LDS
+// with direct-to-LDS loads into a ring of NST stages, NST - 1 of them in
+// flight; one barrier per step.  The fragments of one depth of 64 are read
+// while those of the depth before are multiplied, across the barrier too, so
+// that the matrix cores do not wait for LDS.  Every 16-byte unit of a row is
+// placed by an XOR of its index with bits of the row, so that the rows read
+// together fall in different banks.
+//
+// 11008 x 4096 x 4096: 123 us (3.0 PFLOP/s).  Its 688 tiles are 2.7 rounds of
+// the chip, the matrix instructions alone take 90 us, the loads alone 74, and
+// the stores of y add 20; LDS is as busy as the matrix cores, so that what
+// overlaps is limited by both.  5632 x 2048 x 512: 11.2 us, of which 4 pass
+// before the first products and after the last.  (K steps of 128, four stages
+// deep, were slower: 64-byte pieces of lines need twice the L2's requests.  So
+// were four waves of 128 x 128 each, and fetching later steps' lines into the L2
+// changed nothing.)
 #include "gemm_common.h"
 #include "lds_load.h"
 
@@ -34,24 +47,24 @@ struct GemmMxArgs {
     int64_t M, N;
     int32_t nb;                   // 32-blocks per row
     int32_t qoff;
-    int32_t n_tiles;              // token tiles
+    int32_t m_tiles, n_tiles;     // tiles of weight rows and of tokens
     int32_t steps;                // K steps of 256
 };
+
+constexpr int kBandTiles = 5;     // token tiles of a band: 32 CUs of an XCD work on about 6 x 5 tiles
 
 template <int TM, int TN, int WR, int WC, int NST>
 struct MxTile {
     static constexpr int BM = 32 * TM * WR, BN = 32 * TN * WC, NW = WR * WC, THREADS = 64 * NW;
-    static constexpr int W_CODES = BM * 128, X_CODES = BN * 128;
-    static constexpr int W_OFF = 0, X_OFF = W_CODES, WS_OFF = X_OFF + X_CODES, XS_OFF = WS_OFF + BM * 8;
+    static constexpr int W_OFF = 0, X_OFF = BM * 128, WS_OFF = X_OFF + BN * 128, XS_OFF = WS_OFF + BM * 8;
     static constexpr int STAGE = XS_OFF + BN * 8;
     static constexpr int LDS = NST * STAGE;
     static_assert(LDS <= 160 * 1024, "one workgroup's LDS");
-    static constexpr int WL = BM / 8 / NW, XL = BN / 8 / NW;       // code loads per wave and step
-    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole code loads per wave");
-    // scale loads: one covers 32 rows (two dwords each); the waves share
-    // them, waves without one repeat the last
-    static constexpr int WSL = (BM / 32 + NW - 1) / NW, XSL = (BN / 32 + NW - 1) / NW;
-    static constexpr int LOADS = WL + XL + WSL + XSL;
+    // code loads (8 rows each) and scale loads (32 rows) per wave and step
+    static constexpr int WL = BM / 8 / NW, XL = BN / 8 / NW, SL = (BM + BN) / 32 / NW;
+    static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "an even number of whole code loads per wave");
+    static_assert(SL * 32 * NW == BM + BN, "whole scale loads per wave");
+    static constexpr int LOADS = WL + XL + SL;
     static_assert(LOADS * (NST - 1) <= 63, "vmcnt range");
 };
 
@@ -66,9 +79,13 @@ __global__ __launch_bounds__((MxTile<TM, TN, WR, WC, NST>::THREADS)) void gemm_m
     const int wr = wave % WR, wc = wave / WR;
     const int h = lane >> 5;
 
-    const int tile = xcd_order_index();
-    const int mt = __builtin_amdgcn_readfirstlane(tile / a.n_tiles);
-    const int nt = __builtin_amdgcn_readfirstlane(tile - mt * a.n_tiles);
+    // ---- the tile: bands of token tiles, weight tiles within a band, so that
+    // the tiles an XCD works on together share both operands in its L2 ----
+    const int order = xcd_order_index(), per_band = kBandTiles * a.m_tiles;
+    const int band = __builtin_amdgcn_readfirstlane(order / per_band), in_band = order - band * per_band;
+    const int left = a.n_tiles - band * kBandTiles, wide_of = left < kBandTiles ? left : kBandTiles;
+    const int mt = __builtin_amdgcn_readfirstlane(in_band / wide_of);
+    const int nt = __builtin_amdgcn_readfirstlane(band * kBandTiles + in_band - mt * wide_of);
     const int64_t m0 = (int64_t)mt * L::BM, n0 = (int64_t)nt * L::BN;
     const int rows = (int)(a.M - m0 < L::BM ? a.M - m0 : L::BM);
     const int toks = (int)(a.N - n0 < L::BN ? a.N - n0 : L::BN);
@@ -77,50 +94,78 @@ __global__ __launch_bounds__((MxTile<TM, TN, WR, WC, NST>::THREADS)) void gemm_m
     const ll_i32x4 wres = ll_rsrc(a.w + (uint64_t)m0 * a.w_pitch, (uint32_t)(rows - 1) * wp + row_bytes);
     const ll_i32x4 xres = ll_rsrc(a.x + (uint64_t)n0 * a.x_pitch, (uint32_t)(toks - 1) * xp + row_bytes);
 
-    // ---- loads: lane slot e of a row holds its unit e ^ ((row >> 1) & 7);
-    // rows and blocks that do not exist read zeros ----
-    const int nb = a.nb, qoff = a.qoff;
-    auto codes = [&](const ll_i32x4 &res, uint32_t pitch, int nrows, uint32_t dst, int i, int step) {
-        const int row = 8 * i + (lane >> 3), unit = (lane & 7) ^ ((row >> 1) & 7);
-        const int blk = 8 * step + unit;
-        ll_load<16>(res, dst + 1024u * i,
-                    row < nrows && blk < nb ? (uint32_t)row * pitch + (uint32_t)(qoff + 16 * blk) : OUT_OF_RANGE);
-    };
-    auto scales = [&](const ll_i32x4 &res, uint32_t pitch, int nrows, uint32_t dst, int i, int step) {
-        const int row = 32 * i + (lane >> 1), blk = 8 * step + 4 * (lane & 1);
-        ll_load<4>(res, dst + 256u * i, row < nrows && blk < nb ? (uint32_t)row * pitch + (uint32_t)blk : OUT_OF_RANGE);
-    };
+    // ---- loads: lane slot e of a row holds its unit e ^ ((row >> 1) & 7).  Rows
+    // that do not exist lie past the buffers' ends, and blocks that do not
+    // are sent there: both read zeros.  Of a wave's code loads the even ones
+    // and the odd ones hold the same units. ----
+    const int nb = a.nb;
+    const int lrow = lane >> 3, unit0 = (lane & 7) ^ (lrow >> 1), unit1 = unit0 ^ 4;
+    const uint32_t woff = (uint32_t)(8 * L::WL * wave + lrow) * wp + (uint32_t)a.qoff;
+    const uint32_t xoff = (uint32_t)(8 * L::XL * wave + lrow) * xp + (uint32_t)a.qoff;
+    const uint32_t woff0 = woff + 16u * unit0, woff1 = woff + 16u * unit1, xoff0 = xoff + 16u * unit0, xoff1 = xoff + 16u * unit1;
+    // scale loads: the weights', then the activations', in turn over the waves
+    const uint32_t wsoff = (uint32_t)(lane >> 1) * wp + 4u * (lane & 1), xsoff = (uint32_t)(lane >> 1) * xp + 4u * (lane & 1);
     auto issue = [&](int step) {
-        const uint32_t st = lds0 + (uint32_t)(step % NST) * L::STAGE;
+        const uint32_t st = lds0 + (uint32_t)(step % NST) * L::STAGE, k = 128u * step;
+        const bool in0 = 8 * step + unit0 < nb, in1 = 8 * step + unit1 < nb, ins = 8 * step + 4 * (lane & 1) < nb;
 #pragma unroll
-        for (int i = 0; i < L::WL; ++i) codes(wres, wp, rows, st + L::W_OFF, L::WL * wave + i, step);
-#pragma unroll
-        for (int i = 0; i < L::XL; ++i) codes(xres, xp, toks, st + L::X_OFF, L::XL * wave + i, step);
-#pragma unroll
-        for (int i = 0; i < L::WSL; ++i) {
-            const int k = L::WSL * wave + i;
-            scales(wres, wp, rows, st + L::WS_OFF, k < L::BM / 32 ? k : L::BM / 32 - 1, step);
+        for (int i = 0; i < L::WL; ++i) {
+            const uint32_t off = (i & 1 ? woff1 : woff0) + (8u * i * wp + k);
+            ll_load<16>(wres, st + L::W_OFF + 1024u * (L::WL * wave + i), (i & 1 ? in1 : in0) ? off : OUT_OF_RANGE);
         }
 #pragma unroll
-        for (int i = 0; i < L::XSL; ++i) {
-            const int k = L::XSL * wave + i;
-            scales(xres, xp, toks, st + L::XS_OFF, k < L::BN / 32 ? k : L::BN / 32 - 1, step);
+        for (int i = 0; i < L::XL; ++i) {
+            const uint32_t off = (i & 1 ? xoff1 : xoff0) + (8u * i * xp + k);
+            ll_load<16>(xres, st + L::X_OFF + 1024u * (L::XL * wave + i), (i & 1 ? in1 : in0) ? off : OUT_OF_RANGE);
+        }
+#pragma unroll
+        for (int i = 0; i < L::SL; ++i) {
+            const int n = L::SL * wave + i, nx = n - L::BM / 32;
+            const bool of_w = nx < 0;
+            const uint32_t off = (of_w ? wsoff : xsoff) + ((of_w ? 32u * n * wp : 32u * nx * xp) + 8u * step);
+            ll_load<4>(of_w ? wres : xres, st + (of_w ? L::WS_OFF + 256u * n : L::XS_OFF + 256u * nx), ins ? off : OUT_OF_RANGE);
         }
     };
 
-    // ---- fragment addresses within a stage ----
+    // ---- fragments: depth s of a stage is blocks 2 s + h ----
     const int wrow = 32 * TM * wr + (lane & 31), xrow = 32 * TN * wc + (lane & 31);
-    auto frag = [&](const uint8_t *base, int row, int s) {
-        const int unit = (2 * s + h) ^ ((row >> 1) & 7);
-        return *reinterpret_cast<const u32x4 *>(base + row * 128 + 16 * unit);
+    auto slot = [&](int s) { return 16u * (uint32_t)((2 * s + h) ^ ((lane >> 1) & 7)); };
+    struct Frags {
+        u32x4 w[TM], x[TN];
     };
-    // scale bytes of blocks h, 2 + h, 4 + h, 6 + h of a row's step
-    const uint32_t sel = h ? 0x07050301u : 0x06040200u;
-    auto scale4 = [&](const uint8_t *base, int row, uint32_t mask) {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(base + row * 8);
-        return (int)(__builtin_amdgcn_perm(v[1], v[0], sel) & mask);
+    struct RawScales {
+        u32x2 w[TM], x[TN];
+    };
+    struct Scales {
+        int w[TM], x[TN];
     };
     auto wide = [](u32x4 v) { return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; };
+    auto read = [&](Frags &f, const uint8_t *st, int s) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            f.w[i] = *reinterpret_cast<const u32x4 *>(st + L::W_OFF + (wrow + 32 * i) * 128 + slot(s));
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            f.x[j] = *reinterpret_cast<const u32x4 *>(st + L::X_OFF + (xrow + 32 * j) * 128 + slot(s));
+    };
+    auto read_scales = [&](RawScales &c, const uint8_t *st) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) c.w[i] = *reinterpret_cast<const u32x2 *>(st + L::WS_OFF + (wrow + 32 * i) * 8);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) c.x[j] = *reinterpret_cast<const u32x2 *>(st + L::XS_OFF + (xrow + 32 * j) * 8);
+    };
+    // scale bytes of blocks h, 2 + h, 4 + h, 6 + h of a row's step; those of
+    // blocks past the row may be any bytes, NaN among them, and become zeros
+    // (no branch: across one the compiler sinks the matrix instructions before it)
+    auto order_scales = [&](Scales &c, const RawScales &raw, int t) {
+        const int in = (nb - h - 8 * t + 1) >> 1;                     // blocks in the row
+        const uint32_t cut = in >= 4 ? 0u : in <= 0 ? ~0u : ~0u << (8 * in);
+        const uint32_t sel = ((h ? 0x07050301u : 0x06040200u) & ~cut) | (0x0C0C0C0Cu & cut);    // 12: a zero byte
+#pragma unroll
+        for (int i = 0; i < TM; ++i) c.w[i] = (int)__builtin_amdgcn_perm(raw.w[i][1], raw.w[i][0], sel);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) c.x[j] = (int)__builtin_amdgcn_perm(raw.x[j][1], raw.x[j][0], sel);
+    };
 
     f32x16 acc[TN][TM];
 #pragma unroll
@@ -129,41 +174,48 @@ __global__ __launch_bounds__((MxTile<TM, TN, WR, WC, NST>::THREADS)) void gemm_m
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+    auto multiply = [&](const Frags &f, const Scales &c, auto S) {
+        constexpr int s = decltype(S)::value;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(f.x[j]), wide(f.w[i]), acc[j][i], 4, 4, s, c.x[j],
+                                                                           s, c.w[i]);
+    };
+    // this wave's loads of the next step have landed and its reads of this one
+    // too, then every wave's
+    auto meet = [&] {
+        ll_wait<L::LOADS *(NST - 2)>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
 
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s) issue(s);
+    meet();
+    issue(NST - 1);
+    Frags f[2];
+    RawScales raw;
+    Scales c;
+    read(f[0], lds, 0);
+    read_scales(raw, lds);
     for (int t = 0; t < a.steps; ++t) {
-        // this wave's loads of step t have landed, then every wave's; and
-        // every wave is done with step t - 1, whose stage the next loads take
-        ll_wait<L::LOADS *(NST - 2)>();
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        issue(t + NST - 1);
-        const uint8_t *st = lds + (t % NST) * L::STAGE;
-        // scales of blocks past the row may be any bytes, NaN among them
-        uint32_t mask = 0xFFFFFFFFu;
-        if (8 * t + 8 > nb) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                if (8 * t + 2 * s + h >= nb) mask &= ~(0xFFu << (8 * s));
-        }
-        int ws[TM], xs[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) ws[i] = scale4(st + L::WS_OFF, wrow + 32 * i, mask);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) xs[j] = scale4(st + L::XS_OFF, xrow + 32 * j, mask);
+        const uint8_t *const st = lds + (t % NST) * L::STAGE, *const next = lds + ((t + 1) % NST) * L::STAGE;
+        order_scales(c, raw, t);
         static_for<4>([&](auto S) {
             constexpr int s = decltype(S)::value;
-            i32x8 wf[TM], xf[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) wf[i] = wide(frag(st + L::W_OFF, wrow + 32 * i, s));
-#pragma unroll
-            for (int j = 0; j < TN; ++j) xf[j] = wide(frag(st + L::X_OFF, xrow + 32 * j, s));
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xf[j], wf[i], acc[j][i], 4, 4, s, xs[j],
-                                                                               s, ws[i]);
+            if constexpr (s < 3) {
+                read(f[(s + 1) % 2], st, s + 1);
+            } else {
+                // every wave has read step t's stage: the step NST later takes it
+                meet();
+                issue(t + NST);
+                read(f[(s + 1) % 2], next, 0);
+                read_scales(raw, next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(f[s % 2], c, S);
+            __builtin_amdgcn_sched_barrier(0);
         });
     }
     ll_wait<0>();                  // no load may still write the LDS of a finished workgroup
@@ -190,6 +242,7 @@ hipError_t launch_tile(GemmMxArgs a, hipStream_t stream)
     using L = MxTile<TM, TN, WR, WC, NST>;
     const int64_t mt = (a.M + L::BM - 1) / L::BM, nt = (a.N + L::BN - 1) / L::BN;
     if (mt * nt >= (1ll << 31)) return hipErrorInvalidValue;
+    a.m_tiles = (int32_t)mt;
     a.n_tiles = (int32_t)nt;
     const void *fn = reinterpret_cast<const void *>(&gemm_mx_kernel<TM, TN, WR, WC, NST>);
     const hipError_t e = allow_dynamic_lds(fn, L::LDS);
@@ -212,12 +265,19 @@ hipError_t launch_gemm_mx(const WeightView &w, const ActView &x, const OutView &
     a.M = w.M;
     a.N = x.N;
     a.nb = (int32_t)(w.K / 32);
+    a.steps = (a.nb + 7) / 8;
     a.qoff = (int32_t)quant_offset(w.K, w.scale_shift);
-    a.steps = (int32_t)((w.K + 255) / 256);
-    const int64_t large = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+    
+    // 256 x 256 tiles read half the bytes of 128 x 128 ones per product, but one
+    // takes a little over twice as long: they win where the small ones need more
+    // than two rounds on the chip's CUs for each of theirs (2048-deep, us, large
+    // and small: 2048 x 2048 23.4, 12.6; 5632 x 1024 23.6, 21.2; 5632 x 2048
+    // 26.9, 33.0; 5632 x 4096 52.8, 60.2).
+    const int64_t cus = device_cus();
+    auto rounds = [&](int64_t tile) { return (((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) + cus - 1) / cus; };
     const bool offsets = 256ull * a.w_pitch < (1ull << 31) && 256ull * a.x_pitch < (1ull << 31);
-    if (offsets && large >= device_cus()) return launch_tile<2, 4, 4, 2, 2>(a, stream);
-    return launch_tile<2, 2, 2, 2, 4>(a, stream);
+    if (offsets && rounds(128) > 2 * rounds(256)) return launch_tile<2, 4, 4, 2, 2>(a, stream);
+    return launch_tile<2, 1, 2, 4, 3>(a, stream);
 }
 
 }  // namespace qmm
