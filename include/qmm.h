@@ -400,7 +400,8 @@ QMM_API int qmm_moe_route(const qmm_tensor *logits_f32, int32_t top_k, int32_t r
  * qmm_moe_route writes them, read on the device.  A slot whose id is negative
  * or not below E is empty, whatever its weight; an expert named twice by a
  * token counts with both weights; a token without experts gets zeros.
- * Every chosen expert's weights are read once.  The three products and the
+ * Tokens that choose an expert share the reads of its weights, two by two
+ * (the next two find them in the caches).  The three products and the
  * epilogue keep binary32 accuracy (the products of weights and activations
  * are exact, sums and the epilogue round); the result depends on no timing.
  * workspace: qmm_moe_workspace_size bytes (fewer: QMM_ERR_SCRATCH) of device

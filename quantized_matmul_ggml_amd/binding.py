@@ -262,6 +262,8 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
     QUANT_Q4_AMAX7 for the symmetric amax/7 Q4 rule), or MXFP4 rows (fp32 or
     bf16 w)."""
     dev = _need_gpu(w)
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("quantize takes float32 rows (or bfloat16 ones, for MXFP4)")
     M, K = w.shape
     rs = row_size(type_, K)
     pitch = rs if pitch is None else pitch
@@ -476,6 +478,8 @@ def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, str
     its logits (N, E) fp32, largest first, with softmax weights over all
     experts (ROUTE_ALL) or over the chosen ones (ROUTE_CHOSEN).  Experts
     masked by -inf are never chosen; empty slots hold id -1 and weight 0."""
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError("logits must be float32 (N, E)")
     dev, n = _need_gpu(logits), logits.shape[0]
     ids = torch.empty(n, top_k, dtype=torch.int32, device=logits.device)
     weights = torch.empty(n, top_k, dtype=torch.float32, device=logits.device)
@@ -495,13 +499,15 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
     SwiGLU block of expert ids (int32), both (N, top_k) and contiguous;
     x (N, K) fp32, N <= 8.  workspace: a uint8 device tensor of at least
     moe_workspace_size bytes, or None to allocate one (graph-capture safe)."""
-    top_k = ids.shape[1]
-    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
-        raise ValueError("ids must be int32 and weights float32")
-    if ids.shape != weights.shape or ids.shape[0] != x.shape[0] or not (ids.is_contiguous() and weights.is_contiguous()):
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or x.dtype != torch.float32:
+        raise ValueError("ids must be int32, weights and x float32")
+    if ids.dim() != 2 or x.dim() != 2 or ids.shape != weights.shape or ids.shape[0] != x.shape[0] or not (ids.is_contiguous() and weights.is_contiguous()):
         raise ValueError("ids and weights must be contiguous and (N, top_k)")
+    top_k = ids.shape[1]
     if out is None:
         out = torch.empty(x.shape[0], w_down.M, dtype=torch.float32, device=x.device)
+    elif out.dtype != torch.float32:
+        raise ValueError("out must be float32")
     gd, xd = w_gate._desc(), _dense(x, F32)
     if workspace is None:
         n = int(lib().qmm_moe_workspace_size(gd, xd, top_k))

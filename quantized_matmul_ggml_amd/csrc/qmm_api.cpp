@@ -445,7 +445,7 @@ const char *qmm_strerror(int status)
     case QMM_ERR_ALIAS: return "the output overlaps an input";
     case QMM_ERR_UNSUPPORTED: return "unsupported tensor rank or size";
     case QMM_ERR_DEVICE: return "the HIP runtime refused the launch";
-    case QMM_ERR_SCRATCH: return "the call needs more scratch memory than the library's static array holds";
+    case QMM_ERR_SCRATCH: return "the call needs more scratch memory than the library's static array or the workspace holds";
     default: return "unknown qmm status";
     }
 }

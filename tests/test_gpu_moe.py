@@ -97,6 +97,22 @@ def test_moe_swiglu(kind, E, k, N, K, F, M):
     _check(y, ref, bound, kind)
 
 
+@pytest.mark.parametrize("kind,K", [("mxfp4", 2080), ("q4_0", 2080), ("q4_b64", 2112), ("q8_0", 1056), ("q8_b64", 1088)])
+def test_moe_many_tiles(kind, K):
+    """Enough tiles that a wave keeps eight units in flight, with rows that end
+    inside the last ones, and experts with one to eight pairs."""
+    E, k, N, F, M = 12, 6, 8, 704, 24
+    print(f"[case] moe many tiles {kind} K {K}", flush=True)
+    rng = np.random.default_rng(K)
+    (g, u, d), (G, U, D) = _layer(rng, kind, E, K, F, M, pad=32)
+    x = (rng.standard_normal((N, K)) * 0.05 + 0.01).astype(np.float32)
+    ids = np.stack([np.concatenate([[0], 1 + rng.permutation(E - 1)[:k - 1]]) for _ in range(N)]).astype(np.int32)
+    w = rng.uniform(-0.2, 1, (N, k)).astype(np.float32)
+    ref, bound = R.moe(G, U, D, x.astype(np.float64), ids, w)
+    y = Q.moe_swiglu(g, u, d, torch.from_numpy(x).to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(w).to(DEV))
+    _check(y, ref, bound, kind)
+
+
 @pytest.mark.parametrize("kind", ["mxfp4", "q4_0", "q8_0"])
 def test_moe_empty_and_repeated_slots(kind):
     """Ids outside the range are empty slots (whatever their weight), a token
@@ -241,3 +257,20 @@ def test_binding_refuses_mismatches():
     with pytest.raises(Q.QmmError) as e:
         Q.moe_swiglu(g, u, d, x, ids, w, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == B.ERR_SCRATCH
+
+
+def test_binding_refuses_other_types():
+    (g, u, d), _ = _layer(np.random.default_rng(0), "q4_0", 2, 64, 64, 8)
+    x, ids, w = torch.zeros((1, 64), device=DEV), torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV)
+    with pytest.raises(ValueError):
+        Q.moe_route(x.bfloat16(), 1)
+    with pytest.raises(ValueError):
+        Q.moe_route(x[0], 1)
+    with pytest.raises(ValueError):
+        Q.moe_swiglu(g, u, d, x.half(), ids, w)
+    with pytest.raises(ValueError):
+        Q.moe_swiglu(g, u, d, x, ids[0], w[0])
+    with pytest.raises(ValueError):
+        Q.moe_swiglu(g, u, d, x, ids, w, out=torch.empty((1, 8), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        Q.quantize(x.half(), Q.MXFP4)

@@ -123,6 +123,24 @@ def test_gemv(M, K):
         _check(y, x @ W.T, np.abs(x) @ np.abs(W).T, K, f"N {N}", norm=False)
 
 
+@pytest.mark.parametrize("M,K,N", [(70001, 160, 1), (70001, 160, 8), (70001, 1056, 3), (33000, 5664, 2), (33000, 2080, 7)])
+def test_gemv_more_tiles_than_workgroups(M, K, N):
+    """Workgroups take several tiles each, with one and with several passes over
+    K; rows at both ends and in between against the reference."""
+    print(f"[case] mxfp4 gemv {M}x{K} N {N}", flush=True)
+    rng = np.random.default_rng(M + K + N)
+    some = R.random_rows(rng, "mxfp4", (97,), K)
+    at = np.unique(np.concatenate([np.arange(40), np.arange(M - 40, M), rng.integers(0, M, 400)]))
+    rows = some[np.arange(M) % 97]
+    w, W = _weight(rows, K), R.values(some, "mxfp4", K)[at % 97]
+    x = rng.standard_normal((N, K)).astype(np.float32)
+    y = Q.gemv(w, torch.from_numpy(x).to(DEV))
+    x = x.astype(np.float64)
+    _check(y[:, torch.from_numpy(at).to(DEV)], x @ W.T, np.abs(x) @ np.abs(W).T, K, "some rows", norm=False)
+    # the rows repeat, and so do the results, bit for bit
+    assert torch.equal(y[:, :M - 97], y[:, 97:])
+
+
 def test_gemv_relative_error():
     """Gaussian activations: the relative error of the whole product."""
     print("[case] mxfp4 gemv relative error", flush=True)
