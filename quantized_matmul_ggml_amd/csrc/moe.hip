@@ -354,7 +354,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a)
     const int last_q = (a.nb2 - 1) / QB;
     const __amdgpu_buffer_rsrc_t hres = __builtin_amdgcn_make_buffer_rsrc(
         a.h, 0, (int)((uint32_t)P * (uint32_t)a.h_pair), BUFFER_FLAGS);
-    constexpr int D = 3;
+    constexpr int D = 2;                         // items in flight (three or four: no faster)
     uint4 part[D][NA];
     Unit<WT, SS> z[D];
     // The wave takes items wave, wave + 16, ...: entry n, step p.  Two cursors
