@@ -272,9 +272,14 @@ hipError_t launch_gemm_mx(const WeightView &w, const ActView &x, const OutView &
     // takes a little over twice as long: they win where the small ones need more
     // than two rounds on the chip's CUs for each of theirs (2048-deep, us, large
     // and small: 2048 x 2048 23.4, 12.6; 5632 x 1024 23.6, 21.2; 5632 x 2048
-    // 26.9, 33.0; 5632 x 4096 52.8, 60.2).
+    // 26.9, 33.0; 5632 x 4096 52.8, 60.2).  A step of a 64 x 64 tile takes half a
+    // step of a 128 x 128 one, and three fit a CU: they win up to two a CU (us, 64
+    // and 128: 2048 x 5632 x 512 13.9, 23.6; 2048 x 2048 x 100 5.7, 8.7;
+    // 5632 x 2048 x 256 9.1, 10.3; 5632 x 2048 x 512 14.0, 11.4).
     const int64_t cus = device_cus();
-    auto rounds = [&](int64_t tile) { return (((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) + cus - 1) / cus; };
+    auto tiles = [&](int64_t size) { return ((a.M + size - 1) / size) * ((a.N + size - 1) / size); };
+    auto rounds = [&](int64_t size) { return (tiles(size) + cus - 1) / cus; };
+    if (tiles(64) <= 2 * cus) return launch_tile<1, 1, 2, 2, 3>(a, stream);
     const bool offsets = 256ull * a.w_pitch < (1ull << 31) && 256ull * a.x_pitch < (1ull << 31);
     if (offsets && rounds(128) > 2 * rounds(256)) return launch_tile<2, 4, 4, 2, 2>(a, stream);
     return launch_tile<2, 1, 2, 4, 3>(a, stream);

@@ -294,6 +294,12 @@ def test_gemm_mx(M, K, N):
         _check(y, ref, a, K, "mx noalloc")
 
 
+@pytest.mark.parametrize("M,K,N", [(1700, 544, 1500), (1701, 96, 1499), (1650, 2080, 1590), (1537, 32, 1537)])
+def test_gemm_mx_middle_sizes(M, K, N):
+    """Enough tiles of 64 x 64 for tiles of 128 x 128, too few for 256 x 256."""
+    test_gemm_mx(M, K, N)
+
+
 def test_gemm_mx_extreme_scales():
     """Scales at both ends of the range: products of 2^-127 and 2^127."""
     print("[case] mxfp4 gemm mx extreme scales", flush=True)
