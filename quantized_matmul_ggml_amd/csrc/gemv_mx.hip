@@ -32,18 +32,17 @@ struct alignas(64) MxItem {
     int32_t M;
     int32_t n_groups;         // tile groups (16 / S tiles each)
     int32_t wgs;              // workgroups of this item (grid x)
-    int32_t pad;
+    int32_t N;                // tokens
 };
 static_assert(sizeof(MxItem) == 64, "one 64-byte record per item");
 
 struct MxArgs {
-    int32_t N;
     int32_t nb;               // 32-blocks per row
     int32_t qoff;
     int32_t steps;            // units (HALF: pairs of units) per row
     int32_t s_log2;           // waves per tile
     int32_t pass;             // steps per pass over K (a multiple of S, or all)
-    int32_t pad[10];
+    int32_t pad[11];
     MxItem item[QMM_GEMV_BATCH_MAX];
 };
 
@@ -63,7 +62,7 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
     float *const Y = it.y;
     const uint32_t pitch = it.pitch, pitch2 = it.pitch2, x_pitch = it.x_pitch, y_pitch = it.y_pitch;
     const int M = it.M, n_groups = it.n_groups, wgs = it.wgs;
-    const int N = a.N, nb = a.nb, qoff = a.qoff, steps = a.steps, s_log2 = a.s_log2, pass = a.pass;
+    const int N = it.N, nb = a.nb, qoff = a.qoff, steps = a.steps, s_log2 = a.s_log2, pass = a.pass;
     if ((int)blockIdx.x >= wgs) return;
 
     const int threads = blockDim.x, waves = threads >> 6;
@@ -196,7 +195,8 @@ Kernel pick(int depth)
 
 hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStream_t stream)
 {
-    const int64_t K = tasks[0].w.K, N = tasks[0].x.N;
+    const int64_t K = tasks[0].w.K;
+    int64_t N = tasks[0].x.N;
     const bool sw = up != nullptr;
     int64_t full = 0, half = 0;
     for (int i = 0; i < count; ++i) {
@@ -204,10 +204,21 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
         half += (tasks[i].w.M + 7) / 8;
     }
     if (half == 0 || N == 0) return hipSuccess;
+    // With tiles for no more than half the CUs, every workgroup's reading and
+    // splitting of all the activations is what takes the time, and half the
+    // tokens each in twice the workgroups is faster although the weights are
+    // read twice, once from the caches (us, whole and halved: 2047 x 5632, eight
+    // tokens 11.0, 7.9; 2048 x 2048, eight 5.8, 4.3; 2048 x 5632, four 8.1, 5.7,
+    // two 5.9, 5.1; but 11008 x 4096, eight 19.1, 26.7).
+    const bool halve = N > 1 && 2 * (sw ? half : full) <= device_cus() && 2 * count <= QMM_GEMV_BATCH_MAX;
+    const int parts = halve ? 2 : 1;
+    const int64_t all = N;
+    N = (N + parts - 1) / parts;
+    full *= parts;
+    half *= parts;
     const RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N, (int)N);
     const int rows = sw || p.half ? 8 : 16, T = p.waves >> p.s_log2, tg = N > 4 ? 2 : 1;
     MxArgs a = {};
-    a.N = (int32_t)N;
     a.nb = (int32_t)(K / 32);
     a.qoff = (int32_t)quant_offset(K, 1);
     a.steps = p.steps;
@@ -218,21 +229,24 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
     const int per_cu = 16 / p.waves;
     const int64_t cap = (int64_t)per_cu * device_cus();
     int64_t total = 0, widest = 0;
-    for (int i = 0; i < count; ++i) total += ((tasks[i].w.M + rows - 1) / rows + T - 1) / T;
+    for (int i = 0; i < count; ++i) total += parts * (((tasks[i].w.M + rows - 1) / rows + T - 1) / T);
     int n = 0;
-    for (int i = 0; i < count; ++i) {
-        if (tasks[i].w.M == 0) continue;
+    for (int i = 0; i < parts * count; ++i) {
+        const GemvTask &t = tasks[i / parts];
+        const int64_t from = N * (i % parts);
+        if (t.w.M == 0 || from >= all) continue;
         MxItem &it = a.item[n++];
-        it.w = tasks[i].w.base;
-        it.pitch = (uint32_t)tasks[i].w.pitch;
+        it.w = t.w.base;
+        it.pitch = (uint32_t)t.w.pitch;
         it.w2 = sw ? up->base : it.w;
         it.pitch2 = sw ? (uint32_t)up->pitch : it.pitch;
-        it.x = static_cast<const float *>(tasks[i].x.data);
-        it.x_pitch = (uint32_t)tasks[i].x.pitch_elems;
-        it.y = tasks[i].y.data;
-        it.y_pitch = (uint32_t)tasks[i].y.pitch_elems;
-        it.M = (int32_t)tasks[i].w.M;
-        it.n_groups = (int32_t)(((tasks[i].w.M + rows - 1) / rows + T - 1) / T);
+        it.x = static_cast<const float *>(t.x.data) + (uint64_t)from * t.x.pitch_elems;
+        it.x_pitch = (uint32_t)t.x.pitch_elems;
+        it.y = t.y.data + (uint64_t)from * t.y.pitch_elems;
+        it.y_pitch = (uint32_t)t.y.pitch_elems;
+        it.M = (int32_t)t.w.M;
+        it.N = (int32_t)(all - from < N ? all - from : N);
+        it.n_groups = (int32_t)(((t.w.M + rows - 1) / rows + T - 1) / T);
         int64_t wgs = it.n_groups;
         if (total > cap) {
             wgs = wgs * cap / total;

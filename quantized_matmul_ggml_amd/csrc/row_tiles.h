@@ -513,7 +513,9 @@ struct RowPlan {
 // choosing four of sixteen experts of 1408 x 2048: 25.2 us with four waves a
 // tile, 27.0 with two, 29.4 with one).  With two token groups a unit is twice
 // the work and two units will do (5632 x 2048 for eight tokens: 6.0 us with
-// eight waves a tile, 6.8 with four).  Where a launch has so few tiles that most
+// eight waves a tile, 6.8 with four), and so they will with several tokens and
+// no more tiles than CUs (256 tiles of 5632 for two tokens: 5.7 us with
+// sixteen waves a tile, 7.2 with eight).  Where a launch has so few tiles that most
 // of the chip idles even so, tiles of eight rows and pairs of units double
 // them (2048 x 5632 for one token: 4.4 us against 4.9; 5632 x 2048, whose 352
 // tiles are enough, 5.0 against 4.4).  Workgroups are small (four waves) while
@@ -529,7 +531,7 @@ inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tile
         while (s < 4 && t << s < 16 * cus && steps >> (s + 1) >= least) ++s;
         return s;
     };
-    p.s_log2 = share(tiles, steps_of(0), tokens > 4 ? 2 : 4);
+    p.s_log2 = share(tiles, steps_of(0), tokens > 4 || (tokens > 1 && tiles <= cus) ? 2 : 4);
     if (half_tiles && tokens <= 4 && tiles << p.s_log2 < 5 * cus) {
         p.half = 1;
         p.s_log2 = share(half_tiles, steps_of(1), 2);
