@@ -209,14 +209,30 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
     // tokens each in twice the workgroups is faster although the weights are
     // read twice, once from the caches (us, whole and halved: 2047 x 5632, eight
     // tokens 11.0, 7.9; 2048 x 2048, eight 5.8, 4.3; 2048 x 5632, four 8.1, 5.7,
-    // two 5.9, 5.1; but 11008 x 4096, eight 19.1, 26.7).
-    const bool halve = N > 1 && 2 * (sw ? half : full) <= device_cus() && 2 * count <= QMM_GEMV_BATCH_MAX;
+    // two 5.9, 5.1; but 32000 x 2048, eight 11.3, 13.8).
+    // The same where the image of half the tokens holds all of K and that of all
+    // of them does not, since every tile group would build it again for each
+    // pass (11008 x 4096, eight tokens 18.9, 11.3; 32000 x 4096 25.7, 20.2).
+    const int64_t token = (K + 127) / 128 * 4 * kImageBytes;
+    const bool few = 2 * (sw ? half : full) <= device_cus(), fits = N * token > kImageMost && (N + 1) / 2 * token <= kImageMost;
+    const bool halve = N > 1 && (few || fits) && 2 * count <= QMM_GEMV_BATCH_MAX;
     const int parts = halve ? 2 : 1;
     const int64_t all = N;
     N = (N + parts - 1) / parts;
     full *= parts;
     half *= parts;
-    const RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N, (int)N);
+    RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N, (int)N);
+    // One more split of the tiles where the workgroups' last round is mostly
+    // empty otherwise (11008 x 4096 for eight tokens in two halves: 344 groups of
+    // four tiles on 256 CUs 13.9 us, 688 of two 11.3).
+    auto busy = [&](int s_log2) {
+        const int64_t held = 16 / p.waves * (int64_t)device_cus(), tiles = p.half ? half : sw ? half : full;
+        const int64_t groups = (tiles * (1 << s_log2) + p.waves - 1) / p.waves;
+        return (double)groups / (double)((groups + held - 1) / held * held);
+    };
+    const bool one_pass = p.image >= (int64_t)p.steps * p.step_bytes * N;
+    if (one_pass && 2 << p.s_log2 <= p.waves && p.steps >> (p.s_log2 + 1) >= 4 && busy(p.s_log2 + 1) > 1.2 * busy(p.s_log2))
+        ++p.s_log2;
     const int rows = sw || p.half ? 8 : 16, T = p.waves >> p.s_log2, tg = N > 4 ? 2 : 1;
     MxArgs a = {};
     a.nb = (int32_t)(K / 32);

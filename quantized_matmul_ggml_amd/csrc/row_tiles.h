@@ -520,7 +520,10 @@ struct RowPlan {
 // them (2048 x 5632 for one token: 4.4 us against 4.9; 5632 x 2048, whose 352
 // tiles are enough, 5.0 against 4.4).  Workgroups are small (four waves) while
 // their image is, so that several share a CU and one's loads run beside
-// another's setup; with more tokens a larger workgroup shares one image.
+// another's setup; with more tokens a larger workgroup shares one image, and so
+// it does where a larger one's image then holds all of K (11008 x 4096 for four
+// tokens: 9.4 us with sixteen waves, 13.4 with eight and two passes).
+constexpr int kImageMost = 112 * 1024;
 inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens, int likely)
 {
     const int64_t cus = device_cus();
@@ -538,7 +541,10 @@ inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tile
     }
     p.waves = likely <= 2 ? 4 : likely <= 4 ? 8 : 16;
     if (p.waves < 1 << p.s_log2) p.waves = 1 << p.s_log2;
-    auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : 112 * 1024; };
+    auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : kImageMost; };
+    const int64_t whole = (int64_t)steps_of(p.half) * (1 + p.half) * mf * kImageBytes * tokens;
+    if (likely == tokens && whole > budget() && whole <= kImageMost)
+        while (whole > budget()) p.waves *= 2;
     // one step of every wave of a tile has to fit the image
     for (;;) {
         p.step_bytes = (1 + p.half) * mf * kImageBytes;
