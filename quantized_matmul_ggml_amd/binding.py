@@ -220,6 +220,9 @@ def _dense(t: torch.Tensor, type_: int) -> bytes:
 # The current stream's handle without building a Stream object (2.8 us less per
 # call), where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device, for callers that hold a tensor of a GPU (so that torch's
+# own check that the GPU is initialised is not needed).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
@@ -233,7 +236,7 @@ def _stream(stream) -> int:
 def _launch(dev: int, stream, name: str, *args):
     """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
     stream; raises what it refuses."""
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _launch(dev, stream, name, *args)
     if stream is not None:
