@@ -47,6 +47,7 @@ class QmmTensor(ctypes.Structure):
 
 _PACK = struct.Struct("=ii4q4QQ").pack      # the fields of QmmTensor
 _ELEM = {F32: 4, F16: 2, BF16: 2}
+_DTYPE = {F32: torch.float32, F16: torch.float16, BF16: torch.bfloat16}
 _U64 = (1 << 64) - 1
 assert struct.calcsize("=ii4q4QQ") == ctypes.sizeof(QmmTensor)
 
@@ -204,7 +205,11 @@ def _dense_desc(t: torch.Tensor, type_: int) -> QmmTensor:
 
 
 def _dense(t: torch.Tensor, type_: int) -> bytes:
-    """_dense_desc's bytes."""
+    """_dense_desc's bytes.  The element type is checked here: a descriptor
+    says nothing of how many bytes its memory holds, so that the library would
+    read or write past the end of a narrower tensor."""
+    if t.dtype is not _DTYPE[type_]:
+        raise ValueError(f"expected a {_DTYPE[type_]} tensor, not {t.dtype}")
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     es = t.element_size()

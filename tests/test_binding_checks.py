@@ -1,0 +1,52 @@
+"""What the Python binding refuses before anything is launched, on the CPU:
+the launch itself and the check for GPU tensors are replaced, so that a call
+which gets past the binding's own checks fails the test."""
+import pytest
+import torch
+
+import quantized_matmul_ggml_amd as Q
+from quantized_matmul_ggml_amd import binding as B
+
+
+@pytest.fixture
+def no_launch(monkeypatch, qmm_lib):
+    def launch(dev, stream, name, *args):
+        pytest.fail(f"{name} was launched")
+
+    monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
+    monkeypatch.setattr(B, "_launch", launch)
+
+
+def _weight(type_=B.MXFP4, K=64, M=32):
+    return B.Weight(torch.zeros((M, B.row_size(type_, K)), dtype=torch.uint8), type_, K, M)
+
+
+# ----------------------------------------------------------- element types
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+@pytest.mark.parametrize("N", [1, 4])
+def test_element_types(no_launch, N):
+    """Operands of another element type, of one row too (whose pitch the
+    library does not look at)."""
+    w, K, M = _weight(), 64, 32
+    x = {t: torch.zeros((N, K), dtype=t) for t in (F32, F16, BF16, torch.float64)}
+    y = {t: torch.zeros((N, M), dtype=t) for t in (F32, F16, BF16)}
+    calls = []
+    for t in (F16, BF16, torch.float64):
+        calls += [lambda t=t: Q.gemv(w, x[t]), lambda t=t: Q.gemv_swiglu(w, w, x[t]), lambda t=t: Q.gemv_batch([(w, x[t], None)])]
+    for t in (F32, F16):
+        calls += [lambda t=t: Q.gemm(w, x[t]), lambda t=t: Q.gemm(w, x[t], workspace=None), lambda t=t: Q.gemm_swiglu(w, w, x[t]),
+                  lambda t=t: Q.gemm_batch([(w, x[t], None)]), lambda t=t: Q.gemm_noalloc(w, x[t], y[F32]),
+                  lambda t=t: Q.gemm_workspace_size(w, x[t])]
+    for t in (F16, BF16):
+        calls += [lambda t=t: Q.gemv(w, x[F32], out=y[t]), lambda t=t: Q.gemv_swiglu(w, w, x[F32], out=y[t]),
+                  lambda t=t: Q.gemv_batch([(w, x[F32], y[t])]), lambda t=t: Q.gemm(w, x[BF16], out=y[t]),
+                  lambda t=t: Q.gemm(w, x[BF16], out=y[t], workspace=None), lambda t=t: Q.gemm_swiglu(w, w, x[BF16], out=y[t]),
+                  lambda t=t: Q.gemm_batch([(w, x[BF16], y[t])]), lambda t=t: Q.gemm_noalloc(w, x[BF16], y[t]),
+                  lambda t=t: Q.gemv(w, _weight(B.Q8_0, K, N), out=y[t]),
+                  lambda t=t: Q.dequantize(_weight(M=N), out=torch.zeros((N, K), dtype=t))]
+    for call in calls:
+        with pytest.raises(ValueError, match="expected a torch.(float32|bfloat16) tensor"):
+            call()
