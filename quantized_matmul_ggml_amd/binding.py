@@ -199,6 +199,25 @@ def _need_gpu(*ts: torch.Tensor) -> int:
     return dev
 
 
+def _need_bytes(t: torch.Tensor, nbytes: int, what: str):
+    """Refuses a buffer that is not one run of at least nbytes bytes (a strided
+    or expanded tensor's memory is not all its own, nor as much as its elements)."""
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{what} holds fewer than {nbytes} bytes")
+
+
+def _row_pitch(pitch: int | None, row_bytes: int) -> int:
+    """The pitch of packed rows to make: a single row's, too, holds the row (the
+    library does not look at it)."""
+    if pitch is None:
+        return row_bytes
+    if pitch < row_bytes:
+        raise ValueError(f"a pitch of {pitch} bytes is below the row's {row_bytes}")
+    return pitch
+
+
 def _dense_desc(t: torch.Tensor, type_: int) -> QmmTensor:
     """2-D row-major torch tensor (rows, cols) -> ne = [cols, rows]."""
     return QmmTensor.from_buffer_copy(_dense(t, type_))
@@ -274,7 +293,7 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
         raise ValueError("quantize takes float32 rows (or bfloat16 ones, for MXFP4)")
     M, K = w.shape
     rs = row_size(type_, K)
-    pitch = rs if pitch is None else pitch
+    pitch = _row_pitch(pitch, rs)
     out = torch.empty(M, pitch, dtype=torch.uint8, device=w.device)
     if pitch > rs:
         out[:, rs:].zero_()
@@ -353,8 +372,8 @@ def records_to_rows(records: torch.Tensor, type_: int, K: int, M: int, *, pitch:
                     stream=None) -> Weight:
     """Packed rows (a Weight) from M * K/32 block records (uint8 device tensor)."""
     dev = _need_gpu(records)
-    rs = row_size(type_, K)
-    pitch = rs if pitch is None else pitch
+    pitch = _row_pitch(pitch, row_size(type_, K))
+    _need_bytes(records, M * (K // 32) * record_size(type_), "records")
     out = torch.zeros((M, pitch), dtype=torch.uint8, device=records.device)
     wt = Weight(out, type_, K, M)
     _launch(dev, stream, "qmm_records_to_rows", records.data_ptr(), wt._desc())
@@ -366,6 +385,7 @@ def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) 
     n = w.M * (w.K // 32) * record_size(w.type)
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=w.data.device)
+    _need_bytes(out, n, "out")
     _launch(_need_gpu(w.data, out), stream, "qmm_rows_to_records", w._desc(), out.data_ptr())
     return out
 
@@ -400,6 +420,7 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
         _launch(dev, stream, "qmm_gemm", wd, xd, yd)
     else:
         _need_gpu(out, workspace)
+        _need_bytes(workspace, 0, "workspace")
         _launch(dev, stream, "qmm_gemm_ws", wd, xd, yd, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
@@ -524,6 +545,8 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
             # freed when this call returns: keep the allocator from handing it
             # out again before the kernels on `stream` have run
             workspace.record_stream(stream)
+    else:
+        _need_bytes(workspace, 0, "workspace")
     dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)
     _launch(dev, stream, "qmm_moe_swiglu", gd, w_up._desc(), w_down._desc(), xd, ids.data_ptr(), weights.data_ptr(), top_k,
             _dense(out, F32), workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -550,8 +573,8 @@ def stream_read(src: torch.Tensor, sink: torch.Tensor, *, nbytes: int | None = N
     tensor src; sink: an int32 device tensor of at least `workgroups` words."""
     _need_gpu(src, sink)
     n = src.numel() * src.element_size() if nbytes is None else nbytes
-    if sink.numel() * sink.element_size() < 4 * workgroups:
-        raise ValueError("sink holds fewer words than workgroups")
+    _need_bytes(src, n, "src")
+    _need_bytes(sink, 4 * workgroups, "sink")
     _check(lib().qmm_stream_read(ctypes.c_void_p(src.data_ptr()), ctypes.c_size_t(n),
                                  ctypes.c_void_p(sink.data_ptr()), workgroups, _stream(stream)),
            "qmm_stream_read")

@@ -50,3 +50,43 @@ def test_element_types(no_launch, N):
     for call in calls:
         with pytest.raises(ValueError, match="expected a torch.(float32|bfloat16) tensor"):
             call()
+
+
+# ---------------------------------------------------- sizes the caller gives
+
+def test_pitch_below_the_row(no_launch):
+    for type_ in (B.MXFP4, B.Q4_0, B.Q8_0):
+        rs = Q.row_size(type_, 64)
+        for M in (1, 3):
+            with pytest.raises(ValueError, match="below the row"):
+                Q.quantize(torch.zeros((M, 64)), type_, pitch=rs - 16)
+            if type_ != B.MXFP4:
+                with pytest.raises(ValueError, match="below the row"):
+                    Q.records_to_rows(torch.zeros(1 << 12, dtype=torch.uint8), type_, 64, M, pitch=rs - 16)
+
+
+def test_buffers_too_small_or_with_holes(no_launch):
+    w = _weight(B.Q4_0)
+    n = 32 * 2 * 18
+    byte = lambda k: torch.zeros(k, dtype=torch.uint8)
+    wide = byte(4 * n).view(n, 4)[:, 0]                 # n bytes, four apart
+    one = byte(1).expand(n)
+    for bad in (byte(n - 1), wide, one):
+        with pytest.raises(ValueError, match="records"):
+            Q.records_to_rows(bad, B.Q4_0, 64, 32)
+        with pytest.raises(ValueError, match="out"):
+            Q.rows_to_records(w, out=bad)
+    sink = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError, match="src"):
+        Q.stream_read(byte(64), sink, nbytes=80, workgroups=8)
+    with pytest.raises(ValueError, match="src"):
+        Q.stream_read(wide, sink, workgroups=8)
+    with pytest.raises(ValueError, match="sink"):
+        Q.stream_read(byte(64), sink, workgroups=9)
+    x = torch.zeros((4, 64), dtype=BF16)
+    for ws in (wide, one):
+        with pytest.raises(ValueError, match="workspace"):
+            Q.gemm(w, x, workspace=ws)
+        ex = Q.Experts(torch.zeros((2, 64, Q.row_size(B.Q4_0, 64)), dtype=torch.uint8), B.Q4_0, 64, 64)
+        with pytest.raises(ValueError, match="workspace"):
+            Q.moe_swiglu(ex, ex, ex, x.float(), torch.zeros((4, 1), dtype=torch.int32), torch.zeros((4, 1)), workspace=ws)
