@@ -160,6 +160,11 @@ def _packed(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int) -> bytes:
     return _PACK(type_, 2, ne0, ne1, 1, 1, _ELEM.get(type_, 0), nb1, nb2, nb2, data_ptr)
 
 
+# The library checks a descriptor's sizes against each other, not against the
+# memory behind them: neither a single row's pitch nor the end of the last row.
+_DATA = "data must hold M rows of K packed weights, each contiguous"
+
+
 @dataclass
 class Weight:
     """A weight matrix W (ne = [K, M]): M rows of K weights on the GPU.
@@ -176,11 +181,14 @@ class Weight:
         return self.data.stride(0) * self.data.element_size()
 
     def desc(self) -> QmmTensor:
-        return make_desc(self.type, self.K, self.M, self.pitch, self.data.data_ptr())
+        return QmmTensor.from_buffer_copy(self._desc())
 
     def _desc(self) -> bytes:
-        d = self.data
-        return _packed(self.type, self.K, self.M, d.stride(0) * d.element_size(), d.data_ptr())
+        d, M = self.data, self.M
+        (pitch, step), (rows, cols), es = d.stride(), d.shape, d.element_size()
+        if step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K):
+            raise ValueError(_DATA)
+        return _packed(self.type, self.K, M, pitch * es, d.data_ptr())
 
     def rows(self, r0: int, r1: int) -> "Weight":
         """Row-range view [r0, r1): no copy, same pitch."""
@@ -477,16 +485,15 @@ class Experts:
     M: int
 
     def desc(self) -> QmmTensor:
-        t = make_desc(self.type, self.K, self.M, self.data.stride(1) * self.data.element_size(), self.data.data_ptr(),
-                      n_dims=3)
-        t.ne[2], t.nb[2] = self.data.shape[0], self.data.stride(0) * self.data.element_size()
-        return t
+        return QmmTensor.from_buffer_copy(self._desc())
 
     def _desc(self) -> bytes:
-        d = self.data
-        es, E = d.element_size(), d.shape[0]
-        nb2 = d.stride(0) * es
-        return _PACK(self.type, 3, self.K, self.M, E, 1, 0, d.stride(1) * es, nb2, nb2 * E, d.data_ptr())
+        d, M = self.data, self.M
+        (apart, pitch, step), (E, rows, cols), es = d.stride(), d.shape, d.element_size()
+        if step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K):
+            raise ValueError(_DATA)
+        nb2 = apart * es
+        return _PACK(self.type, 3, self.K, M, E, 1, 0, pitch * es, nb2, nb2 * E, d.data_ptr())
 
     def expert(self, e: int) -> Weight:
         """Expert e's matrix: no copy."""

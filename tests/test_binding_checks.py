@@ -90,3 +90,29 @@ def test_buffers_too_small_or_with_holes(no_launch):
         ex = Q.Experts(torch.zeros((2, 64, Q.row_size(B.Q4_0, 64)), dtype=torch.uint8), B.Q4_0, 64, 64)
         with pytest.raises(ValueError, match="workspace"):
             Q.moe_swiglu(ex, ex, ex, x.float(), torch.zeros((4, 1), dtype=torch.int32), torch.zeros((4, 1)), workspace=ws)
+
+
+def test_weights_that_their_data_does_not_hold(no_launch):
+    """More rows than the data has (a row range past the end among them), a
+    single row or rows of a view that are shorter than K weights, and elements that are apart."""
+    K, x = 64, torch.zeros((1, 64))
+    rs = Q.row_size(B.MXFP4, K)
+    data = torch.zeros((32, rs), dtype=torch.uint8)
+    apart = torch.zeros((32, 2 * rs), dtype=torch.uint8)[:, ::2]
+    for w in (B.Weight(data, B.MXFP4, K, 33), B.Weight(data, B.MXFP4, K, 32).rows(8, 40), B.Weight(data[:1, :16], B.MXFP4, K, 1),
+              B.Weight(data[:, :rs - 16], B.MXFP4, K, 32), B.Weight(apart, B.MXFP4, K, 32), B.Weight(apart.t(), B.MXFP4, K, 32),
+              B.Weight(torch.zeros((1, K - 1), dtype=torch.float16), B.F16, K, 1)):
+        for call in (lambda: Q.gemv(w, x), lambda: Q.gemm(w, x.bfloat16()), lambda: Q.gemv_batch([(w, x, None)]), w.desc,
+                     lambda: Q.dequantize(w), lambda: Q.rows_to_records(w)):
+            with pytest.raises(ValueError, match="packed weights"):
+                call()
+    good = B.Experts(torch.zeros((2, K, rs), dtype=torch.uint8), B.MXFP4, K, K)
+    ids, p = torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 1))
+    for bad in (B.Experts(data.view(2, 16, rs), B.MXFP4, K, 17), B.Experts(data[:, :16].unsqueeze(1), B.MXFP4, K, 1),
+                B.Experts(data.view(2, 16, rs)[:, :, :16], B.MXFP4, K, 16), B.Experts(apart.unsqueeze(0), B.MXFP4, K, 32)):
+        for args in ((bad, good, good), (good, bad, good), (good, good, bad)):
+            with pytest.raises(ValueError, match="packed weights"):
+                Q.moe_swiglu(*args, x, ids, p)
+        with pytest.raises(ValueError, match="packed weights"):
+            bad.desc()
+    assert bytes(good.desc()) == good._desc()
