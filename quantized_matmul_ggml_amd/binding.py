@@ -8,6 +8,7 @@ is not on the GPU, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -265,6 +266,14 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on(stream):
+    """Makes `stream` the current one (None: leaves it), for what a call does
+    through torch before its launch: a copy made on any other stream would run
+    in no order with the launch, and its memory could be handed out again
+    before the launch has read it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _launch(dev: int, stream, name: str, *args):
     """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
     stream; raises what it refuses."""
@@ -501,12 +510,15 @@ class Experts:
 
 
 def quantize_experts(w: torch.Tensor, type_: int, *, stream=None) -> Experts:
-    """Quantize fp32 matrices w (E, M, K) on the GPU into Experts."""
+    """Quantize fp32 matrices w (E, M, K) on the GPU into Experts (MXFP4: or bf16
+    ones).  Matrices whose rows are not evenly spaced are copied first."""
     if w.dim() != 3:
         raise ValueError("expected a 3-D tensor")
     E, M, K = w.shape
-    q = quantize(w.reshape(E * M, K), type_, stream=stream)
-    return Experts(q.data.view(E, M, -1), type_, K, M)
+    with _on(stream):
+        rows = w.reshape(E * M, K)
+    q = quantize(rows, type_, stream=stream)
+    return Experts(q.data.view(E, M, q.data.shape[1]), type_, K, M)
 
 
 def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, stream=None) -> tuple:

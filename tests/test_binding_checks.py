@@ -1,8 +1,12 @@
 """What the Python binding refuses before anything is launched, on the CPU:
 the launch itself and the check for GPU tensors are replaced, so that a call
 which gets past the binding's own checks fails the test."""
+import contextlib
+import types
+
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import quantized_matmul_ggml_amd as Q
 from quantized_matmul_ggml_amd import binding as B
@@ -116,3 +120,45 @@ def test_weights_that_their_data_does_not_hold(no_launch):
         with pytest.raises(ValueError, match="packed weights"):
             bad.desc()
     assert bytes(good.desc()) == good._desc()
+
+
+# ------------------------------------------------------------------ streams
+
+class _Work(TorchDispatchMode):
+    """The torch operators that run inside and outside the fake stream."""
+
+    def __init__(self, monkeypatch):
+        super().__init__()
+        self.stream = types.SimpleNamespace(cuda_stream=7, device_index=0)
+        self.inside, self.ops, self.launched = False, [], []
+
+        @contextlib.contextmanager
+        def on(stream):
+            assert stream is self.stream
+            self.inside = True
+            yield
+            self.inside = False
+
+        monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
+        monkeypatch.setattr(B, "_launch", lambda dev, stream, name, *args: self.launched.append((name, stream)))
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        self.ops.append((func.overloadpacket.__name__, self.inside))
+        return func(*args, **(kwargs or {}))
+
+    def named(self, *names):
+        return [o for o in self.ops if o[0] in names]
+
+
+@pytest.mark.parametrize("layout", ["rows", "transposed", "gaps"])
+def test_quantize_experts_copies_on_its_stream(monkeypatch, qmm_lib, layout):
+    """Matrices whose rows cannot be one list are copied, on the call's stream:
+    on another one the quantizer could read the copy before it is made."""
+    w = {"rows": torch.randn(3, 8, 64), "transposed": torch.randn(3, 64, 8).transpose(1, 2), "gaps": torch.randn(3, 9, 64)[:, :8]}[layout]
+    with _Work(monkeypatch) as work:
+        q = Q.quantize_experts(w, B.MXFP4, stream=work.stream)
+    assert (q.K, q.M, q.data.shape) == (64, 8, (3, 8, Q.row_size(B.MXFP4, 64)))
+    copies = work.named("clone", "copy_", "_to_copy")
+    assert len(copies) == (0 if layout == "rows" else 1) and all(inside for _, inside in copies)
+    assert work.launched == [("qmm_quantize_rule", work.stream)]
