@@ -274,6 +274,27 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+# Memory that a call makes for itself belongs to the stream it runs on: what the
+# allocator hands out for another stream may still be in use there by earlier
+# work, in no order with this call's.
+def _output(stream, device, dtype, *shape) -> torch.Tensor:
+    """A tensor to return.  The caller goes on with it on the current stream,
+    and may let go of it while that still reads."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(*shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
+def _workspace(stream, device, nbytes: int) -> torch.Tensor:
+    """Scratch memory that is let go of when the call returns: work that takes
+    it over on its stream runs after the call's."""
+    with _on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _launch(dev: int, stream, name: str, *args):
     """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
     stream; raises what it refuses."""
@@ -311,9 +332,10 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
     M, K = w.shape
     rs = row_size(type_, K)
     pitch = _row_pitch(pitch, rs)
-    out = torch.empty(M, pitch, dtype=torch.uint8, device=w.device)
+    out = _output(stream, w.device, torch.uint8, M, pitch)
     if pitch > rs:
-        out[:, rs:].zero_()
+        with _on(stream):
+            out[:, rs:].zero_()
     wt = Weight(out, type_, K, M)
     _launch(dev, stream, "qmm_quantize_rule", _dense(w, BF16 if w.dtype == torch.bfloat16 else F32), wt._desc(), rule)
     return wt
@@ -322,7 +344,7 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
 def dequantize(w: Weight, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """W' as fp32 (M, K)."""
     if out is None:
-        out = torch.empty(w.M, w.K, dtype=torch.float32, device=w.data.device)
+        out = _output(stream, w.data.device, torch.float32, w.M, w.K)
     _launch(_need_gpu(w.data, out), stream, "qmm_dequantize", w._desc(), _dense(out, F32))
     return out
 
@@ -340,7 +362,7 @@ def gemv(w: Weight, x, *, out: torch.Tensor | None = None, stream=None) -> torch
     integer-activation path."""
     xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, F32))
     if out is None:
-        out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+        out = _output(stream, xt.device, torch.float32, n, w.M)
     _launch(_need_gpu(w.data, xt, out), stream, "qmm_gemv", w._desc(), xd, _dense(out, F32))
     return out
 
@@ -354,7 +376,7 @@ def gemv_batch(items, *, stream=None) -> list:
     for w, x, out in items:
         xt, n, xd = (x.data, x.M, x.desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense_desc(x, F32))
         if out is None:
-            out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+            out = _output(stream, xt.device, torch.float32, n, w.M)
         tensors += [w.data, xt, out]
         wd, yd = w.desc(), _dense_desc(out, F32)
         keep += [wd, xd, yd]
@@ -374,7 +396,7 @@ def gemv_swiglu(w_gate: Weight, w_up: Weight, x, *, out: torch.Tensor | None = N
     x is fp32 (N, K), or a Q8_0 Weight of N rows for the integer-activation path."""
     xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, F32))
     if out is None:
-        out = torch.empty(n, w_gate.M, dtype=torch.float32, device=xt.device)
+        out = _output(stream, xt.device, torch.float32, n, w_gate.M)
     _launch(_need_gpu(w_gate.data, w_up.data, xt, out), stream, "qmm_gemv_swiglu", w_gate._desc(), w_up._desc(), xd,
             _dense(out, F32))
     return out
@@ -391,7 +413,9 @@ def records_to_rows(records: torch.Tensor, type_: int, K: int, M: int, *, pitch:
     dev = _need_gpu(records)
     pitch = _row_pitch(pitch, row_size(type_, K))
     _need_bytes(records, M * (K // 32) * record_size(type_), "records")
-    out = torch.zeros((M, pitch), dtype=torch.uint8, device=records.device)
+    out = _output(stream, records.device, torch.uint8, M, pitch)
+    with _on(stream):
+        out.zero_()
     wt = Weight(out, type_, K, M)
     _launch(dev, stream, "qmm_records_to_rows", records.data_ptr(), wt._desc())
     return wt
@@ -401,7 +425,7 @@ def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) 
     """The M * K/32 block records of a quantized Weight (uint8 device tensor)."""
     n = w.M * (w.K // 32) * record_size(w.type)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=w.data.device)
+        out = _output(stream, w.data.device, torch.uint8, n)
     _need_bytes(out, n, "out")
     _launch(_need_gpu(w.data, out), stream, "qmm_rows_to_records", w._desc(), out.data_ptr())
     return out
@@ -422,17 +446,13 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
     (qmm_gemm), or a uint8 device tensor to use as is."""
     xt, n, xd = (x.data, x.M, x._desc()) if isinstance(x, Weight) else (x, x.shape[0], _dense(x, BF16))
     if out is None:
-        out = torch.empty(n, w.M, dtype=torch.float32, device=xt.device)
+        out = _output(stream, xt.device, torch.float32, n, w.M)
     dev, wd, yd = _need_gpu(w.data, xt, out), w._desc(), _dense(out, F32)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         n = int(lib().qmm_gemm_workspace_size(wd, xd))
-        workspace = torch.empty(n, dtype=torch.uint8, device=xt.device) if n else None
-        if workspace is not None and stream is not None:
-            # freed when this call returns: keep the allocator from handing it
-            # out again before the kernels on `stream` have run
-            workspace.record_stream(stream)
+        workspace = _workspace(stream, xt.device, n) if n else None
     if workspace is None:
         _launch(dev, stream, "qmm_gemm", wd, xd, yd)
     else:
@@ -458,7 +478,7 @@ def gemm_swiglu(w_gate: Weight, w_up: Weight, x: torch.Tensor, *, out: torch.Ten
                 stream=None) -> torch.Tensor:
     """h (N, M) fp32 = Swish(x W_gate'^T) * (x W_up'^T) for bf16 x (N, K), one fused launch."""
     if out is None:
-        out = torch.empty(x.shape[0], w_gate.M, dtype=torch.float32, device=x.device)
+        out = _output(stream, x.device, torch.float32, x.shape[0], w_gate.M)
     _launch(_need_gpu(w_gate.data, w_up.data, x, out), stream, "qmm_gemm_swiglu", w_gate._desc(), w_up._desc(),
             _dense(x, BF16), _dense(out, F32))
     return out
@@ -470,7 +490,7 @@ def gemm_batch(items, *, stream=None) -> list:
     descs, keep, outs, tensors = [], [], [], []
     for w, x, out in items:
         if out is None:
-            out = torch.empty(x.shape[0], w.M, dtype=torch.float32, device=x.device)
+            out = _output(stream, x.device, torch.float32, x.shape[0], w.M)
         tensors += [w.data, x, out]
         wd, xd, yd = w.desc(), _dense_desc(x, BF16), _dense_desc(out, F32)
         keep += [wd, xd, yd]
@@ -529,8 +549,8 @@ def moe_route(logits: torch.Tensor, top_k: int, *, rule: int = ROUTE_CHOSEN, str
     if logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be float32 (N, E)")
     dev, n = _need_gpu(logits), logits.shape[0]
-    ids = torch.empty(n, top_k, dtype=torch.int32, device=logits.device)
-    weights = torch.empty(n, top_k, dtype=torch.float32, device=logits.device)
+    ids = _output(stream, logits.device, torch.int32, n, top_k)
+    weights = _output(stream, logits.device, torch.float32, n, top_k)
     _launch(dev, stream, "qmm_moe_route", _dense(logits, F32), top_k, rule, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
@@ -553,17 +573,12 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
         raise ValueError("ids and weights must be contiguous and (N, top_k)")
     top_k = ids.shape[1]
     if out is None:
-        out = torch.empty(x.shape[0], w_down.M, dtype=torch.float32, device=x.device)
+        out = _output(stream, x.device, torch.float32, x.shape[0], w_down.M)
     elif out.dtype != torch.float32:
         raise ValueError("out must be float32")
     gd, xd = w_gate._desc(), _dense(x, F32)
     if workspace is None:
-        n = int(lib().qmm_moe_workspace_size(gd, xd, top_k))
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-        if stream is not None:
-            # freed when this call returns: keep the allocator from handing it
-            # out again before the kernels on `stream` have run
-            workspace.record_stream(stream)
+        workspace = _workspace(stream, x.device, int(lib().qmm_moe_workspace_size(gd, xd, top_k)))
     else:
         _need_bytes(workspace, 0, "workspace")
     dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)

@@ -130,7 +130,7 @@ class _Work(TorchDispatchMode):
     def __init__(self, monkeypatch):
         super().__init__()
         self.stream = types.SimpleNamespace(cuda_stream=7, device_index=0)
-        self.inside, self.ops, self.launched = False, [], []
+        self.inside, self.ops, self.launched, self.recorded = False, [], [], []
 
         @contextlib.contextmanager
         def on(stream):
@@ -140,6 +140,8 @@ class _Work(TorchDispatchMode):
             self.inside = False
 
         monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.recorded.append((t.data_ptr(), s)))
         monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
         monkeypatch.setattr(B, "_launch", lambda dev, stream, name, *args: self.launched.append((name, stream)))
 
@@ -162,3 +164,43 @@ def test_quantize_experts_copies_on_its_stream(monkeypatch, qmm_lib, layout):
     copies = work.named("clone", "copy_", "_to_copy")
     assert len(copies) == (0 if layout == "rows" else 1) and all(inside for _, inside in copies)
     assert work.launched == [("qmm_quantize_rule", work.stream)]
+
+
+def test_allocations_belong_to_the_stream(monkeypatch, qmm_lib):
+    """Outputs and workspaces are allocated (and cleared) on the call's stream,
+    and outputs are also kept for the caller's; without a stream nothing is
+    switched or recorded."""
+    K, M, N = 4096, 64, 5
+    w, q4 = _weight(K=K, M=M), _weight(B.Q4_0, K, M)
+    x, xb, rs = torch.zeros((N, K)), torch.zeros((N, K), dtype=BF16), Q.row_size(B.Q4_0, K)
+    ex = B.Experts(torch.zeros((2, 64, Q.row_size(B.MXFP4, 64)), dtype=torch.uint8), B.MXFP4, 64, 64)
+    ids, p, x64 = torch.zeros((N, 1), dtype=torch.int32), torch.zeros((N, 1)), torch.zeros((N, 64))
+    w3 = torch.zeros((2, 3, 64))
+    rec = torch.zeros(M * K // 32 * 18, dtype=torch.uint8)
+    assert Q.gemm_workspace_size(q4, xb) > 0
+    calls = {
+        "quantize": (1, lambda s: Q.quantize(x, B.Q4_0, pitch=rs + 16, stream=s).data),
+        "quantize_experts": (1, lambda s: Q.quantize_experts(w3, B.MXFP4, stream=s).data),
+        "dequantize": (1, lambda s: Q.dequantize(w, stream=s)),
+        "gemv": (1, lambda s: Q.gemv(w, x, stream=s)),
+        "gemv_batch": (2, lambda s: Q.gemv_batch([(w, x, None), (w, x, None)], stream=s)),
+        "gemv_swiglu": (1, lambda s: Q.gemv_swiglu(w, w, x, stream=s)),
+        "records_to_rows": (1, lambda s: Q.records_to_rows(rec, B.Q4_0, K, M, stream=s).data),
+        "rows_to_records": (1, lambda s: Q.rows_to_records(q4, stream=s)),
+        "gemm": (2, lambda s: Q.gemm(q4, xb, stream=s)),                     # its split-K workspace too
+        "gemm_swiglu": (1, lambda s: Q.gemm_swiglu(w, w, xb, stream=s)),
+        "gemm_batch": (2, lambda s: Q.gemm_batch([(w, xb, None), (w, xb, None)], stream=s)),
+        "moe_route": (2, lambda s: Q.moe_route(x64, 1, stream=s)),
+        "moe_swiglu": (2, lambda s: Q.moe_swiglu(ex, ex, ex, x64, ids, p, stream=s)),
+    }
+    for name, (made, call) in calls.items():
+        with _Work(monkeypatch) as work:
+            outs = call(work.stream)
+        outs = list(outs) if isinstance(outs, (list, tuple)) else [outs]
+        assert len(work.named("empty")) == made, name
+        assert all(inside for _, inside in work.named("empty", "zeros", "zero_", "fill_")), name
+        assert {(o.data_ptr(), "current") for o in outs} <= set(work.recorded), name
+        assert [s for _, s in work.launched] == [work.stream], name
+        with _Work(monkeypatch) as work:
+            call(None)
+        assert not any(inside for _, inside in work.ops) and not work.recorded, name

@@ -48,3 +48,49 @@ def test_quantize_experts_bf16():
     q = Q.quantize_experts(w, B.MXFP4)
     rows = R.quantize_mxfp4(w.float().cpu().numpy().reshape(18, 64))
     assert np.array_equal(q.data.cpu().numpy().reshape(18, -1), rows)
+
+
+def test_calls_on_a_busy_streams_side():
+    """With the current stream held back, memory that it has freed but not yet
+    written to must not become a side call's output or workspace: what is
+    pending there would write over it."""
+    K, M, N, E, k = 1024, 512, 6, 4, 2
+    g = torch.Generator(device=DEV).manual_seed(5)
+    w = Q.quantize(torch.randn((M, K), device=DEV, generator=g) * 0.05, B.Q4_0)
+    mx = Q.quantize(torch.randn((M, K), device=DEV, generator=g) * 0.05, B.MXFP4)
+    up = Q.quantize_experts(torch.randn((E, M, K), device=DEV, generator=g) * 0.05, B.MXFP4)
+    down = Q.quantize_experts(torch.randn((E, K, M), device=DEV, generator=g) * 0.05, B.MXFP4)
+    x = torch.randn((N, K), device=DEV, generator=g)
+    xb, xl = x.bfloat16(), torch.randn((N, E), device=DEV, generator=g)
+    ids, p = Q.moe_route(xl, k)
+    rec = Q.rows_to_records(w)
+    calls = {
+        "quantize": lambda s: Q.quantize(x, B.Q8_0, pitch=Q.row_size(B.Q8_0, K) + 32, stream=s).data,
+        "dequantize": lambda s: Q.dequantize(mx, stream=s), "gemv": lambda s: Q.gemv(mx, x, stream=s),
+        "gemv_swiglu": lambda s: Q.gemv_swiglu(w, w, x, stream=s), "gemm": lambda s: Q.gemm(w, xb, stream=s),
+        "gemm_swiglu": lambda s: Q.gemm_swiglu(w, w, xb, stream=s), "gemm_batch": lambda s: Q.gemm_batch([(w, xb, None)], stream=s)[0],
+        "gemv_batch": lambda s: Q.gemv_batch([(w, x, None)], stream=s)[0],
+        "records_to_rows": lambda s: Q.records_to_rows(rec, B.Q4_0, K, M, pitch=w.pitch + 16, stream=s).data,
+        "rows_to_records": lambda s: Q.rows_to_records(w, stream=s),
+        "moe_route": lambda s: torch.cat([t.float() for t in _on(s, Q.moe_route(xl, k, stream=s))]),
+        "moe_swiglu": lambda s: Q.moe_swiglu(up, up, down, x, ids, p, stream=s),
+    }
+
+    def _on(s, outs):
+        if s is not None:
+            s.synchronize()
+        return outs
+
+    for name, call in calls.items():
+        print(f"[case] busy current stream {name}", flush=True)
+        want = call(None)
+        side = _side()
+        torch.cuda._sleep(BUSY)
+        # blocks of the outputs' and the workspaces' sizes that the current
+        # stream has let go of and is still to write to
+        sizes = {want.numel() * want.element_size(), Q.gemm_workspace_size(w, xb), Q.moe_workspace_size(up, x, k), 4 * N * k}
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+        got = call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), name
