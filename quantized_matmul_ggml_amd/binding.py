@@ -298,6 +298,8 @@ def _workspace(stream, device, nbytes: int) -> torch.Tensor:
 def _launch(dev: int, stream, name: str, *args):
     """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
     stream; raises what it refuses."""
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"a stream of GPU {stream.device_index} cannot run work on tensors of GPU {dev}")
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _launch(dev, stream, name, *args)
@@ -605,13 +607,11 @@ def stream_read(src: torch.Tensor, sink: torch.Tensor, *, nbytes: int | None = N
                 stream=None) -> None:
     """qmm_stream_read over the first nbytes (default: all) of the device
     tensor src; sink: an int32 device tensor of at least `workgroups` words."""
-    _need_gpu(src, sink)
+    dev = _need_gpu(src, sink)
     n = src.numel() * src.element_size() if nbytes is None else nbytes
     _need_bytes(src, n, "src")
     _need_bytes(sink, 4 * workgroups, "sink")
-    _check(lib().qmm_stream_read(ctypes.c_void_p(src.data_ptr()), ctypes.c_size_t(n),
-                                 ctypes.c_void_p(sink.data_ptr()), workgroups, _stream(stream)),
-           "qmm_stream_read")
+    _launch(dev, stream, "qmm_stream_read", src.data_ptr(), n, sink.data_ptr(), workgroups)
 
 
 def clock_probe(workgroups: int = 256, iters: int = 20000, mode: int = 0) -> float:

@@ -204,3 +204,14 @@ def test_allocations_belong_to_the_stream(monkeypatch, qmm_lib):
         with _Work(monkeypatch) as work:
             call(None)
         assert not any(inside for _, inside in work.ops) and not work.recorded, name
+
+
+def test_stream_of_another_gpu(monkeypatch, qmm_lib):
+    """A stream of another GPU than the tensors' is refused, also by the
+    measuring read (which launched on the current GPU, whatever its tensors')."""
+    other = types.SimpleNamespace(cuda_stream=7, device_index=1)
+    with pytest.raises(ValueError, match="stream of GPU 1"):
+        B._launch(0, other, "qmm_gemv", None, None, None)
+    monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
+    with pytest.raises(ValueError, match="stream of GPU 1"):
+        Q.stream_read(torch.zeros(64, dtype=torch.uint8), torch.zeros(8, dtype=torch.int32), workgroups=8, stream=other)
