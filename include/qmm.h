@@ -379,7 +379,7 @@ typedef enum {
 
 /* The experts of each token: the top_k largest of its E logits, largest first,
  * ties to the lower index, and their softmax weights (binary32).
- * logits: F32 ne = [E, N], any N >= 0, E <= QMM_MOE_MAX_ROUTED (else
+ * logits: F32 ne = [E, N], N < 2^31, E <= QMM_MOE_MAX_ROUTED (else
  * QMM_ERR_UNSUPPORTED);  1 <= top_k <= min(E, QMM_MOE_MAX_TOP_K) (else
  * QMM_ERR_SHAPE);  ids, weights: top_k consecutive values per token, token n's
  * at ids + n * top_k, 4-byte aligned device memory overlapping neither each

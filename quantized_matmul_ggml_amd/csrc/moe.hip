@@ -461,15 +461,21 @@ void pick(int depth, Kernel *up, Kernel *down)
 hipError_t launch_moe_route(const float *logits, uint64_t pitch, int64_t N, int E, int k, bool all, int32_t *ids,
                             float *weights, hipStream_t stream)
 {
-    if (N == 0) return hipSuccess;
-    const dim3 grid((unsigned)((N + 3) / 4)), block(256);
-#define QMM_ROUTE(R) hipLaunchKernelGGL(moe_route_kernel<R>, grid, block, 0, stream, logits, pitch, N, E, k, (int)all, ids, weights)
-    if (E <= 64) QMM_ROUTE(1);
-    else if (E <= 128) QMM_ROUTE(2);
-    else if (E <= 256) QMM_ROUTE(4);
-    else QMM_ROUTE(16);
+    // 2^25 tokens (2^31 threads) per launch: see kMaxGridThreads
+    constexpr int64_t MOST = 1ll << 25;
+    for (; N > 0; N -= MOST, logits += MOST * pitch, ids += MOST * k, weights += MOST * k) {
+        const int64_t n = N < MOST ? N : MOST;
+        const dim3 grid((unsigned)((n + 3) / 4)), block(256);
+#define QMM_ROUTE(R) hipLaunchKernelGGL(moe_route_kernel<R>, grid, block, 0, stream, logits, pitch, n, E, k, (int)all, ids, weights)
+        if (E <= 64) QMM_ROUTE(1);
+        else if (E <= 128) QMM_ROUTE(2);
+        else if (E <= 256) QMM_ROUTE(4);
+        else QMM_ROUTE(16);
 #undef QMM_ROUTE
-    return hipGetLastError();
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Workspace bytes of one (token, slot) pair.

@@ -39,6 +39,11 @@ constexpr int kStreamLoad = 2;
 constexpr int BUFFER_FLAGS = 0x00020000;
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
 
+// Threads of a launch along one dimension of its grid stay below this: the
+// runtime counts them modulo 2^32, so that a larger grid runs a part of its
+// workgroups and reports success.
+constexpr uint64_t kMaxGridThreads = 1ull << 32;
+
 // One weight matrix as the kernels see it: M rows of K weights, row r at
 // base + r * pitch (bytes).  type is the code format (W_Q8_0, W_Q4_0 or
 // W_F16) or W_MXFP4 (scale_shift 1); the 64-block types arrive as their code format with scale_shift 1
