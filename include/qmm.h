@@ -396,8 +396,9 @@ QMM_API int qmm_moe_route(const qmm_tensor *logits_f32, int32_t top_k, int32_t r
  * multiple of 16, at least one expert's matrix);  w_down: ne = [F, M, E];  all
  * of one type, Q8_0, Q4_0, Q8_B64, Q4_B64 or MXFP4 (else QMM_ERR_TYPE);
  * x: F32 ne = [K, N], N <= QMM_MOE_MAX_TOKENS;  y: F32 ne = [M, N];
- * 1 <= top_k <= QMM_MOE_MAX_TOP_K (else QMM_ERR_SHAPE);  ids, weights: as
- * qmm_moe_route writes them, read on the device.  A slot whose id is negative
+ * 1 <= top_k <= QMM_MOE_MAX_TOP_K (else QMM_ERR_SHAPE);  K, F <= 2^28,
+ * M <= 2^25 - 8 and a workspace below 2^31 bytes (else QMM_ERR_UNSUPPORTED);
+ * ids, weights: as qmm_moe_route writes them, read on the device.  A slot whose id is negative
  * or not below E is empty, whatever its weight; an expert named twice by a
  * token counts with both weights; a token without experts gets zeros.
  * Tokens that choose an expert share the reads of its weights, two by two

@@ -84,7 +84,7 @@ int check_layer(const qmm_tensor *gate, const qmm_tensor *up, const qmm_tensor *
     if (top_k < 1 || top_k > QMM_MOE_MAX_TOP_K || x->ne[1] > QMM_MOE_MAX_TOKENS) return QMM_ERR_SHAPE;
     // row counts, blocks and the workspace are indexed with 32 bits
     const int64_t lim = 1ll << 28;
-    if (gate->ne[0] > lim || gate->ne[1] > lim || down->ne[1] > lim) return QMM_ERR_UNSUPPORTED;
+    if (gate->ne[0] > lim || gate->ne[1] > lim || down->ne[1] > qmm::kMoeMostRows) return QMM_ERR_UNSUPPORTED;
     *ws_bytes = x->ne[1] > 0 ? qmm::moe_workspace(x->ne[1], top_k, gate->ne[1]) : 0;
     if (*ws_bytes >= (1ull << 31)) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;

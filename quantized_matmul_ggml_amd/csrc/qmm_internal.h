@@ -160,6 +160,10 @@ hipError_t launch_moe_route(const float *logits, uint64_t pitch, int64_t N, int 
 // Workspace bytes of launch_moe_swiglu; shapes as checked by the caller
 // (N * k pairs of at most QMM_MOE_MAX_TOKENS * QMM_MOE_MAX_TOP_K).
 uint64_t moe_workspace(int64_t N, int64_t k, int64_t F);
+// At most kMoeMostRows output rows: the second launch has 1024 threads per
+// eight of them.  (The first has 64 (tiles << s_log2) threads, s_log2 being 0
+// once the tiles fill the chip: about 2^31 for 2^28 rows.)
+constexpr int64_t kMoeMostRows = (int64_t)((kMaxGridThreads - 1024) / 1024 * 8);
 hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const ExpertView &down, const ActView &x,
                              const int32_t *ids, const float *weights, int k, const OutView &y, void *ws,
                              hipStream_t stream);

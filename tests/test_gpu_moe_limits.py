@@ -22,3 +22,20 @@ def test_route_more_tokens_than_one_grid():
     first, other = 0.5, 1.0 / (1.0 + 2.718281828459045 ** -1)
     want = torch.where(second, other, first)
     assert ((w[:, 0] - want).abs() <= 8 * 2.0 ** -24).all()
+
+
+def test_experts_most_output_rows():
+    """2^25 - 8 output rows, the most that one call takes: rows that repeat give
+    results that repeat, to the last one, and equal those of a small layer."""
+    M, F = (1 << 25) - 8, 32
+    print(f"[case] moe M {M}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    up = Q.quantize_experts(torch.randn((1, F, 32), device=DEV, generator=g), Q.MXFP4)
+    few = Q.quantize(torch.randn((128, F), device=DEV, generator=g), Q.MXFP4).data
+    x, ids, p = torch.randn((1, 32), device=DEV, generator=g), torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV)
+    want = Q.moe_swiglu(up, up, Q.Experts(few.unsqueeze(0), Q.MXFP4, F, 128), x, ids, p)
+    many = few.repeat(1 << 18, 1)[:M].unsqueeze(0)
+    y = Q.moe_swiglu(up, up, Q.Experts(many, Q.MXFP4, F, M), x, ids, p)
+    assert torch.equal(y, want.repeat(1, 1 << 18)[:, :M]) and (want != 0).any()
+    with pytest.raises(Q.QmmError):
+        Q.moe_swiglu(up, up, Q.Experts(few.repeat((1 << 18) + 1, 1).unsqueeze(0), Q.MXFP4, F, (1 << 25) + 8), x, ids, p)
