@@ -270,7 +270,8 @@ QMM_API int qmm_gemv_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up,
 
 /* Prefill GEMM ("No Python! ...", §6: C_ij = sum_k A_ik B_kj, with many tokens
  * per step).  w: Q4_0, Q8_0, Q4_B64, Q8_B64, MXFP4 or F16 (F16 with K % 32 == 0, else
- * QMM_ERR_UNSUPPORTED), ne = [K, M];  x: BF16 ne = [K, N], any N >= 0;
+ * QMM_ERR_UNSUPPORTED), ne = [K, M];  x: BF16 ne = [K, N], any N >= 0, the
+ * 128 x 128 tiles of the product fewer than 2^23 (else QMM_ERR_UNSUPPORTED);
  * y: F32 ne = [M, N], must not overlap w or x.  Weight tiles are dequantized
  * (F16: converted) to bfloat16 (round to nearest even) and multiplied on the
  * bf16 matrix cores with binary32 accumulation (results agree with the exact
@@ -343,10 +344,11 @@ typedef struct qmm_gemm_item {
  * the rules of qmm_gemm; all items must share the weight type, K and N
  * (else QMM_ERR_TYPE / QMM_ERR_SHAPE), and no output may overlap any operand
  * of any item (QMM_ERR_ALIAS).  1 <= count <= QMM_GEMM_BATCH_MAX (else
- * QMM_ERR_SHAPE).  The items' 128 x 128 output tiles form one grid, so
- * small matrices that would leave most compute units idle on their own
- * share a launch; each output equals, bit for bit, that of qmm_gemm on the
- * same item (K is never split in a batch). */
+ * QMM_ERR_SHAPE).  The items' 128 x 128 output tiles form one grid (fewer
+ * than 2^23 of them, else QMM_ERR_UNSUPPORTED), so small matrices that would
+ * leave most compute units idle on their own share a launch; each output
+ * equals, bit for bit, that of qmm_gemm on the same item (K is never split in
+ * a batch). */
 QMM_API int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stream);
 
 /* The fused gate/up prefill projection with its SwiGLU epilogue ("Development
@@ -358,7 +360,7 @@ QMM_API int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stre
  * h: F32 ne = [M, N], overlapping none of the operands (QMM_ERR_ALIAS).
  * Different types: QMM_ERR_TYPE; different ne: QMM_ERR_SHAPE.  One launch
  * computes both products (each workgroup 64 rows of each matrix times 128
- * tokens) and writes h only.  Each sum carries the accuracy of qmm_gemm; the
+ * tokens, fewer than 2^23 of them, else QMM_ERR_UNSUPPORTED) and writes h only.  Each sum carries the accuracy of qmm_gemm; the
  * epilogue runs in binary32 (expf, one division, two products). */
 QMM_API int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *x_bf16,
                             qmm_tensor *h_f32, void *stream);

@@ -241,7 +241,8 @@ hipError_t launch_tile(GemmMxArgs a, hipStream_t stream)
 {
     using L = MxTile<TM, TN, WR, WC, NST>;
     const int64_t mt = (a.M + L::BM - 1) / L::BM, nt = (a.N + L::BN - 1) / L::BN;
-    if (mt * nt >= (1ll << 31)) return hipErrorInvalidValue;
+    // (64 x 64 tiles are taken for a few hundred of them only)
+    static_assert((L::BM >= 128 && L::BN >= 128 && L::THREADS == 512) || L::BM == 64, "no more threads than gemm_tiles counts");
     a.m_tiles = (int32_t)mt;
     a.n_tiles = (int32_t)nt;
     const void *fn = reinterpret_cast<const void *>(&gemm_mx_kernel<TM, TN, WR, WC, NST>);

@@ -35,6 +35,7 @@ namespace {
 constexpr int BM = 128;               // weight rows per tile
 constexpr int BN = 128;               // tokens per tile
 constexpr int THREADS = 512;
+static_assert(BM == 128 && BN == 128 && THREADS == 512, "gemm_tiles counts these");
 constexpr int TOK_BYTES = BN * 128;   // one K-step (64 bf16) of the token tile
 constexpr int DT = 4;                 // K-steps of token loads in flight
 constexpr int TS = DT + 1;            // token stages

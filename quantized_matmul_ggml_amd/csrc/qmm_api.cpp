@@ -298,6 +298,7 @@ int check_gemm(const qmm_tensor *w, const qmm_tensor *x, const qmm_tensor *y, bo
     if (w->type == QMM_TYPE_F16 && w->ne[0] % 32 != 0) return QMM_ERR_UNSUPPORTED;
     if (w->ne[1] == 0 || x->ne[1] == 0) return QMM_OK;
     if (!qmm::gemm_supported(weight_view(w), gemm_act(x))) return QMM_ERR_UNSUPPORTED;
+    if (qmm::gemm_tiles(w->ne[1], x->ne[1], 128) > qmm::kMostGemmTiles) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }
 
@@ -333,16 +334,19 @@ int qmm_gemm_batch(const qmm_gemm_item *items, int32_t count, void *stream)
     qmm::WeightView wv[QMM_GEMM_BATCH_MAX];
     qmm::ActView xv[QMM_GEMM_BATCH_MAX];
     qmm::OutView yv[QMM_GEMM_BATCH_MAX];
+    int64_t tiles = 0;
     for (int i = 0; i < count; ++i) {           // every item on its own first
         const qmm_tensor *w = items[i].w, *x = items[i].x_bf16, *y = items[i].y_f32;
         const int rc = check_gemm(w, x, y, false);
         if (rc) return rc;
+        tiles += qmm::gemm_tiles(w->ne[1], x->ne[1], 128);
         if (i > 0) {
             const qmm_tensor *w0 = items[0].w, *x0 = items[0].x_bf16;
             if (w->type != w0->type) return QMM_ERR_TYPE;
             if (w->ne[0] != w0->ne[0] || x->ne[1] != x0->ne[1]) return QMM_ERR_SHAPE;
         }
     }
+    if (tiles > qmm::kMostGemmTiles) return QMM_ERR_UNSUPPORTED;
     for (int i = 0; i < count; ++i) {           // then outputs against every operand
         const qmm_tensor *w = items[i].w, *x = items[i].x_bf16, *y = items[i].y_f32;
         for (int j = 0; j < count; ++j) {
@@ -367,6 +371,7 @@ int qmm_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_
     if (w_up->type != w_gate->type) return QMM_ERR_TYPE;
     if (w_up->ne[0] != w_gate->ne[0] || w_up->ne[1] != w_gate->ne[1]) return QMM_ERR_SHAPE;
     if (w_gate->ne[1] == 0 || x->ne[1] == 0) return QMM_OK;
+    if (qmm::gemm_tiles(w_gate->ne[1], x->ne[1], 64) > qmm::kMostGemmTiles) return QMM_ERR_UNSUPPORTED;
     qmm::ActView xv{x->data, pitch_elems(x), x->ne[1]};
     qmm::OutView hv{static_cast<float *>(h->data), pitch_elems(h)};
     return status_of(qmm::launch_gemm_swiglu(weight_view(w_gate), weight_view(w_up), xv, hv,

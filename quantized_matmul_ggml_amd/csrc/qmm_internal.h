@@ -241,6 +241,17 @@ hipError_t allow_dynamic_lds(const void *fn, int bytes);
 int record_size(int type);
 hipError_t launch_records(const WeightView &w, uint8_t *records, bool to_rows, hipStream_t stream);
 
+// Workgroups of a GEMM, 512 threads each per tile of `rows` weight rows and 128
+// tokens (MXFP4 x MXFP4: no more): a launch has at most kMostGemmTiles of them
+// (kMaxGridThreads); larger counts are given as kMostGemmTiles + 1.
+constexpr int64_t kMostGemmTiles = (int64_t)(kMaxGridThreads / 512) - 1;
+inline int64_t gemm_tiles(int64_t M, int64_t N, int rows)
+{
+    const int64_t m = (M + rows - 1) / rows, n = (N + 127) / 128;
+    if (m > kMostGemmTiles || n > kMostGemmTiles || m * n > kMostGemmTiles) return kMostGemmTiles + 1;
+    return m * n;
+}
+
 // The prefill GEMM (gemm.hip): whether the operand strides fit its 32-bit
 // per-tile offsets, and its launcher.
 bool gemm_supported(const WeightView &w, const ActView &x);

@@ -37,3 +37,38 @@ def test_experts_output_rows(qmm_lib):
         assert call(M) == B.ERR_UNSUPPORTED, M
     assert call((1 << 25) - 8) == B.ERR_DEVICE
     assert call(8, K=(1 << 28) + 32) == B.ERR_UNSUPPORTED and call(8, F=(1 << 28) + 32) == B.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kind", ["mxfp4 tokens", "mxfp4", "q4_0", "f16"])
+def test_gemm_tiles(qmm_lib, kind):
+    """512 threads per tile of 128 x 128 (fused pair: 64 rows): fewer than 2^23
+    tiles, of one product or of a batch together."""
+    K, type_ = 32, {"q4_0": B.Q4_0, "f16": B.F16}.get(kind, B.MXFP4)
+
+    def weight(M, at=W):
+        return B.make_desc(type_, K, M, B.row_size(type_, K), at)
+
+    def tokens(N, at=X):
+        return B.make_desc(B.MXFP4, K, N, 32, at) if kind == "mxfp4 tokens" else B.make_desc(B.BF16, K, N, 2 * K, at)
+
+    def out(M, N, at=Y):
+        return B.make_desc(B.F32, M, N, 4 * M, at)
+
+    most = 1 << 30
+    for M, N in ((1, most), (1, most - 127), (most, 1), (1 << 17, 1 << 20), (129, most >> 1), (1 << 33, 8), (8, 1 << 33)):
+        assert B.call_raw("qmm_gemm", weight(M), tokens(N), out(M, N)) == B.ERR_UNSUPPORTED, (M, N)
+    for M, N in ((1, most - 128), (most - 128, 1)):
+        assert B.call_raw("qmm_gemm", weight(M), tokens(N), out(M, N)) == B.ERR_DEVICE, (M, N)
+    if kind == "mxfp4 tokens":
+        return
+    for M, N in ((1, most), (most >> 1, 1), (65, most >> 1)):
+        assert B.call_raw("qmm_gemm_swiglu", weight(M), weight(M, U), tokens(N), out(M, N)) == B.ERR_UNSUPPORTED, (M, N)
+    assert B.call_raw("qmm_gemm_swiglu", weight((most >> 1) - 64), weight((most >> 1) - 64, U), tokens(1), out((most >> 1) - 64, 1)) == B.ERR_DEVICE
+
+    def batch(*Ns):
+        items = [B.QmmGemmItem(*(ctypes.pointer(d) for d in (weight(M, W + (i << 37)), tokens(1, X + (i << 37)), out(M, 1, Y + (i << 37)))))
+                 for i, M in enumerate(Ns)]
+        return qmm_lib.lib().qmm_gemm_batch((B.QmmGemmItem * len(items))(*items), len(items), None)
+
+    assert batch(most >> 1, most >> 1) == B.ERR_UNSUPPORTED
+    assert batch(most >> 1, (most >> 1) - 128) == B.ERR_DEVICE
