@@ -433,9 +433,10 @@ def rows_to_records(w: Weight, *, out: torch.Tensor | None = None, stream=None) 
     return out
 
 
-def gemm_workspace_size(w: Weight, x: torch.Tensor) -> int:
-    """Bytes of workspace qmm_gemm_ws uses to split K for these shapes (0: no split)."""
-    return int(lib().qmm_gemm_workspace_size(w._desc(), _dense(x, BF16)))
+def gemm_workspace_size(w: Weight, x) -> int:
+    """Bytes of workspace qmm_gemm_ws uses to split K for these shapes (0: no
+    split, as for every packed x)."""
+    return int(lib().qmm_gemm_workspace_size(w._desc(), x._desc() if isinstance(x, Weight) else _dense(x, BF16)))
 
 
 def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
@@ -464,12 +465,14 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
     return out
 
 
-def gemm_noalloc(w: Weight, x: torch.Tensor, out: torch.Tensor, *, workspace_bytes: int | None = None,
+def gemm_noalloc(w: Weight, x, out: torch.Tensor, *, workspace_bytes: int | None = None,
                  stream=None) -> torch.Tensor:
     """qmm_gemm_noalloc: the GEMM with its split-K partial sums in the
     library's static scratch array (no allocation in the call; `out` is the
-    caller's).  workspace_bytes defaults to the full split of these shapes."""
-    dev, wd, xd = _need_gpu(w.data, x, out), w._desc(), _dense(x, BF16)
+    caller's).  workspace_bytes defaults to the full split of these shapes.  x
+    is bf16 or packed, as in gemm."""
+    xt, xd = (x.data, x._desc()) if isinstance(x, Weight) else (x, _dense(x, BF16))
+    dev, wd = _need_gpu(w.data, xt, out), w._desc()
     if workspace_bytes is None:
         workspace_bytes = int(lib().qmm_gemm_workspace_size(wd, xd))
     _launch(dev, stream, "qmm_gemm_noalloc", wd, xd, _dense(out, F32), workspace_bytes)

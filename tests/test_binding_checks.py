@@ -215,3 +215,14 @@ def test_stream_of_another_gpu(monkeypatch, qmm_lib):
     monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
     with pytest.raises(ValueError, match="stream of GPU 1"):
         Q.stream_read(torch.zeros(64, dtype=torch.uint8), torch.zeros(8, dtype=torch.int32), workgroups=8, stream=other)
+
+
+def test_packed_tokens_of_every_gemm_form(monkeypatch, qmm_lib):
+    """gemm_noalloc and gemm_workspace_size take packed tokens, as gemm does."""
+    w, x, y = _weight(), _weight(M=5), torch.zeros((5, 32))
+    launched = []
+    monkeypatch.setattr(B, "_need_gpu", lambda *ts: 0)
+    monkeypatch.setattr(B, "_launch", lambda dev, stream, name, *args: launched.append((name, *args)))
+    assert Q.gemm_workspace_size(w, x) == 0
+    assert Q.gemm_noalloc(w, x, y) is y
+    assert launched == [("qmm_gemm_noalloc", w._desc(), x._desc(), B._dense(y, B.F32), 0)]

@@ -94,3 +94,12 @@ def test_calls_on_a_busy_streams_side():
         got = call(side)
         torch.cuda.synchronize()
         assert torch.equal(got, want), name
+
+
+def test_gemm_noalloc_packed_tokens():
+    print("[case] gemm_noalloc packed tokens", flush=True)
+    for M, K, N in ((77, 96, 33), (300, 2048, 130)):
+        w = Q.quantize(torch.randn((M, K), device=DEV), B.MXFP4)
+        x = Q.quantize(torch.randn((N, K), device=DEV).bfloat16(), B.MXFP4)
+        y = torch.full((N, M), 9.0, device=DEV)
+        assert Q.gemm_noalloc(w, x, y) is y and torch.equal(y, Q.gemm(w, x))
