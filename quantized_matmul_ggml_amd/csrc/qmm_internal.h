@@ -87,7 +87,9 @@ bool gemv_config(int type, int64_t K, int64_t M, int64_t N, GemvConfig *cfg);
 // Whether the GEMV kernels can address the operands: loads span a few rows
 // with 32-bit buffer offsets, so the weight row pitch is bounded (2^28
 // bytes), and row counts and activation / output pitches are 32-bit.  The
-// MXFP4 kernel spans 16 rows with such offsets.
+// MXFP4 kernel addresses each row with 64 bits and has 32-bit offsets within
+// one only; it is offered for pitches, and so rows, up to 2^26 bytes, far below
+// what those offsets reach.
 inline bool gemv_supported(const WeightView &w, const ActView &x, const OutView &y)
 {
     return w.pitch <= (w.type == W_MXFP4 ? 1ull << 26 : 1ull << 28) && w.M < (1ll << 31) && x.pitch_elems < (1ull << 31) &&

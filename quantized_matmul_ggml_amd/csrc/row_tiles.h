@@ -357,8 +357,8 @@ __device__ inline uint32_t rt_pack(float a, float b)
 // 0 .. 7 are eight rows' unit 2 q and columns 8 .. 15 the same rows' unit
 // 2 q + 1, so that a tile of eight rows still loads sixteen columns at once:
 // each weight fragment meets both halves' activations, and each half of the
-// columns keeps its own product.  qi: this lane's unit; whole: as in
-// load_unit; nb: blocks of the row.
+// columns keeps its own product.  qi: this lane's unit; whole: whether every
+// column's unit lies in the row to its last block; nb: blocks of the row.
 template <int WT, int SS, int TG, bool HALF, class Frag>
 __device__ inline void multiply_unit(const Unit<WT, SS> &z, int qi, bool whole, int nb, int g, bool upper, int groups,
                                         RowAcc<WT, HALF> (&acc)[TG], Frag frag)
