@@ -180,76 +180,36 @@ __global__ __launch_bounds__(1024) void gemv_mx_kernel(const MxArgs a)
 }
 
 typedef void (*Kernel)(MxArgs);
-// depth: units of one wave and pass over K; with one or two there is nothing to
-// load ahead.
 template <int TG, bool SW, bool HALF>
 Kernel pick(int depth)
 {
-    if (depth <= 1) return gemv_mx_kernel<TG, SW, HALF, 1>;
+    if (depth == 1) return gemv_mx_kernel<TG, SW, HALF, 1>;
     if (depth == 2) return gemv_mx_kernel<TG, SW, HALF, 2>;
     if constexpr (!HALF) {
-        if (depth > 4) return gemv_mx_kernel<TG, SW, HALF, 8>;
+        if (depth == 8) return gemv_mx_kernel<TG, SW, HALF, 8>;
     }
     return gemv_mx_kernel<TG, SW, HALF, 4>;
 }
 
 hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStream_t stream)
 {
-    const int64_t K = tasks[0].w.K;
-    int64_t N = tasks[0].x.N;
+    const int64_t K = tasks[0].w.K, all = tasks[0].x.N;
     const bool sw = up != nullptr;
-    int64_t full = 0, half = 0;
-    for (int i = 0; i < count; ++i) {
-        full += (tasks[i].w.M + 15) / 16;
-        half += (tasks[i].w.M + 7) / 8;
-    }
-    if (half == 0 || N == 0) return hipSuccess;
-    // With tiles for no more than half the CUs, every workgroup's reading and
-    // splitting of all the activations is what takes the time, and half the
-    // tokens each in twice the workgroups is faster although the weights are
-    // read twice, once from the caches (us, whole and halved: 2047 x 5632, eight
-    // tokens 11.0, 7.9; 2048 x 2048, eight 5.8, 4.3; 2048 x 5632, four 8.1, 5.7,
-    // two 5.9, 5.1; but 32000 x 2048, eight 11.3, 13.8).
-    // The same where the image of half the tokens holds all of K and that of all
-    // of them does not, since every tile group would build it again for each
-    // pass (11008 x 4096, eight tokens 18.9, 11.3; 32000 x 4096 25.7, 20.2).
-    const int64_t token = (K + 127) / 128 * 4 * kImageBytes;
-    const bool few = 2 * (sw ? half : full) <= device_cus(), fits = N * token > kImageMost && (N + 1) / 2 * token <= kImageMost;
-    const bool halve = N > 1 && (few || fits) && 2 * count <= QMM_GEMV_BATCH_MAX;
-    const int parts = halve ? 2 : 1;
-    const int64_t all = N;
-    N = (N + parts - 1) / parts;
-    full *= parts;
-    half *= parts;
-    RowPlan p = plan_rows((K + 127) / 128, 4, sw ? half : full, sw ? 0 : half, (int)N, (int)N);
-    // One more split of the tiles where the workgroups' last round is mostly
-    // empty otherwise (11008 x 4096 for eight tokens in two halves: 344 groups of
-    // four tiles on 256 CUs 13.9 us, 688 of two 11.3).
-    auto busy = [&](int s_log2) {
-        const int64_t held = 16 / p.waves * (int64_t)device_cus(), tiles = p.half ? half : sw ? half : full;
-        const int64_t groups = (tiles * (1 << s_log2) + p.waves - 1) / p.waves;
-        return (double)groups / (double)((groups + held - 1) / held * held);
-    };
-    const bool one_pass = p.image >= (int64_t)p.steps * p.step_bytes * N;
-    if (one_pass && 2 << p.s_log2 <= p.waves && p.steps >> (p.s_log2 + 1) >= 4 && busy(p.s_log2 + 1) > 1.2 * busy(p.s_log2))
-        ++p.s_log2;
-    const int rows = sw || p.half ? 8 : 16, T = p.waves >> p.s_log2, tg = N > 4 ? 2 : 1;
+    int64_t M[QMM_GEMV_BATCH_MAX], rows = 0;
+    for (int i = 0; i < count; ++i) rows += M[i] = tasks[i].w.M;
+    if (rows == 0 || all == 0) return hipSuccess;
+    const MxPlan p = plan_mx(M, count, K, all, sw);
     MxArgs a = {};
     a.nb = (int32_t)(K / 32);
     a.qoff = (int32_t)quant_offset(K, 1);
-    a.steps = p.steps;
-    a.s_log2 = p.s_log2;
-    a.pass = pass_steps(p.image, p.step_bytes, (int)N, p.s_log2, p.steps);
-    const int lds = p.waves * (2 * tg * 64 * 4 + kScaleLds) + p.image;
-    // as many workgroups as the CUs hold at once stream the tiles between them
-    const int per_cu = 16 / p.waves;
-    const int64_t cap = (int64_t)per_cu * device_cus();
-    int64_t total = 0, widest = 0;
-    for (int i = 0; i < count; ++i) total += parts * (((tasks[i].w.M + rows - 1) / rows + T - 1) / T);
+    a.steps = p.rows.steps;
+    a.s_log2 = p.rows.s_log2;
+    a.pass = p.pass;
+    int64_t widest = 0;
     int n = 0;
-    for (int i = 0; i < parts * count; ++i) {
-        const GemvTask &t = tasks[i / parts];
-        const int64_t from = N * (i % parts);
+    for (int i = 0; i < p.parts * count; ++i) {
+        const GemvTask &t = tasks[i / p.parts];
+        const int64_t from = p.N * (i % p.parts);
         if (t.w.M == 0 || from >= all) continue;
         MxItem &it = a.item[n++];
         it.w = t.w.base;
@@ -261,23 +221,22 @@ hipError_t launch(const GemvTask *tasks, const WeightView *up, int count, hipStr
         it.y = t.y.data + (uint64_t)from * t.y.pitch_elems;
         it.y_pitch = (uint32_t)t.y.pitch_elems;
         it.M = (int32_t)t.w.M;
-        it.N = (int32_t)(all - from < N ? all - from : N);
-        it.n_groups = (int32_t)(((t.w.M + rows - 1) / rows + T - 1) / T);
+        it.N = (int32_t)(all - from < p.N ? all - from : p.N);
+        it.n_groups = (int32_t)(((t.w.M + p.tile_rows - 1) / p.tile_rows + p.T - 1) / p.T);
         int64_t wgs = it.n_groups;
-        if (total > cap) {
-            wgs = wgs * cap / total;
+        if (p.groups > p.cap) {
+            wgs = wgs * p.cap / p.groups;
             if (wgs < 1) wgs = 1;
         }
         it.wgs = (int32_t)wgs;
         if (wgs > widest) widest = wgs;
     }
-    const int depth = (a.pass + (1 << p.s_log2) - 1) >> p.s_log2;
-    const Kernel k = p.half ? pick<1, false, true>(depth)
-                     : sw   ? (tg == 1 ? pick<1, true, false>(depth) : pick<2, true, false>(depth))
-                            : (tg == 1 ? pick<1, false, false>(depth) : pick<2, false, false>(depth));
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(k), 160 * 1024);
+    const Kernel k = p.rows.half ? pick<1, false, true>(p.depth)
+                     : sw        ? (p.tg == 1 ? pick<1, true, false>(p.depth) : pick<2, true, false>(p.depth))
+                                 : (p.tg == 1 ? pick<1, false, false>(p.depth) : pick<2, false, false>(p.depth));
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(k), kLdsMost);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, dim3((unsigned)widest, (unsigned)n), dim3(64 * p.waves), (unsigned)lds, stream, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)widest, (unsigned)n), dim3(64 * p.rows.waves), (unsigned)p.lds, stream, a);
     return hipGetLastError();
 }
 

@@ -451,8 +451,7 @@ typedef void (*Kernel)(MoeArgs);
 template <int WT, int SS>
 void pick(int depth, Kernel *up, Kernel *down)
 {
-    // (with one or two units of a wave and pass there is nothing to load ahead)
-    *up = depth > 4 ? moe_up_kernel<WT, SS, 8> : depth > 2 ? moe_up_kernel<WT, SS, 4> : moe_up_kernel<WT, SS, 2>;
+    *up = depth == 8 ? moe_up_kernel<WT, SS, 8> : depth == 4 ? moe_up_kernel<WT, SS, 4> : moe_up_kernel<WT, SS, 2>;
     *down = moe_down_kernel<WT, SS>;
 }
 
@@ -521,23 +520,15 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
     a.nb2 = (int32_t)(F / 32);
     a.qoff2 = (int32_t)quant_offset(F, down.w.scale_shift);
     const int64_t units1 = (gate.w.K + kpu - 1) / kpu, units2 = (F + kpu - 1) / kpu;
-    // About how many entries the tokens make: a token chooses k of E experts, so
-    // an expert has c pairs of N trials with chance k / E each, and ceil(c / 2)
-    // entries: the mean of c plus the chance that it is odd, halved.
-    const double chance = k < gate.E ? (double)k / (double)gate.E : 1.0;
-    double even = 1.0;
-    for (int64_t n = 0; n < N; ++n) even *= 1.0 - 2.0 * chance;
-    const double mean = (double)gate.E * ((double)N * chance + (1.0 - even) / 2.0) / 2.0;
-    const int64_t entries = mean < 1.0 ? 1 : (int64_t)(mean + 0.5);
-    const RowPlan p = plan_rows(units1, kpu / 32, (F + 7) / 8 * entries, 0, (int)(N * k < 2 ? 1 : 2), 1);
+    const RowPlan p = plan_moe(gate.E, k, N, F, units1, kpu / 32);
     a.steps1 = p.steps;
     a.s_log2 = p.s_log2;
     a.image = p.image;
     const int T = p.waves >> p.s_log2;
-    const int lds = p.waves * (64 * 4 + kScaleLds) + p.image;
+    const int lds = moe_lds(p);
     a.steps2 = (int32_t)((units2 + 1) / 2);
 
-    const int depth = (p.steps + (1 << p.s_log2) - 1) >> p.s_log2;
+    const int depth = moe_depth((p.steps + (1 << p.s_log2) - 1) >> p.s_log2);
     Kernel ku = nullptr, kd = nullptr;
     if (type == W_MXFP4) pick<W_MXFP4, 0>(depth, &ku, &kd);
     else if (type == W_Q4_0) ss ? pick<W_Q4_0, 1>(depth, &ku, &kd) : pick<W_Q4_0, 0>(depth, &ku, &kd);
@@ -545,7 +536,7 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
     else return hipErrorInvalidValue;
     hipError_t e = hipSuccess;
     if (F > 0) {
-        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), 160 * 1024);
+        e = allow_dynamic_lds(reinterpret_cast<const void *>(ku), kLdsMost);
         if (e != hipSuccess) return e;
         const unsigned groups = (unsigned)(((F + 7) / 8 + T - 1) / T);
         hipLaunchKernelGGL(ku, dim3(groups, (unsigned)(N * k)), dim3(64 * p.waves), (unsigned)lds, stream, a);

@@ -30,7 +30,7 @@
 // and 32-block), or come from memory in the same order.
 #pragma once
 
-#include "qmm_internal.h"
+#include "row_plan.h"
 
 #include <type_traits>
 
@@ -54,7 +54,6 @@ __device__ inline void static_steps(F &&f)
 }
 
 constexpr int kTileCols = 16;          // weight rows per tile
-constexpr int kImageBytes = 192;       // activation parts of one token and 32-block
 
 // A row format: MF matrix instructions (32-blocks) per 64-byte unit and SPU
 // scale bytes per unit.
@@ -320,7 +319,7 @@ struct ScaleWindow {
         scale_words<SB>(lds + row * STRIDE + (HALF ? 2 * d + (j >= 8 ? 1 : 0) : d) * SB, z.s);
     }
 };
-constexpr int kScaleLds = 16 * 80;                         // a wave's LDS for it
+static_assert(kScaleLds >= 16 * 80 && kScaleLds >= 8 * 144, "a wave's LDS for it");
 
 // The sum of a lane's row and token over the instructions so far.  MXFP4 keeps
 // the matrix instruction's own accumulators (one per part, added at the end;
@@ -490,79 +489,6 @@ __device__ inline void stream(int n, Head head, Load load, Use use)
 __device__ inline float rt_swish(float z)
 {
     return z / (1.0f + expf(-z));
-}
-
-// ---- host: how a launch splits its rows ----
-struct RowPlan {
-    int half;        // tiles of eight rows (HALF)
-    int s_log2;      // log2 of the waves that share a tile
-    int waves;       // per workgroup
-    int steps;       // units (HALF: pairs of units) per row
-    int step_bytes;  // image bytes per step and token
-    int image;       // LDS bytes for the image
-};
-
-// units: 64-byte units per row, mf: blocks per unit; tiles: tiles of the
-// launch; half_tiles: their number with eight rows each (0: not available);
-// tokens: the most tokens one image holds at once; likely: how many it will hold
-// as a rule.
-//
-// The memory streams at its rate with about sixteen waves on every CU and four
-// or more units of each in flight, so waves share tiles until there are that
-// many (tile, wave) tasks or four units left to a wave (three Q8_0 tokens
-// choosing four of sixteen experts of 1408 x 2048: 25.2 us with four waves a
-// tile, 27.0 with two, 29.4 with one).  With two token groups a unit is twice
-// the work and two units will do (5632 x 2048 for eight tokens: 6.0 us with
-// eight waves a tile, 6.8 with four), and so they will with several tokens and
-// no more tiles than CUs (256 tiles of 5632 for two tokens: 5.7 us with
-// sixteen waves a tile, 7.2 with eight).  Where a launch has so few tiles that most
-// of the chip idles even so, tiles of eight rows and pairs of units double
-// them (2048 x 5632 for one token: 4.4 us against 4.9; 5632 x 2048, whose 352
-// tiles are enough, 5.0 against 4.4).  Workgroups are small (four waves) while
-// their image is, so that several share a CU and one's loads run beside
-// another's setup; with more tokens a larger workgroup shares one image, and so
-// it does where a larger one's image then holds all of K (11008 x 4096 for four
-// tokens: 9.4 us with sixteen waves, 13.4 with eight and two passes).
-constexpr int kImageMost = 112 * 1024;
-inline RowPlan plan_rows(int64_t units, int mf, int64_t tiles, int64_t half_tiles, int tokens, int likely)
-{
-    const int64_t cus = device_cus();
-    RowPlan p = {0, 0, 4, 0, 0, 0};
-    auto steps_of = [&](int half) { return (units + half) / (1 + half); };
-    auto share = [&](int64_t t, int64_t steps, int least) {
-        int s = 0;
-        while (s < 4 && t << s < 16 * cus && steps >> (s + 1) >= least) ++s;
-        return s;
-    };
-    p.s_log2 = share(tiles, steps_of(0), tokens > 4 || (tokens > 1 && tiles <= cus) ? 2 : 4);
-    if (half_tiles && tokens <= 4 && tiles << p.s_log2 < 5 * cus) {
-        p.half = 1;
-        p.s_log2 = share(half_tiles, steps_of(1), 2);
-    }
-    p.waves = likely <= 2 ? 4 : likely <= 4 ? 8 : 16;
-    if (p.waves < 1 << p.s_log2) p.waves = 1 << p.s_log2;
-    auto budget = [&] { return p.waves <= 4 ? 32 * 1024 : p.waves <= 8 ? 64 * 1024 : kImageMost; };
-    const int64_t whole = (int64_t)steps_of(p.half) * (1 + p.half) * mf * kImageBytes * tokens;
-    if (likely == tokens && whole > budget() && whole <= kImageMost)
-        while (whole > budget()) p.waves *= 2;
-    // one step of every wave of a tile has to fit the image
-    for (;;) {
-        p.step_bytes = (1 + p.half) * mf * kImageBytes;
-        if (((int64_t)p.step_bytes * tokens << p.s_log2) <= budget()) break;
-        if (p.waves < 16) p.waves *= 2;
-        else --p.s_log2;
-    }
-    p.steps = (int)steps_of(p.half);
-    const int64_t all = (int64_t)p.steps * p.step_bytes * tokens;
-    p.image = (int)(all < budget() ? all : budget());
-    return p;
-}
-// Steps per pass over K of an image for `tokens` tokens: all of them, or a
-// multiple of the waves per tile.
-__host__ __device__ inline int pass_steps(int image, int step_bytes, int tokens, int s_log2, int steps)
-{
-    const int n = image / (step_bytes * tokens);
-    return n < steps ? n >> s_log2 << s_log2 : steps > 0 ? steps : 1;
 }
 
 }  // namespace qmm
