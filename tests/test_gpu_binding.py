@@ -103,3 +103,65 @@ def test_gemm_noalloc_packed_tokens():
         x = Q.quantize(torch.randn((N, K), device=DEV).bfloat16(), B.MXFP4)
         y = torch.full((N, M), 9.0, device=DEV)
         assert Q.gemm_noalloc(w, x, y) is y and torch.equal(y, Q.gemm(w, x))
+
+
+def test_two_streams_in_a_graph():
+    """Calls on a stream forked inside a capture, with outputs and workspaces of
+    their own, beside calls on the capturing one: replays with new inputs equal
+    the eager calls bit for bit."""
+    print("[case] two streams in a graph", flush=True)
+    K, M, N, E, k = 1024, 512, 6, 4, 2
+    w = Q.quantize(torch.randn((M, 4 * K), device=DEV) * 0.05, B.Q4_0)
+    up = Q.quantize_experts(torch.randn((E, M, K), device=DEV) * 0.05, B.MXFP4)
+    down = Q.quantize_experts(torch.randn((E, K, M), device=DEV) * 0.05, B.MXFP4)
+    x, xb = torch.empty((N, K), device=DEV), torch.empty((N, 4 * K), device=DEV, dtype=torch.bfloat16)
+    logits = torch.empty((N, E), device=DEV)
+
+    def calls(side):
+        here = torch.cuda.current_stream()
+        if side is not None:
+            side.wait_stream(here)
+        ids, p = Q.moe_route(logits, k, stream=side)
+        outs = [ids, p, Q.moe_swiglu(up, up, down, x, ids, p, stream=side), Q.gemm(w, xb, stream=side), Q.gemv(w, xb.float()),
+                Q.gemm(w, xb), Q.quantize(xb, B.MXFP4).data]
+        if side is not None:
+            here.wait_stream(side)
+        return outs
+
+    def fresh(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        for t in (x, xb, logits):
+            t.copy_(torch.randn(t.shape, device=DEV, generator=g))
+
+    fresh(0)
+    assert Q.gemm_workspace_size(w, xb) > 0
+    calls(None)
+    capture, side = _side(), _side()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=capture):
+        outs = calls(side)
+    for seed in (1, 2, 3):
+        fresh(seed)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = calls(None)
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), f"output {i}, seed {seed}"
+
+
+def test_split_k_workspace_beside_a_busy_stream():
+    """As test_calls_on_a_busy_streams_side, for a product that splits K."""
+    print("[case] busy current stream, split K", flush=True)
+    w, x = Q.quantize(torch.randn((256, 4096), device=DEV), B.Q4_0), torch.randn((200, 4096), device=DEV).bfloat16()
+    n = Q.gemm_workspace_size(w, x)
+    assert n > 0
+    out, want = torch.empty((200, 256), device=DEV), Q.gemm(w, x)
+    side = _side()
+    torch.cuda._sleep(BUSY)
+    torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+    for _ in range(3):
+        Q.gemm(w, x, out=out, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
