@@ -187,7 +187,7 @@ class Weight:
     def _desc(self) -> bytes:
         d, M = self.data, self.M
         (pitch, step), (rows, cols), es = d.stride(), d.shape, d.element_size()
-        if step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K):
+        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K)):
             raise ValueError(_DATA)
         return _packed(self.type, self.K, M, pitch * es, d.data_ptr())
 
@@ -524,7 +524,7 @@ class Experts:
     def _desc(self) -> bytes:
         d, M = self.data, self.M
         (apart, pitch, step), (E, rows, cols), es = d.stride(), d.shape, d.element_size()
-        if step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K):
+        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K)):
             raise ValueError(_DATA)
         nb2 = apart * es
         return _PACK(self.type, 3, self.K, M, E, 1, 0, pitch * es, nb2, nb2 * E, d.data_ptr())

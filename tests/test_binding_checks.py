@@ -226,3 +226,14 @@ def test_packed_tokens_of_every_gemm_form(monkeypatch, qmm_lib):
     assert Q.gemm_workspace_size(w, x) == 0
     assert Q.gemm_noalloc(w, x, y) is y
     assert launched == [("qmm_gemm_noalloc", w._desc(), x._desc(), B._dense(y, B.F32), 0)]
+
+
+def test_weights_of_no_rows(qmm_lib):
+    """Strides of empty data mean nothing (torch gives (1, M) to a transposed
+    one, and arrays from elsewhere bring zeros)."""
+    for data, type_ in ((torch.zeros((0, 64), dtype=torch.float16).as_strided((0, 64), (0, 0)), B.F16),
+                        (torch.zeros((64, 0), dtype=torch.uint8).t(), B.MXFP4)):
+        d = B.Weight(data, type_, 64, 0).desc()
+        assert (d.ne[0], d.ne[1]) == (64, 0)
+    d = B.Experts(torch.zeros((48, 0, 3), dtype=torch.uint8).permute(2, 1, 0), B.MXFP4, 64, 0).desc()
+    assert (d.ne[0], d.ne[1], d.ne[2]) == (64, 0, 3)
