@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 from dataclasses import dataclass
@@ -144,6 +145,9 @@ def row_size(type_: int, K: int) -> int:
     return int(lib().qmm_row_size(type_, K))
 
 
+_row_bytes = functools.lru_cache(row_size)      # 0.5 us less, for the checks of every call
+
+
 def make_desc(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int, n_dims: int = 2,
               nb0: int | None = None) -> QmmTensor:
     """A raw descriptor (used directly by the boundary tests)."""
@@ -152,13 +156,6 @@ def make_desc(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int, n_dims: i
     nb2 = nb1 * (ne1 if ne1 > 1 else 1) & _U64
     # one packed copy: filling the fields one by one costs several microseconds
     return QmmTensor.from_buffer_copy(_PACK(type_, n_dims, ne0, ne1, 1, 1, nb0 & _U64, nb1 & _U64, nb2, nb2, data_ptr or 0))
-
-
-def _packed(type_: int, ne0: int, ne1: int, nb1: int, data_ptr: int) -> bytes:
-    """make_desc's bytes, which the entry points take as they are (building a
-    structure from them costs as much again)."""
-    nb2 = nb1 * (ne1 if ne1 > 1 else 1)
-    return _PACK(type_, 2, ne0, ne1, 1, 1, _ELEM.get(type_, 0), nb1, nb2, nb2, data_ptr)
 
 
 # The library checks a descriptor's sizes against each other, not against the
@@ -187,9 +184,11 @@ class Weight:
     def _desc(self) -> bytes:
         d, M = self.data, self.M
         (pitch, step), (rows, cols), es = d.stride(), d.shape, d.element_size()
-        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K)):
+        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < _row_bytes(self.type, self.K)):
             raise ValueError(_DATA)
-        return _packed(self.type, self.K, M, pitch * es, d.data_ptr())
+        pitch *= es
+        nb2 = pitch * M if M > 1 else pitch
+        return _PACK(self.type, 2, self.K, M, 1, 1, _ELEM.get(self.type, 0), pitch, nb2, nb2, d.data_ptr())
 
     def rows(self, r0: int, r1: int) -> "Weight":
         """Row-range view [r0, r1): no copy, same pitch."""
@@ -217,11 +216,9 @@ def _need_bytes(t: torch.Tensor, nbytes: int, what: str):
         raise ValueError(f"{what} holds fewer than {nbytes} bytes")
 
 
-def _row_pitch(pitch: int | None, row_bytes: int) -> int:
+def _row_pitch(pitch: int, row_bytes: int) -> int:
     """The pitch of packed rows to make: a single row's, too, holds the row (the
     library does not look at it)."""
-    if pitch is None:
-        return row_bytes
     if pitch < row_bytes:
         raise ValueError(f"a pitch of {pitch} bytes is below the row's {row_bytes}")
     return pitch
@@ -238,32 +235,31 @@ def _dense(t: torch.Tensor, type_: int) -> bytes:
     read or write past the end of a narrower tensor."""
     if t.dtype is not _DTYPE[type_]:
         raise ValueError(f"expected a {_DTYPE[type_]} tensor, not {t.dtype}")
-    if t.dim() != 2:
+    shape, es = t.shape, _ELEM[type_]
+    if len(shape) != 2:
         raise ValueError("expected a 2-D tensor")
-    es = t.element_size()
-    rows, cols = t.shape
+    rows, cols = shape
     if rows == 0 or cols == 0:          # empty: strides are meaningless
-        return _packed(type_, cols, rows, cols * es, t.data_ptr())
-    pitch, step = t.stride()
-    if step != 1:
-        raise ValueError("rows must be contiguous (stride 1 along the last dimension)")
-    return _packed(type_, cols, rows, pitch * es, t.data_ptr())
+        pitch = cols * es
+    else:
+        pitch, step = t.stride()
+        if step != 1:
+            raise ValueError("rows must be contiguous (stride 1 along the last dimension)")
+        pitch *= es
+    nb2 = pitch * rows if rows > 1 else pitch
+    return _PACK(type_, 2, cols, rows, 1, 1, es, pitch, nb2, nb2, t.data_ptr())
 
 
 # The current stream's handle without building a Stream object (2.8 us less per
 # call), where this torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 # The current device, for callers that hold a tensor of a GPU (so that torch's
 # own check that the GPU is initialised is not needed).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _on(stream):
@@ -291,25 +287,27 @@ def _output(stream, device, dtype, *shape) -> torch.Tensor:
 def _workspace(stream, device, nbytes: int) -> torch.Tensor:
     """Scratch memory that is let go of when the call returns: work that takes
     it over on its stream runs after the call's."""
-    with _on(stream):
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _launch(dev: int, stream, name: str, *args):
     """Calls entry point `name` on GPU dev, on `stream` or that GPU's current
     stream; raises what it refuses."""
-    if stream is not None and stream.device_index != dev:
-        raise ValueError(f"a stream of GPU {stream.device_index} cannot run work on tensors of GPU {dev}")
-    if dev != _current_device():
-        with torch.cuda.device(dev):
-            return _launch(dev, stream, name, *args)
-    if stream is not None:
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
+    if stream is None:
         handle = _raw_stream(dev)
+    elif stream.device_index == dev:
+        handle = stream.cuda_stream
     else:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    status = getattr(_lib or lib(), name)(*args, handle)
+        raise ValueError(f"a stream of GPU {stream.device_index} cannot run work on tensors of GPU {dev}")
+    fn = getattr(_lib or lib(), name)
+    if dev == _current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
     if status != OK:
         raise QmmError(status, name)
 
@@ -332,8 +330,8 @@ def quantize(w: torch.Tensor, type_: int, *, pitch: int | None = None, rule: int
     if w.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("quantize takes float32 rows (or bfloat16 ones, for MXFP4)")
     M, K = w.shape
-    rs = row_size(type_, K)
-    pitch = _row_pitch(pitch, rs)
+    rs = _row_bytes(type_, K)
+    pitch = rs if pitch is None else _row_pitch(pitch, rs)
     out = _output(stream, w.device, torch.uint8, M, pitch)
     if pitch > rs:
         with _on(stream):
@@ -413,7 +411,8 @@ def records_to_rows(records: torch.Tensor, type_: int, K: int, M: int, *, pitch:
                     stream=None) -> Weight:
     """Packed rows (a Weight) from M * K/32 block records (uint8 device tensor)."""
     dev = _need_gpu(records)
-    pitch = _row_pitch(pitch, row_size(type_, K))
+    rs = _row_bytes(type_, K)
+    pitch = rs if pitch is None else _row_pitch(pitch, rs)
     _need_bytes(records, M * (K // 32) * record_size(type_), "records")
     out = _output(stream, records.device, torch.uint8, M, pitch)
     with _on(stream):
@@ -456,11 +455,12 @@ def gemm(w: Weight, x, *, out: torch.Tensor | None = None, workspace="auto",
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         n = int(lib().qmm_gemm_workspace_size(wd, xd))
         workspace = _workspace(stream, xt.device, n) if n else None
+    elif workspace is not None:
+        _need_bytes(workspace, 0, "workspace")
     if workspace is None:
         _launch(dev, stream, "qmm_gemm", wd, xd, yd)
     else:
         _need_gpu(out, workspace)
-        _need_bytes(workspace, 0, "workspace")
         _launch(dev, stream, "qmm_gemm_ws", wd, xd, yd, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
@@ -524,7 +524,7 @@ class Experts:
     def _desc(self) -> bytes:
         d, M = self.data, self.M
         (apart, pitch, step), (E, rows, cols), es = d.stride(), d.shape, d.element_size()
-        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < row_size(self.type, self.K)):
+        if M and (step != 1 or rows < M or (M == 1 or cols != pitch) and cols * es < _row_bytes(self.type, self.K)):
             raise ValueError(_DATA)
         nb2 = apart * es
         return _PACK(self.type, 3, self.K, M, E, 1, 0, pitch * es, nb2, nb2 * E, d.data_ptr())
