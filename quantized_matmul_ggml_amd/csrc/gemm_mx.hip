@@ -9,8 +9,9 @@
 // instruction multiplies the codes, scales by 2^(s_w + s_x - 254) and adds in
 // binary32.  The order of the codes within a block does not matter, since both
 // operands have the same one, so nothing is unpacked.  Four times the bf16
-// rate per instruction: 9.9 PFLOP/s of zeros and 6.0 of random codes, for which
-// the clock falls to 1.5 GHz (all CUs, registers only).
+// rate per instruction: 9.8 PFLOP/s of zeros and 6.8 of random codes, for which
+// the clock falls to 1.7 GHz (all CUs, registers only; 6.0 and 1.5 GHz on another
+// card).
 //
 // Work split: a workgroup of WR x WC waves computes BM weight rows x BN tokens,
 // each wave TM x TN tiles of 32 x 32, so that a fragment read from LDS feeds TM
@@ -23,11 +24,13 @@
 // placed by an XOR of its index with bits of the row, so that the rows read
 // together fall in different banks.
 //
-// 11008 x 4096 x 4096: 123 us (3.0 PFLOP/s).  Its 688 tiles are 2.7 rounds of
-// the chip, the matrix instructions alone take 90 us, the loads alone 74, and
-// the stores of y add 20; LDS is as busy as the matrix cores, so that what
-// overlaps is limited by both.  5632 x 2048 x 512: 11.2 us, of which 4 pass
-// before the first products and after the last.  (K steps of 128, four stages
+// 11008 x 4096 x 4096: 122 us (3.0 PFLOP/s).  Its 688 tiles are 2.7 rounds of
+// the chip; in copies of the kernel that left parts out, the matrix instructions
+// and their LDS reads alone took 90 us, the loads alone 74, and the stores of y
+// added 20.  Of the cycles that a CU is busy its matrix cores are for 39 %, its
+// texture data unit, through which the direct-to-LDS loads go, for 86 % (56 %
+// waiting for the caches), LDS reads for 17 %.  5632 x 2048 x 512: 10.5 us, of
+// which 4 pass before the first products and after the last.  (K steps of 128, four stages
 // deep, were slower: 64-byte pieces of lines need twice the L2's requests.  So
 // were four waves of 128 x 128 each, and fetching later steps' lines into the L2
 // changed nothing.)
