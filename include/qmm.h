@@ -415,6 +415,89 @@ QMM_API int qmm_moe_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, con
                            const qmm_tensor *x_f32, const int32_t *ids, const float *weights, int32_t top_k,
                            qmm_tensor *y_f32, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Products whose weights each token picks, for many tokens: a
+ * mixture-of-experts layer for prompts and batches (the feed-forward block of the
+ * Development Guide for Small AI Models (TinyLLaMA, etc.) Using C++, §4.4, with E
+ * experts), and low-rank adapters of several requests beside a projection that
+ * all share.  Grouping is done on the device: no host reads the router's choice. */
+
+/* Slots grouped by expert.  ids: n_slots values as qmm_moe_route writes them
+ * (token n's top_k slots from n * top_k on); an id that is negative or not below
+ * n_experts is an empty slot.
+ * offsets: n_experts + 1 values; expert e's slots are order[offsets[e]] ..
+ * order[offsets[e + 1] - 1], ascending; the empty slots follow from
+ * offsets[n_experts] on, ascending.  order: n_slots values, every slot once.
+ * place: n_slots values, the position in order of each slot, -1 for an empty one.
+ * All are 4-byte aligned device memory (ids too), none overlapping another.
+ * 1 <= n_experts <= QMM_MOE_MAX_ROUTED, n_slots < 2^31.  n_slots = 0 fills offsets
+ * with zeros.  workspace: qmm_moe_group_workspace_size bytes (0 up to 16384
+ * slots), 16-byte aligned, scratch for this call alone until its kernels have
+ * run (fewer bytes: QMM_ERR_SCRATCH). */
+QMM_API size_t qmm_moe_group_workspace_size(int64_t n_slots, int32_t n_experts);
+QMM_API int qmm_moe_group(const int32_t *ids, int64_t n_slots, int32_t n_experts, int32_t *offsets, int32_t *order,
+                          int32_t *place, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Products grouped by expert, with ragged group sizes:
+ *   y[r] = W_e x[t(r)]  for offsets[e] <= r < offsets[e + 1],
+ * t(r) = order[r] / top_k (the token of slot order[r]), or r without an order (order
+ * NULL: then x has y's number of rows).  Rows of y outside all groups are left
+ * as they are; a row whose token is not one of x's N gets zeros.
+ * w: ne = [K, M, E] as in qmm_moe_swiglu, E <= QMM_MOE_MAX_ROUTED;  x: BF16 ne =
+ * [K, N], 16-byte aligned rows;  y: F32 or BF16 ne = [M, R];  offsets: E + 1
+ * values, never descending (what they hold beyond 0 .. R is cut), order: R values
+ * (device memory, 4-byte aligned, read on the device).  top_k >= 1.
+ * Products are exact: a block's codes and the activations multiply exactly, the
+ * block's scale multiplies their binary32 sum, and only binary32 sums (and a
+ * BF16 y, once) round.  Block scales must be finite.
+ * Limits (else QMM_ERR_UNSUPPORTED): K, M <= 2^28, R and N < 2^31, weight pitches
+ * below 2^24 bytes, N (or, without an order, 128) rows of x below 2^31 bytes, fewer
+ * than 2^24 tiles. */
+QMM_API int qmm_gemm_grouped(const qmm_tensor *w, const qmm_tensor *x_bf16, const int32_t *offsets, const int32_t *order,
+                             int32_t top_k, qmm_tensor *y, void *stream);
+
+/* The gate/up pair of such products with its SwiGLU epilogue (as qmm_gemm_swiglu):
+ *   h[r] = Swish(Wg_e x[t(r)]) * (Wu_e x[t(r)]);
+ * w_gate, w_up: one type and ne (else QMM_ERR_TYPE, QMM_ERR_SHAPE), each with its
+ * own pitches; h: F32 or BF16 ne = [M, R].  The epilogue runs in binary32. */
+QMM_API int qmm_gemm_grouped_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *x_bf16,
+                                    const int32_t *offsets, const int32_t *order, int32_t top_k, qmm_tensor *h, void *stream);
+
+/* The mixture-of-experts layer for any number of tokens:
+ *   y[n] = sum_s weights[n][s] Wd_e (Swish(Wg_e x[n]) * (Wu_e x[n])), e = ids[n][s],
+ * as qmm_moe_swiglu, with x BF16 ne = [K, N] and y F32 or BF16 ne = [M, N]; empty
+ * slots, experts named twice and tokens without experts as there.  It groups the
+ * slots and runs the two grouped products; between them h is BF16 (the activation
+ * type of every product of many tokens), the sum over a token's slots is
+ * binary32.  Limits as in qmm_gemm_grouped, with R = N top_k and F < 2^23.
+ * workspace: qmm_moe_gemm_workspace_size bytes (about R (2 F + 4 M); fewer:
+ * QMM_ERR_SCRATCH) of device memory, 16-byte aligned, overlapping no operand;
+ * scratch for this call alone until its kernels have run. */
+QMM_API size_t qmm_moe_gemm_workspace_size(const qmm_tensor *w_gate, const qmm_tensor *w_down, const qmm_tensor *x_bf16,
+                                           int32_t top_k);
+QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *w_down,
+                                const qmm_tensor *x_bf16, const int32_t *ids, const float *weights, int32_t top_k,
+                                qmm_tensor *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Low-rank adapters of many requests at once, beside a projection that all share:
+ *   y[n] = base[n] + s_a B_a (A_a x[n]),  a = ids[n].
+ * a: BF16 ne = [K, r, L] (n_dims 3), b: BF16 ne = [r, M, L], each matrix and row
+ * 16-byte aligned;  K % 32 = 0, r % 8 = 0, 8 <= r <= QMM_LORA_MAX_RANK (else
+ * QMM_ERR_SHAPE);  x: F32 or BF16 (16-byte aligned rows) ne = [K, N], N <=
+ * QMM_LORA_MAX_TOKENS, K, M <= 2^28;  ids: N values, read on the device: a token
+ * whose id is negative or not below L has no adapter, its y is base;  scales: L
+ * values s_a, or NULL for 1;  base: F32 ne = [M, N] (the shared projection's
+ * output), or NULL for 0;  y: F32 ne = [M, N], which may be base itself (same data
+ * and pitch) and overlaps no other operand.
+ * Products are exact, their sums and the product with s_a round in binary32; a
+ * token's result depends on no other token.
+ * workspace: qmm_lora_workspace_size bytes (fewer: QMM_ERR_SCRATCH), 16-byte
+ * aligned, scratch for this call alone until its kernels have run. */
+#define QMM_LORA_MAX_RANK 128
+#define QMM_LORA_MAX_TOKENS (1 << 24)
+QMM_API size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *x);
+QMM_API int qmm_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x, const int32_t *ids, const float *scales,
+                     const qmm_tensor *base_f32, qmm_tensor *y_f32, void *workspace, size_t workspace_bytes, void *stream);
+
 /* GGUF-style block records ("Development Guide for Small AI Models (TinyLLaMA,
  * etc.) Using C++", §3.2: a GGUF file's tensor data is an aligned array;
  * §6.1: a Q4_0 block is one FP16 scale (2 bytes) followed by 32 4-bit

@@ -33,9 +33,12 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 
 EXPORTS = ("qmm_row_size", "qmm_quantize", "qmm_quantize_rule", "qmm_dequantize", "qmm_gemv", "qmm_gemv_batch",
            "qmm_gemv_swiglu", "qmm_gemm", "qmm_gemm_ws", "qmm_gemm_noalloc", "qmm_gemm_workspace_size", "qmm_gemm_batch", "qmm_gemm_swiglu", "qmm_record_size", "qmm_records_to_rows",
-           "qmm_rows_to_records", "qmm_moe_route", "qmm_moe_workspace_size", "qmm_moe_swiglu", "qmm_stream_read", "qmm_clock_probe", "qmm_wall_clock_khz", "qmm_strerror")
+           "qmm_rows_to_records", "qmm_moe_route", "qmm_moe_workspace_size", "qmm_moe_swiglu", "qmm_moe_group_workspace_size", "qmm_moe_group",
+           "qmm_gemm_grouped", "qmm_gemm_grouped_swiglu", "qmm_moe_gemm_workspace_size", "qmm_moe_gemm_swiglu",
+           "qmm_lora_workspace_size", "qmm_lora", "qmm_stream_read", "qmm_clock_probe", "qmm_wall_clock_khz", "qmm_strerror")
 GEMV_BATCH_MAX = 8
 MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_MAX_ROUTED = 8, 16, 1024
+LORA_MAX_RANK, LORA_MAX_TOKENS = 128, 1 << 24
 # qmm_route_rule
 ROUTE_ALL, ROUTE_CHOSEN = 0, 1
 
@@ -121,6 +124,23 @@ def lib() -> ctypes.CDLL:
         h.qmm_moe_workspace_size.restype = ctypes.c_size_t
         h.qmm_moe_swiglu.argtypes = [P, P, P, P, V, V, I, P, V, ctypes.c_size_t, V]
         h.qmm_moe_swiglu.restype = ctypes.c_int
+        S = ctypes.c_size_t
+        h.qmm_moe_group_workspace_size.argtypes = [ctypes.c_int64, I]
+        h.qmm_moe_group_workspace_size.restype = S
+        h.qmm_moe_group.argtypes = [V, ctypes.c_int64, I, V, V, V, V, S, V]
+        h.qmm_moe_group.restype = ctypes.c_int
+        h.qmm_gemm_grouped.argtypes = [P, P, V, V, I, P, V]
+        h.qmm_gemm_grouped.restype = ctypes.c_int
+        h.qmm_gemm_grouped_swiglu.argtypes = [P, P, P, V, V, I, P, V]
+        h.qmm_gemm_grouped_swiglu.restype = ctypes.c_int
+        h.qmm_moe_gemm_workspace_size.argtypes = [P, P, P, I]
+        h.qmm_moe_gemm_workspace_size.restype = S
+        h.qmm_moe_gemm_swiglu.argtypes = [P, P, P, P, V, V, I, P, V, S, V]
+        h.qmm_moe_gemm_swiglu.restype = ctypes.c_int
+        h.qmm_lora_workspace_size.argtypes = [P, P]
+        h.qmm_lora_workspace_size.restype = S
+        h.qmm_lora.argtypes = [P, P, P, V, V, P, P, V, S, V]
+        h.qmm_lora.restype = ctypes.c_int
         for f in ("qmm_quantize", "qmm_dequantize", "qmm_gemv", "qmm_gemm"):
             getattr(h, f).restype = ctypes.c_int
         h.qmm_stream_read.argtypes = [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int32,
@@ -589,6 +609,160 @@ def moe_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor,
     dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)
     _launch(dev, stream, "qmm_moe_swiglu", gd, w_up._desc(), w_down._desc(), xd, ids.data_ptr(), weights.data_ptr(), top_k,
             _dense(out, F32), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def _ints(t: torch.Tensor, what: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{what} must be int32 and contiguous")
+    return t
+
+
+def _dense_out(out, stream, device, dtype, rows: int, cols: int) -> tuple:
+    """The output tensor (None: made here, of dtype) and its descriptor."""
+    if out is None:
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = _output(stream, device, dtype, rows, cols)
+    return out, _dense(out, BF16 if out.dtype == torch.bfloat16 else F32)
+
+
+def moe_group_workspace_size(n_slots: int, n_experts: int) -> int:
+    """Bytes of workspace qmm_moe_group needs (0 up to 16384 slots)."""
+    return int(lib().qmm_moe_group_workspace_size(n_slots, n_experts))
+
+
+def moe_group(ids: torch.Tensor, n_experts: int, *, workspace: torch.Tensor | None = None, stream=None) -> tuple:
+    """(offsets, order, place), int32: the slots of ids (int32, contiguous, e.g. the
+    (N, top_k) of moe_route) grouped by expert.  Expert e's slots are
+    order[offsets[e]:offsets[e + 1]], ascending, empty ones (ids outside 0 ..
+    n_experts - 1) follow after offsets[n_experts]; place, shaped like ids, is
+    each slot's position in order, -1 for an empty one.  workspace: a uint8 device
+    tensor of moe_group_workspace_size bytes, or None to allocate one."""
+    dev, n = _need_gpu(_ints(ids, "ids")), ids.numel()
+    if n_experts < 1 or n_experts > MOE_MAX_ROUTED:
+        raise ValueError(f"n_experts must be 1 to {MOE_MAX_ROUTED}")
+    offsets = _output(stream, ids.device, torch.int32, n_experts + 1)
+    order = _output(stream, ids.device, torch.int32, n)
+    place = _output(stream, ids.device, torch.int32, *ids.shape)
+    need = int((_lib or lib()).qmm_moe_group_workspace_size(n, n_experts))
+    if workspace is not None:
+        _need_bytes(workspace, 0, "workspace")
+        _need_gpu(ids, workspace)
+    elif need:
+        workspace = _workspace(stream, ids.device, need)
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch(dev, stream, "qmm_moe_group", ids.data_ptr(), n, n_experts, offsets.data_ptr(), order.data_ptr(), place.data_ptr(), ws, size)
+    return offsets, order, place
+
+
+def _grouped(name: str, ws: tuple, x: torch.Tensor, offsets, order, top_k: int, out, dtype, stream) -> torch.Tensor:
+    w = ws[0]
+    if _ints(offsets, "offsets").numel() != w.data.shape[0] + 1:
+        raise ValueError("offsets must hold one value more than there are experts")
+    tensors = [t.data for t in ws] + [x, offsets]
+    if order is not None:
+        tensors.append(_ints(order, "order"))
+    rows = x.shape[0] if order is None else order.numel() if out is None else out.shape[0]
+    if order is not None and order.numel() != rows:
+        raise ValueError("order must hold one value for each row of out")
+    out, yd = _dense_out(out, stream, x.device, dtype, rows, w.M)
+    dev = _need_gpu(*tensors, out)
+    _launch(dev, stream, name, *(t._desc() for t in ws), _dense(x, BF16), offsets.data_ptr(),
+            None if order is None else order.data_ptr(), top_k, yd)
+    return out
+
+
+def gemm_grouped(w: Experts, x: torch.Tensor, offsets: torch.Tensor, *, order: torch.Tensor | None = None, top_k: int = 1,
+                 dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y (R, M): y[r] = W_e x[t(r)] for the rows r of each expert e, offsets[e] <= r <
+    offsets[e + 1] (offsets int32, E + 1 values); x (N, K) bf16.  t(r) is order[r] //
+    top_k (order int32, R values, as moe_group returns it), or r without an order.
+    Rows outside all groups are left as they are (in a y made here: undefined).
+    dtype: float32 or bfloat16, of the y made here."""
+    return _grouped("qmm_gemm_grouped", (w,), x, offsets, order, top_k, out, dtype, stream)
+
+
+def gemm_grouped_swiglu(w_gate: Experts, w_up: Experts, x: torch.Tensor, offsets: torch.Tensor, *,
+                        order: torch.Tensor | None = None, top_k: int = 1, dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h (R, M): Swish(Wg_e x[t(r)]) * (Wu_e x[t(r)]), otherwise as gemm_grouped."""
+    return _grouped("qmm_gemm_grouped_swiglu", (w_gate, w_up), x, offsets, order, top_k, out, dtype, stream)
+
+
+def moe_gemm_workspace_size(w_gate: Experts, w_down: Experts, x: torch.Tensor, top_k: int) -> int:
+    """Bytes of workspace qmm_moe_gemm_swiglu needs for these shapes."""
+    return int(lib().qmm_moe_gemm_workspace_size(w_gate._desc(), w_down._desc(), _dense(x, BF16), top_k))
+
+
+def moe_gemm_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor, ids: torch.Tensor,
+                    weights: torch.Tensor, *, dtype=torch.float32, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y (N, M): moe_swiglu for any number of tokens, x (N, K) bf16; ids (int32) and
+    weights (fp32) (N, top_k), contiguous.  dtype: float32 or bfloat16, of the y
+    made here.  workspace: a uint8 device tensor of at least
+    moe_gemm_workspace_size bytes, or None to allocate one (graph-capture safe)."""
+    if weights.dtype != torch.float32 or ids.dim() != 2 or x.dim() != 2 or ids.shape != weights.shape \
+            or ids.shape[0] != x.shape[0] or not weights.is_contiguous():
+        raise ValueError("ids (int32) and weights (float32) must be contiguous and (N, top_k)")
+    top_k = _ints(ids, "ids").shape[1]
+    gd, dd, xd = w_gate._desc(), w_down._desc(), _dense(x, BF16)
+    out, yd = _dense_out(out, stream, x.device, dtype, x.shape[0], w_down.M)
+    if workspace is None:
+        workspace = _workspace(stream, x.device, int(lib().qmm_moe_gemm_workspace_size(gd, dd, xd, top_k)))
+    else:
+        _need_bytes(workspace, 0, "workspace")
+    dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)
+    _launch(dev, stream, "qmm_moe_gemm_swiglu", gd, w_up._desc(), dd, xd, ids.data_ptr(), weights.data_ptr(), top_k, yd,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def _adapters(t: torch.Tensor) -> bytes:
+    """bf16 matrices (L, rows, cols), each row contiguous -> ne = [cols, rows, L]."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError("adapters must be bfloat16 (L, rows, cols)")
+    (apart, pitch, step), (L, rows, cols) = t.stride(), t.shape
+    if rows == 0 or cols == 0:          # empty: strides are meaningless
+        apart, pitch, step = rows * cols, cols, 1
+    if step != 1 and cols > 1:
+        raise ValueError("adapter rows must be contiguous")
+    return _PACK(BF16, 3, cols, rows, L, 1, 2, 2 * pitch, 2 * apart, 2 * apart * L, t.data_ptr())
+
+
+def lora_workspace_size(a: torch.Tensor, x: torch.Tensor) -> int:
+    """Bytes of workspace qmm_lora needs for these shapes."""
+    return int(lib().qmm_lora_workspace_size(_adapters(a), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)))
+
+
+def lora(a: torch.Tensor, b: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, *, scales: torch.Tensor | None = None,
+         base: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
+    """y (N, M) fp32 = base[n] + scales[ids[n]] * (x[n] A^T) B^T with adapter ids[n]:
+    a (L, r, K) and b (L, M, r) bf16, x (N, K) fp32 or bf16, ids (N) int32 (outside
+    0 .. L - 1: no adapter), scales (L) fp32 or None for 1, base (N, M) fp32 or None
+    for 0; out may be base.  workspace: a uint8 device tensor of at least
+    lora_workspace_size bytes, or None to allocate one (graph-capture safe)."""
+    if _ints(ids, "ids").dim() != 1 or x.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError("ids must be (N)")
+    ad, xd = _adapters(a), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)
+    tensors = [a, b, x, ids]
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.shape != (a.shape[0],) or not scales.is_contiguous():
+            raise ValueError("scales must be float32, contiguous and (L)")
+        tensors.append(scales)
+    if base is not None:
+        tensors.append(base)
+    if out is None:
+        out = _output(stream, x.device, torch.float32, x.shape[0], b.shape[1])
+    if workspace is None:
+        workspace = _workspace(stream, x.device, int((_lib or lib()).qmm_lora_workspace_size(ad, xd)))
+    else:
+        _need_bytes(workspace, 0, "workspace")
+    dev = _need_gpu(*tensors, out, workspace)
+    _launch(dev, stream, "qmm_lora", ad, _adapters(b), xd, ids.data_ptr(), None if scales is None else scales.data_ptr(),
+            None if base is None else _dense(base, F32), _dense(out, F32), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out
 
 

@@ -32,6 +32,20 @@ __device__ inline void ll_load(const ll_i32x4 &rsrc, uint32_t lds, uint32_t voff
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                      :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
 }
+// The same with a scalar byte offset added to the lane's: only where lane
+// offset + soff is known to stay inside the buffer, or the lane offset alone is
+// out of range.
+template <int SIZE>
+__device__ inline void ll_load_at(const ll_i32x4 &rsrc, uint32_t lds, uint32_t voff, uint32_t soff)
+{
+    static_assert(SIZE == 4 || SIZE == 16, "dword or dwordx4");
+    if constexpr (SIZE == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :: "s"(lds), "v"(voff), "s"(rsrc), "s"(soff) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                     :: "s"(lds), "v"(voff), "s"(rsrc), "s"(soff) : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // Wait until at most N vector memory operations of this wave are pending.

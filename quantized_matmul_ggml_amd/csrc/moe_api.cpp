@@ -8,62 +8,6 @@ using namespace qmm::api;
 
 namespace {
 
-// Bytes of one expert's matrix.
-uint64_t matrix_bytes(const qmm_tensor *t)
-{
-    const uint64_t rs = qmm_row_size(t->type, t->ne[0]);
-    return t->ne[1] > 0 ? (uint64_t)(t->ne[1] - 1) * t->nb[1] + rs : 0;
-}
-
-// An expert tensor: ne = [K, M, E], quantized rows.
-int check_experts(const qmm_tensor *t)
-{
-    if (!t) return QMM_ERR_NULL;
-    if (!is_quant(t->type)) return QMM_ERR_TYPE;
-    if (t->n_dims != 3 || t->ne[3] != 1) return QMM_ERR_UNSUPPORTED;
-    if (t->ne[2] < 1) return QMM_ERR_SHAPE;
-    if (t->ne[2] >= (1ll << 31)) return QMM_ERR_UNSUPPORTED;
-    // each expert's matrix by the rules of a two-dimensional tensor
-    qmm_tensor m = *t;
-    m.n_dims = 2;
-    m.ne[2] = 1;
-    const int rc = check_tensor(&m, 16);
-    if (rc) return rc;
-    if (t->ne[2] > 1) {
-        if (t->nb[2] < matrix_bytes(t) || t->nb[2] % 16 != 0) return QMM_ERR_LAYOUT;
-        uint64_t span;
-        if (__builtin_mul_overflow((uint64_t)(t->ne[2] - 1), t->nb[2], &span) || span > kMaxSpan ||
-            span + matrix_bytes(t) > kMaxSpan || (uintptr_t)t->data > UINTPTR_MAX - (span + matrix_bytes(t)))
-            return QMM_ERR_UNSUPPORTED;
-    }
-    return QMM_OK;
-}
-
-struct Range {
-    uintptr_t lo, hi;
-};
-Range range_of(const qmm_tensor *t)
-{
-    Range r;
-    if (t->n_dims == 3) {
-        const uint64_t one = matrix_bytes(t);
-        r.lo = (uintptr_t)t->data;
-        r.hi = one ? r.lo + (uint64_t)(t->ne[2] - 1) * t->nb[2] + one : r.lo;
-    } else {
-        extent(t, &r.lo, &r.hi);
-    }
-    return r;
-}
-Range range_of(const void *p, uint64_t bytes) { return Range{(uintptr_t)p, (uintptr_t)p + bytes}; }
-bool meet(Range a, Range b) { return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi; }
-// Whether `bytes` bytes at p are a range of the address space.
-bool spans(const void *p, uint64_t bytes) { return bytes <= kMaxSpan && (uintptr_t)p <= UINTPTR_MAX - bytes; }
-
-qmm::ExpertView expert_view(const qmm_tensor *t)
-{
-    return qmm::ExpertView{weight_view(t), t->ne[2] > 1 ? t->nb[2] : 0, t->ne[2]};
-}
-
 // The shape rules of a layer; on success *ws_bytes is its workspace.
 int check_layer(const qmm_tensor *gate, const qmm_tensor *up, const qmm_tensor *down, const qmm_tensor *x, int32_t top_k,
                 uint64_t *ws_bytes)

@@ -170,6 +170,76 @@ hipError_t launch_moe_swiglu(const ExpertView &gate, const ExpertView &up, const
                              const int32_t *ids, const float *weights, int k, const OutView &y, void *ws,
                              hipStream_t stream);
 
+// Products grouped by expert (gemm_grouped.hip): R rows, group e's from
+// offsets[e] to offsets[e + 1] (device memory, as the kernel finds them cut to
+// 0 .. R), times expert e's weights; row r takes token order[r] / top_k of x, or
+// token r without an order.  With `up`, w is the gate of a fused SwiGLU pair.
+struct GroupedOut {
+    void *data;
+    uint64_t pitch_elems;
+    int64_t R;
+    bool bf16;
+};
+// The most row tiles of bn rows that R rows of E groups can need.
+inline int64_t grouped_row_tiles(int64_t R, int64_t E, int bn)
+{
+    const int64_t used = E < R ? E : R;
+    return (R + used * (bn - 1)) / bn;
+}
+// Waves of a workgroup that split K (1, 2 or 4), which makes its tile 128, 64
+// or 32 rows.
+inline int grouped_k_waves(int64_t R, int64_t E)
+{
+    return R >= 96 * E ? 1 : R >= 40 * E ? 2 : 4;
+}
+// Workgroups of the launch stay below 2^24 (kMaxGridThreads).
+inline bool grouped_fits(int64_t M, int64_t R, int64_t E, bool swiglu)
+{
+    const int kp = grouped_k_waves(R, E), bm = (swiglu ? 64 : 128) / kp;
+    const int64_t m = (M + bm - 1) / bm, n = grouped_row_tiles(R, E, 128 / kp), most = (int64_t)(kMaxGridThreads / 256) - 1;
+    return m <= most && n <= most && m * n <= most;
+}
+hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const ActView &x, const int32_t *offsets,
+                               const int32_t *order, int top_k, const GroupedOut &y, hipStream_t stream);
+
+// Slots grouped by expert (moe_group.hip): S ids of E experts.  Workgroups: one
+// up to kGroupSlots slots, whose counts need no workspace.
+constexpr int64_t kGroupSlots = 16384;
+inline int64_t moe_group_chunks(int64_t S)
+{
+    const int64_t n = (S + kGroupSlots / 2 - 1) / (kGroupSlots / 2);
+    return S <= kGroupSlots ? 1 : n < 64 ? n : 64;
+}
+inline uint64_t moe_group_workspace(int64_t S, int64_t E)
+{
+    const int64_t n = moe_group_chunks(S);
+    return n > 1 ? (uint64_t)(n * (E + 1)) * 4 : 0;
+}
+hipError_t launch_moe_group(const int32_t *ids, int64_t S, int64_t E, int32_t *offsets, int32_t *order, int32_t *place,
+                            void *ws, hipStream_t stream);
+// y[n] = the sum of weights[n][s] times row place[n][s] of d (rows a multiple
+// of four floats apart, 16-byte aligned) over s < k; negative places are empty.
+hipError_t launch_moe_combine(const float *d, uint64_t d_pitch, const int32_t *place, const float *weights, int k,
+                              int64_t N, int64_t M, const GroupedOut &y, hipStream_t stream);
+
+// Low-rank adapters (lora.hip): shapes as checked by the caller, pitches in
+// elements, ws as large as lora_plan.h's parts need.
+struct LoraTask {
+    const uint16_t *a, *b;
+    uint64_t a_pitch, b_pitch, a_adapter, b_adapter;
+    const void *x;
+    uint64_t x_pitch;
+    bool f32x;
+    const int32_t *ids;
+    const float *scales, *base;
+    uint64_t base_pitch;
+    float *y;
+    uint64_t y_pitch;
+    void *ws;
+    int64_t N, K, M, r, L;
+};
+hipError_t launch_lora(const LoraTask &t, hipStream_t stream);
+
 // Which launches the matrix-core kernels take (measured on the decoder's
 // shapes, graph-replayed): from 5 tokens every one; at 3 and 4 tokens those
 // of more than 2048 rows or of rows over 4096 (5632 x 2048: 5.8 against
