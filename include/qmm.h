@@ -483,7 +483,7 @@ QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up
  * a: BF16 ne = [K, r, L] (n_dims 3), b: BF16 ne = [r, M, L], each matrix and row
  * 16-byte aligned;  K % 32 = 0, r % 8 = 0, 8 <= r <= QMM_LORA_MAX_RANK (else
  * QMM_ERR_SHAPE);  x: F32 or BF16 (16-byte aligned rows) ne = [K, N], N <=
- * QMM_LORA_MAX_TOKENS, K, M <= 2^28;  ids: N values, read on the device: a token
+ * QMM_LORA_MAX_TOKENS, M and the pitches of x, base and y below 2^24 elements, those of a and b below 2^23;  ids: N values, read on the device: a token
  * whose id is negative or not below L has no adapter, its y is base;  scales: L
  * values s_a, or NULL for 1;  base: F32 ne = [M, N] (the shared projection's
  * output), or NULL for 0;  y: F32 ne = [M, N], which may be base itself (same data

@@ -79,46 +79,26 @@ struct GrpArgs {
 template <int E>
 __device__ inline float sbyte(uint32_t w) { return (float)(int8_t)(w >> (8 * E)); }
 
-// One lane's 16 weights of a block as bf16 pairs, k = 8 h .. 8 h + 7 in b[0..3]
-// and 16 + 8 h .. 16 + 8 h + 7 in b[4..7] (h: the lane's half of the wave).
+// Pair P of one lane's 16 weights of a block as bf16: k = 8 h + 2 P, + 1 for P < 4
+// and 16 + 8 h + 2 (P - 4), + 1 from there on (h: the lane's half of the wave).
 //  Q4_0: a nibble with its top bit flipped, at the top of a byte, is the int8
 //        16 (code - 8); the block's scale takes the 16 back.
 //  Q8_0: the signed bytes themselves.
 //  MXFP4: the value times its scale, exactly.
-template <int WT>
-__device__ inline void unpack(u32x2 c0, u32x2 c1, float scale, u32x4 &lo, u32x4 &hi)
+template <int WT, int P>
+__device__ inline uint32_t unpack_pair(u32x2 c0, u32x2 c1, float scale)
 {
+    constexpr int i = P / 2 % 2, e = 2 * (P % 2);
     if constexpr (WT == W_Q4_0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t v = c0[i] ^ 0x88888888u;
-            const uint32_t a = (v << 4) & 0xF0F0F0F0u, b = v & 0xF0F0F0F0u;
-            lo[2 * i] = pack_bf16(sbyte<0>(a), sbyte<1>(a));
-            lo[2 * i + 1] = pack_bf16(sbyte<2>(a), sbyte<3>(a));
-            hi[2 * i] = pack_bf16(sbyte<0>(b), sbyte<1>(b));
-            hi[2 * i + 1] = pack_bf16(sbyte<2>(b), sbyte<3>(b));
-        }
+        const uint32_t v = c0[i] ^ 0x88888888u, b = (P < 4 ? v << 4 : v) & 0xF0F0F0F0u;
+        return pack_bf16(sbyte<e>(b), sbyte<e + 1>(b));
     } else if constexpr (WT == W_Q8_0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            lo[2 * i] = pack_bf16(sbyte<0>(c0[i]), sbyte<1>(c0[i]));
-            lo[2 * i + 1] = pack_bf16(sbyte<2>(c0[i]), sbyte<3>(c0[i]));
-            hi[2 * i] = pack_bf16(sbyte<0>(c1[i]), sbyte<1>(c1[i]));
-            hi[2 * i + 1] = pack_bf16(sbyte<2>(c1[i]), sbyte<3>(c1[i]));
-        }
+        const uint32_t b = P < 4 ? c0[i] : c1[i];
+        return pack_bf16(sbyte<e>(b), sbyte<e + 1>(b));
     } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t a = c0[i] & 0x0F0F0F0Fu, b = (c0[i] >> 4) & 0x0F0F0F0Fu;
-            const uint32_t p = a | (a >> 4), q = b | (b >> 4);
-            auto cvt = [&](uint32_t v, auto SEL) {
-                return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, decltype(SEL)::value));
-            };
-            lo[2 * i] = cvt(p, std::integral_constant<int, 0>{});
-            lo[2 * i + 1] = cvt(p, std::integral_constant<int, 2>{});
-            hi[2 * i] = cvt(q, std::integral_constant<int, 0>{});
-            hi[2 * i + 1] = cvt(q, std::integral_constant<int, 2>{});
-        }
+        // the even and odd bytes' nibbles side by side: a pair is neighbouring k
+        const uint32_t n = (P < 4 ? c0[i] : c0[i] >> 4) & 0x0F0F0F0Fu;
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(n | (n >> 4), scale, e));
     }
 }
 
@@ -254,26 +234,29 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
                               ? (uint32_t)(smr * (scale_upper ? a.pitch2 : a.pitch)) + 4u * (lane % DPR) : OUT_OF_RANGE;
     const int sk = (a.K / 32 * 2 >> SS) - 4 * (lane % DPR);
     const int full = a.K / BK;                           // steps wholly in K
-    auto issue = [&](int s, int stage) {
+    // Load L of a wave for step s.  FAST: the step is wholly in K, its offset goes
+    // in as a scalar; else every lane is checked against K (past the last step
+    // all read zeros).
+    auto load = [&](auto FAST, auto L, int s, int stage) {
+        constexpr int l = decltype(L)::value;
+        constexpr bool fast = decltype(FAST)::value;
         const uint32_t base = lds0 + (uint32_t)(stage * T::STAGE) + 1024u * wave;
-        const uint32_t sb = (uint32_t)(STEP_SCALES * s) & ~3u;
-        const uint32_t sdst = lds0 + (uint32_t)(stage * T::STAGE + T::SCALE_OFF) + 256u * wave;
-        if (s < full) {
-#pragma unroll
-            for (int i = 0; i < T::TOK_LOADS; ++i) ll_load_at<16>(xres, base + 4096u * i, xoff[i], 2u * BK * s);
-#pragma unroll
-            for (int i = 0; i < T::CODE_LOADS; ++i)
-                ll_load_at<16>(code_upper(i) ? ures : wres, base + T::CODE_OFF + 4096u * i, coff[i], 16u * T::UPR * s);
-            ll_load_at<4>(scale_upper ? ures : wres, sdst, soff, sb);
+        if constexpr (l < T::TOK_LOADS) {
+            const uint32_t dst = base + 4096u * l, o = 2u * BK * s;
+            if constexpr (fast) ll_load_at<16>(xres, dst, xoff[l], o);
+            else ll_load<16>(xres, dst, BK * s < xk[l] ? xoff[l] + o : OUT_OF_RANGE);
+        } else if constexpr (l < T::TOK_LOADS + T::CODE_LOADS) {
+            constexpr int i = l - T::TOK_LOADS;
+            const uint32_t dst = base + T::CODE_OFF + 4096u * i, o = 16u * T::UPR * s;
+            const ll_i32x4 &res = code_upper(i) ? ures : wres;
+            if constexpr (fast) ll_load_at<16>(res, dst, coff[i], o);
+            else ll_load<16>(res, dst, (int)o < ck[i] && coff[i] != OUT_OF_RANGE ? coff[i] + o : OUT_OF_RANGE);
         } else {
-#pragma unroll
-            for (int i = 0; i < T::TOK_LOADS; ++i)
-                ll_load<16>(xres, base + 4096u * i, BK * s < xk[i] ? xoff[i] + 2u * BK * s : OUT_OF_RANGE);
-#pragma unroll
-            for (int i = 0; i < T::CODE_LOADS; ++i)
-                ll_load<16>(code_upper(i) ? ures : wres, base + T::CODE_OFF + 4096u * i,
-                            16 * T::UPR * s < ck[i] && coff[i] != OUT_OF_RANGE ? coff[i] + 16u * T::UPR * s : OUT_OF_RANGE);
-            ll_load<4>(scale_upper ? ures : wres, sdst, (int)sb < sk && soff != OUT_OF_RANGE ? soff + sb : OUT_OF_RANGE);
+            const uint32_t dst = lds0 + (uint32_t)(stage * T::STAGE + T::SCALE_OFF) + 256u * wave;
+            const uint32_t o = (uint32_t)(STEP_SCALES * s) & ~3u;
+            const ll_i32x4 &res = scale_upper ? ures : wres;
+            if constexpr (fast) ll_load_at<4>(res, dst, soff, o);
+            else ll_load<4>(res, dst, (int)o < sk && soff != OUT_OF_RANGE ? soff + o : OUT_OF_RANGE);
         }
     };
 
@@ -300,64 +283,115 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
 
-    auto multiply = [&](const uint8_t *st, int s) {
+    // ---- the steps ----
+    // A unit is one tile's products with one block (two blocks that share a
+    // scale): its matrix instructions start from zero and their sums are scaled
+    // and added while the next unit's run.  Each matrix instruction is followed
+    // by its share of that, of the second block's unpacking and of the fragment
+    // and LDS loads, in this order: with the two waves of a SIMD out of step, one's
+    // vector work runs beside the other's matrix work (all loads of a step issued
+    // together took 367 us instead of XXX for 8186 rows x 2048 x 5632 Q8_0).
+    constexpr bool SCALED = WT != W_MXFP4;
+    constexpr int PER = SCALED && SS ? 2 : 1;            // blocks of a unit
+    constexpr int UNITS = 2 / PER * TT, PU = 2 * PER;    // units per step, instructions per unit
+    constexpr int MI = UNITS * PU, AHEAD = MI < 4 ? MI : 4;
+    f32x16 sum[2] = {};                                  // of the units at hand
+    float pending = 0.0f;                                // the last unit's scale
+    auto add = [&](auto U, int from, int to, float d) {  // unit U's sums, registers from .. to - 1
+        constexpr int j = decltype(U)::value % TT;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (r >= from && r < to) acc[j][r] = fmaf(sum[decltype(U)::value & 1][r], d, acc[j][r]);
+    };
+    // step s from its stage, and the loads of step s + kStages - 1 into another
+    auto multiply = [&](auto FAST, const uint8_t *st, int s, int next) {
+        u32x2 c0[2], c1[2];
+        float d[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int bi = 2 * par + b;                  // block of the step
-            u32x2 c0, c1;
             if constexpr (T::QB == 16) {
-                c0 = *reinterpret_cast<const u32x2 *>(st + code_at(bi));
-                c1 = c0;
+                c0[b] = c1[b] = *reinterpret_cast<const u32x2 *>(st + code_at(bi));
             } else {
-                c0 = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi));
-                c1 = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi + 1));
-            }
-            // a block past K gets a zero scale
-            const bool live = 2 * KP * s + bi < blocks;
-            float d;
-            if constexpr (WT == W_MXFP4) {
-                const uint32_t byte = st[s_row + (KP == 1 ? 2 * (s & 1) : 0) + bi];
-                d = __builtin_bit_cast(float, live ? byte << 23 : 0u);
-            } else {
-                const uint32_t o = SS ? (KP == 1 ? 2 * (s & 1) : 2 * (bi >> 1)) : 2 * bi;
-                d = live ? (float)*reinterpret_cast<const _Float16 *>(st + s_row + o) : 0.0f;
-                if constexpr (WT == W_Q4_0) d *= 0.0625f;
-            }
-            u32x4 lo, hi;
-            unpack<WT>(c0, c1, d, lo, hi);
-            const bf16x8 b0 = __builtin_bit_cast(bf16x8, lo), b1 = __builtin_bit_cast(bf16x8, hi);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) {
-                auto frag = [&](int c) {
-                    const uint32_t q = (uint32_t)(8 * par + 4 * b + 2 * c + h);
-                    return *reinterpret_cast<const bf16x8 *>(st + t_row[j] + 16u * (q ^ t_sw[j]));
-                };
-                if constexpr (WT == W_MXFP4) {
-                    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(0), b0, acc[j], 0, 0, 0);
-                    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(1), b1, acc[j], 0, 0, 0);
-                } else {
-                    f32x16 sum = {};
-                    sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(0), b0, sum, 0, 0, 0);
-                    sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(1), b1, sum, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[j][r] = fmaf(sum[r], d, acc[j][r]);
-                }
+                c0[b] = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi));
+                c1[b] = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi + 1));
             }
         }
+        uint32_t raw[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int bi = 2 * par + b;
+            if constexpr (WT == W_MXFP4) raw[b] = st[s_row + (KP == 1 ? 2 * (s & 1) : 0) + bi];
+            else raw[b] = *reinterpret_cast<const uint16_t *>(st + s_row + (SS ? (KP == 1 ? 2 * (s & 1) : 2 * (bi >> 1)) : 2 * bi));
+        }
+        // instruction k: block b, tile j, chunk c of the block
+        auto frag = [&](auto K) {
+            constexpr int k = decltype(K)::value, u = k / PU, b = PER == 2 ? k % PU / 2 : u / TT, j = u % TT, c = k % 2;
+            const uint32_t q = (uint32_t)(8 * par + 4 * b + 2 * c + h);
+            return *reinterpret_cast<const bf16x8 *>(st + t_row[j] + 16u * (q ^ t_sw[j]));
+        };
+        bf16x8 x[AHEAD];
+        static_for<AHEAD>([&](auto K) { x[decltype(K)::value] = frag(K); });
+        if constexpr (SCALED && UNITS > 1) add(std::integral_constant<int, UNITS - 1>{}, 0, 16, pending);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            // a block past K gets a zero scale (a mask: no branch between the products)
+            raw[b] &= 2 * KP * s + 2 * par + b < blocks ? 0xFFFFu : 0u;
+            if constexpr (WT == W_MXFP4) d[b] = __builtin_bit_cast(float, raw[b] << 23);
+            else d[b] = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[b]) * (WT == W_Q4_0 ? 0.0625f : 1.0f);
+        }
+        u32x4 w[2][2];
+        static_for<8>([&](auto P) {
+            constexpr int p = decltype(P)::value;
+            w[0][p / 4][p % 4] = unpack_pair<WT, p>(c0[0], c1[0], d[0]);
+        });
+        static_for<MI>([&](auto K) {
+            constexpr int k = decltype(K)::value, u = k / PU, b = PER == 2 ? k % PU / 2 : u / TT, j = u % TT, c = k % 2;
+            const bf16x8 wf = __builtin_bit_cast(bf16x8, w[b][c]), xf = x[k % AHEAD];
+            if constexpr (!SCALED) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, acc[j], 0, 0, 0);
+            else if constexpr (k % PU == 0) sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, f32x16{}, 0, 0, 0);
+            else sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, sum[u & 1], 0, 0, 0);
+            if constexpr (k + AHEAD < MI) x[k % AHEAD] = frag(std::integral_constant<int, k + AHEAD>{});
+            constexpr int per = (T::LOADS + MI - 1) / MI, gap = per > 1 ? 1 : MI / T::LOADS;
+            static_for<per>([&](auto I) {
+                constexpr int l = k / gap * per + decltype(I)::value;
+                if constexpr (k % gap == 0 && l < T::LOADS) load(FAST, std::integral_constant<int, l>{}, s + kStages - 1, next);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+            // the second block's pairs, before the first instruction that takes them
+            constexpr int B1 = PER == 2 ? 2 : MI / 2, n = (8 + B1 - 1) / B1;
+            static_for<n>([&](auto I) {
+                constexpr int p = k * n + decltype(I)::value;
+                if constexpr (k < B1 && p < 8) w[1][p / 4][p % 4] = unpack_pair<WT, p>(c0[1], c1[1], d[1]);
+            });
+            // the unit before
+            constexpr int share = 16 / PU;
+            if constexpr (SCALED && u > 0)
+                add(std::integral_constant<int, u - 1>{}, share * (k % PU), share * (k % PU + 1), d[PER == 2 ? 0 : (u - 1) / TT]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (SCALED) {
+            pending = d[PER == 2 ? 0 : 1];
+            if constexpr (UNITS == 1) add(std::integral_constant<int, 0>{}, 0, 16, pending);
+        }
     };
-
-    // ---- the steps ----
-    for (int s = 0; s < kStages - 1; ++s) issue(s, s);
+    for (int s = 0; s < kStages - 1; ++s)
+        static_for<T::LOADS>([&](auto L) { load(std::false_type{}, L, s, s); });
     int stage = 0, next = kStages - 1;
-    for (int s = 0; s < steps; ++s) {
-        ll_wait<T::LOADS * (kStages - 2)>();             // this wave's loads of step s have landed
-        // every wave's have, and the stage of step s - 1 is free
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        issue(s + kStages - 1, next);                    // past the last step: zeros
-        multiply(lds + stage * T::STAGE, s);
-        next = stage;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-    }
+    auto run_steps = [&](auto FAST, int s, int to) {
+        for (; s < to; ++s) {
+            ll_wait<T::LOADS * (kStages - 2)>();         // this wave's loads of step s have landed
+            // every wave's have, and the stage of step s - 1 is free
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            multiply(FAST, lds + stage * T::STAGE, s, next);
+            next = stage;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+    };
+    const int fast_to = full - (kStages - 1) > 0 ? full - (kStages - 1) : 0;
+    run_steps(std::true_type{}, 0, fast_to);
+    run_steps(std::false_type{}, fast_to, steps);
+    if constexpr (SCALED && UNITS > 1) add(std::integral_constant<int, UNITS - 1>{}, 0, 16, pending);
 
     // ---- the KP waves of a sub-tile add their sums, each a part of them ----
     ll_wait<0>();                    // no load may still write the ring

@@ -12,7 +12,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (1ll << 31) - 1;        // grouped rows, tokens: 32-bit numbers
 constexpr int64_t kMaxDim = 1ll << 28;               // K and M
-constexpr uint64_t kMaxPitch = 1ull << 24;           // of weight rows: 128 of them below 2^31 bytes
+constexpr uint64_t kMaxPitch = 1ull << 24;           // of weight rows (bytes: 128 below 2^31), base and y (floats: 32)
 
 uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
 
@@ -147,10 +147,17 @@ int check_lora(const qmm_tensor *a, const qmm_tensor *x)
     return QMM_OK;
 }
 
+// What either form of the first launch needs, so that it does not depend on
+// where x lies.
 uint64_t lora_workspace(int64_t N, int64_t K, int64_t r)
 {
-    const qmm::LoraPlan p = qmm::plan_lora(N, K, 1, r, qmm::device_cus());
-    return (uint64_t)p.chunks * (uint64_t)N * 16 * (uint64_t)p.rt * 4;
+    uint64_t most = 0;
+    for (const bool wide : {false, true}) {
+        const qmm::LoraPlan p = qmm::plan_lora(N, K, 1, r, wide, qmm::device_cus());
+        const uint64_t bytes = (uint64_t)p.chunks * (uint64_t)N * 16 * (uint64_t)p.rt * 4;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 }  // namespace
@@ -269,11 +276,14 @@ int qmm_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x, cons
         if (base->type != QMM_TYPE_F32) return QMM_ERR_TYPE;
         if (base->ne[0] != M || base->ne[1] != N) return QMM_ERR_SHAPE;
     }
-    if (M > kMaxDim) return QMM_ERR_UNSUPPORTED;
+    // 32 rows of x, base and y and 128 rows of A and B are reached with 32-bit offsets
+    if (pitch_elems(x) >= kMaxPitch || pitch_elems(a) >= kMaxPitch / 2 || pitch_elems(b) >= kMaxPitch / 2) return QMM_ERR_UNSUPPORTED;
+    if (M > kMaxDim || pitch_elems(y) >= kMaxPitch || (base && pitch_elems(base) >= kMaxPitch)) return QMM_ERR_UNSUPPORTED;
     if (N == 0 || M == 0) return QMM_OK;
-    const qmm::LoraPlan p = qmm::plan_lora(N, K, M, r, qmm::device_cus());
+    const bool f32x = x->type == QMM_TYPE_F32;
+    const qmm::LoraPlan p = qmm::plan_lora(N, K, M, r, qmm::lora_wide(x->data, pitch_elems(x), f32x), qmm::device_cus());
     const int64_t most = (int64_t)(qmm::kMaxGridThreads / 256) - 1;
-    if (p.tasks1 / 4 >= most || p.blocks2 > most) return QMM_ERR_UNSUPPORTED;
+    if (2 * p.blocks1 > most || p.blocks2 > most) return QMM_ERR_UNSUPPORTED;
     const uint64_t need = lora_workspace(N, K, r);
     if (!ids || (need && !workspace)) return QMM_ERR_NULL;
     if (((uintptr_t)ids | (uintptr_t)scales) % 4 != 0 || (need && (uintptr_t)workspace % 16 != 0)) return QMM_ERR_LAYOUT;
@@ -299,7 +309,7 @@ int qmm_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x, cons
     t.b_adapter = L > 1 ? b->nb[2] / 2 : 0;
     t.x = x->data;
     t.x_pitch = pitch_elems(x);
-    t.f32x = x->type == QMM_TYPE_F32;
+    t.f32x = f32x;
     t.ids = ids;
     t.scales = scales;
     t.base = base ? static_cast<const float *>(base->data) : nullptr;

@@ -74,6 +74,22 @@ def test_lora_in_place_pitches_and_runs():
     assert (y[:, M:] == 7).all()
 
 
+@pytest.mark.parametrize("pad,shift", [(4, 0), (1, 0), (8, 3)])
+def test_lora_many_tokens_at_any_alignment(pad, shift):
+    """More than 512 binary32 tokens with aligned rows, odd pitches and odd starts."""
+    print(f"[case] lora pad {pad} shift {shift}", flush=True)
+    rng = np.random.default_rng(pad + shift)
+    N, L, r, K, M = 530, 9, 16, 224, 40
+    a, A, b, Bm, x, X, ids, s, base = _case(rng, N, L, r, K, M, "f32")
+    ids = np.sort(ids)
+    wide = torch.full((N, K + pad), float("nan"), device=DEV)
+    view = wide[:, shift:shift + K]
+    view.copy_(x)
+    ref, bound = G.lora(A, Bm, X, ids, s, base)
+    y = Q.lora(a, b, view, _dev(ids), scales=_dev(s), base=_dev(base))
+    _check(y, ref, bound, "aligned" if pad % 4 == 0 and shift == 0 else "odd")
+
+
 def test_lora_wild_ids_and_special_values_stay_in_their_token():
     print("[case] lora special values", flush=True)
     rng = np.random.default_rng(2)
