@@ -430,7 +430,7 @@ QMM_API int qmm_moe_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, con
  * place: n_slots values, the position in order of each slot, -1 for an empty one.
  * All are 4-byte aligned device memory (ids too), none overlapping another.
  * 1 <= n_experts <= QMM_MOE_MAX_ROUTED, n_slots < 2^31.  n_slots = 0 fills offsets
- * with zeros.  workspace: qmm_moe_group_workspace_size bytes (0 up to 16384
+ * with zeros.  workspace: qmm_moe_group_workspace_size bytes (0 up to 65536
  * slots), 16-byte aligned, scratch for this call alone until its kernels have
  * run (fewer bytes: QMM_ERR_SCRATCH). */
 QMM_API size_t qmm_moe_group_workspace_size(int64_t n_slots, int32_t n_experts);

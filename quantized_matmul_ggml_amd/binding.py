@@ -628,7 +628,7 @@ def _dense_out(out, stream, device, dtype, rows: int, cols: int) -> tuple:
 
 
 def moe_group_workspace_size(n_slots: int, n_experts: int) -> int:
-    """Bytes of workspace qmm_moe_group needs (0 up to 16384 slots)."""
+    """Bytes of workspace qmm_moe_group needs (0 up to 65536 slots)."""
     return int(lib().qmm_moe_group_workspace_size(n_slots, n_experts))
 
 

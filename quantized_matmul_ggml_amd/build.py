@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqmm.so")
 SOURCES = ["qmm_api.cpp", "moe_api.cpp", "grouped_api.cpp", "quant.hip", "gemv.hip", "gemv_i8.hip", "gemv_mf.hip",
            "gemv_mx.hip", "gemm.hip", "gemm_rq.hip", "gemm_mx.hip", "moe.hip", "moe_group.hip",
-           "gemm_grouped.hip", "lora.hip", "records.hip", "probe.hip"]
+           "gemm_grouped.hip", "gemm_rows.hip", "lora.hip", "records.hip", "probe.hip"]
 ARCH = os.environ.get("QMM_OFFLOAD_ARCH", "gfx950")
 
 

@@ -24,6 +24,7 @@
 // each; two workgroups share a CU, so that one's matrix instructions run
 // beside the other's waits, unpacking and epilogue.
 #include "gemm_common.h"
+#include "grouped_tile.h"
 #include "lds_load.h"
 
 namespace qmm {
@@ -59,22 +60,6 @@ struct GrpTile {
     static_assert(KP == 1 || 4 * 64 * TT * 16 * 4 <= LDS_BYTES, "the waves' sums fit the ring");
 };
 
-struct GrpArgs {
-    const uint8_t *w, *w2;        // SW: the gate and the up matrices
-    uint64_t pitch, pitch2;       // bytes between rows
-    uint64_t expert, expert2;     // bytes between experts
-    const uint16_t *x;
-    uint64_t x_pitch;             // elements
-    const int32_t *offsets, *order;
-    void *y;
-    uint64_t y_pitch;             // elements
-    int64_t M;                    // weight rows
-    int32_t K, qoff, E, top_k;
-    int32_t N, R;                 // tokens, grouped rows
-    int32_t m_tiles;
-    int32_t bf16_out;
-};
-
 // Byte E of w as a signed int8, converted to float (one SDWA conversion).
 template <int E>
 __device__ inline float sbyte(uint32_t w) { return (float)(int8_t)(w >> (8 * E)); }
@@ -104,25 +89,6 @@ __device__ inline uint32_t unpack_pair(u32x2 c0, u32x2 c1, float scale)
 
 __device__ inline float grp_swish(float z) { return z / (1.0f + expf(-z)); }
 
-__device__ inline int wave_inclusive_sum(int v, int lane)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_up(v, m);
-        v += lane >= m ? o : 0;
-    }
-    return v;
-}
-
-// A group of rows: expert e's [first, end), cut to the rows that there are,
-// whatever the offsets hold.
-__device__ inline void group_rows(const int32_t *offsets, int e, int R, int &first, int &end)
-{
-    const int a = offsets[e], b = offsets[e + 1];
-    first = a < 0 ? 0 : a > R ? R : a;
-    end = b < first ? first : b > R ? R : b;
-}
-
 template <int WT, int SS, int KP, bool SW>
 __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs a)
 {
@@ -133,48 +99,11 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    // ---- this workgroup's tile ----
-    // Each lane counts the row tiles of a run of experts; the launch has a
-    // workgroup for every tile that R rows of E experts can need, in an order
-    // (expert, weight tile, row tile) whose consecutive tiles share weights;
-    // the eight XCDs take contiguous parts of the tiles that there are.
-    const int run = (a.E + 63) / 64;
-    int mine = 0;
-    for (int i = 0; i < run; ++i) {
-        const int e = lane * run + i;
-        if (e < a.E) {
-            int first, end;
-            group_rows(a.offsets, e, a.R, first, end);
-            mine += (end - first + BN - 1) / BN;
-        }
-    }
-    const int upto = wave_inclusive_sum(mine, lane);
-    const int64_t total = (int64_t)__builtin_amdgcn_readlane(upto, 63) * a.m_tiles;
-    if ((int64_t)blockIdx.x >= total) return;
-    const int nwg = (int)(total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x);
-    const int x8 = (int)blockIdx.x % 8, q8 = nwg / 8, r8 = nwg % 8;
-    const int at = x8 * q8 + (x8 < r8 ? x8 : r8) + (int)blockIdx.x / 8;
-    const int row_tile = at / a.m_tiles;
-    const int owner = __builtin_ctzll(__ballot(upto > row_tile));
-    int before = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner);
-    int e = owner * run, first = 0, end = 0, tiles = 0;
-    for (;; ++e) {
-        group_rows(a.offsets, e, a.R, first, end);
-        tiles = (end - first + BN - 1) / BN;
-        if (row_tile < before + tiles) break;
-        before += tiles;
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    first = __builtin_amdgcn_readfirstlane(first);
-    end = __builtin_amdgcn_readfirstlane(end);
-    tiles = __builtin_amdgcn_readfirstlane(tiles);
-    const int local = at - __builtin_amdgcn_readfirstlane(before) * a.m_tiles;
-    const int mt = __builtin_amdgcn_readfirstlane(local / tiles);
-    const int nt = local - mt * tiles;
+    GroupTile tile;
+    if (!find_tile<BN>(a, tile)) return;
+    const int e = tile.e, n0 = tile.n0, toks = tile.rows;
     constexpr int MROWS = SW ? T::BM / 2 : T::BM;         // matrix rows per tile
-    const int64_t m0 = (int64_t)mt * MROWS;
-    const int n0 = first + nt * BN;
-    const int toks = end - n0 < BN ? end - n0 : BN;
+    const int64_t m0 = (int64_t)tile.mt * MROWS;
 
     // ---- loads ----
     // Activations: load i of a thread is unit 256 i + thread of the tile's
@@ -191,12 +120,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
     for (int i = 0; i < T::TOK_LOADS; ++i) {
         const int u = kThreads * i + (int)threadIdx.x, t = u / T::TPR;
         const int q = u % T::TPR ^ (T::TPR >= 16 ? t & 15 : t >> 1 & 7);
-        int row = t < toks ? t : -1;
-        if (a.order && row >= 0) {
-            const int slot = a.order[n0 + t];
-            row = slot >= 0 ? slot / a.top_k : -1;
-            if (row >= a.N) row = -1;
-        }
+        const int row = t >= toks ? -1 : a.order ? token_of(a, n0 + t) : t;
         xoff[i] = row >= 0 ? (uint32_t)((uint64_t)row * a.x_pitch * 2) + 16u * q : OUT_OF_RANGE;
         xk[i] = row >= 0 ? a.K - 8 * q : INT32_MIN;      // the chunk of step s is in K iff BK s < xk
     }
@@ -490,8 +414,9 @@ hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const 
     a.N = (int32_t)x.N;
     a.R = (int32_t)y.R;
     a.bf16_out = y.bf16;
-    const int kp = grouped_k_waves(y.R, w.E);
     const bool sw = up != nullptr;
+    if (grouped_streams(y.R, w.E)) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
+    const int kp = grouped_k_waves(y.R, w.E);
     if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, kp, sw, stream);
     if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, kp, sw, stream) : launch_type<W_Q4_0, 0>(a, kp, sw, stream);
     if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, kp, sw, stream) : launch_type<W_Q8_0, 0>(a, kp, sw, stream);

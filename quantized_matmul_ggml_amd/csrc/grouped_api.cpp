@@ -59,6 +59,12 @@ qmm::GroupedOut grouped_out(const qmm_tensor *y)
     return qmm::GroupedOut{y->data, pitch_elems(y), y->ne[1], y->type == QMM_TYPE_BF16};
 }
 
+// Whether R rows times w's experts make a launch that one grid takes.
+bool fits(const qmm_tensor *w, int64_t R, bool swiglu)
+{
+    return qmm::grouped_fits(w->ne[1], w->ne[0], R, w->ne[2], weight_view(w).type, swiglu, qmm::device_cus());
+}
+
 // The products of one launch; up is w again without SwiGLU.
 int grouped(const qmm_tensor *w, const qmm_tensor *up, bool swiglu, const qmm_tensor *x, const int32_t *offsets,
             const int32_t *order, int32_t top_k, qmm_tensor *y, void *stream)
@@ -69,7 +75,7 @@ int grouped(const qmm_tensor *w, const qmm_tensor *up, bool swiglu, const qmm_te
     if (rc) return rc;
     const int64_t R = y->ne[1], E = w->ne[2];
     if (y->ne[0] != w->ne[1] || top_k < 1 || (!order && x->ne[1] != R)) return QMM_ERR_SHAPE;
-    if (R > kMaxRows || !x_reach(x, order != nullptr) || !qmm::grouped_fits(w->ne[1], R, E, swiglu)) return QMM_ERR_UNSUPPORTED;
+    if (R > kMaxRows || !x_reach(x, order != nullptr) || !fits(w, R, swiglu)) return QMM_ERR_UNSUPPORTED;
     if (R == 0 || w->ne[1] == 0) return QMM_OK;
     if (!offsets) return QMM_ERR_NULL;
     if ((uintptr_t)offsets % 4 != 0 || (uintptr_t)order % 4 != 0) return QMM_ERR_LAYOUT;
@@ -120,7 +126,7 @@ int check_layer(const qmm_tensor *gate, const qmm_tensor *up, const qmm_tensor *
     const int64_t R = N * top_k;
     // the rows of h are F apart; a tile has 128 of them
     if (!x_reach(x, true) || 256 * (uint64_t)gate->ne[1] >= 1ull << 31 ||
-        !qmm::grouped_fits(gate->ne[1], R, E, true) || !qmm::grouped_fits(down->ne[1], R, E, false)) return QMM_ERR_UNSUPPORTED;
+        !fits(gate, R, true) || !fits(down, R, false)) return QMM_ERR_UNSUPPORTED;
     return layer_space(N, top_k, E, gate->ne[1], down->ne[1], s) ? QMM_OK : QMM_ERR_UNSUPPORTED;
 }
 

@@ -186,34 +186,54 @@ inline int64_t grouped_row_tiles(int64_t R, int64_t E, int bn)
     const int64_t used = E < R ? E : R;
     return (R + used * (bn - 1)) / bn;
 }
-// Waves of a workgroup that split K (1, 2 or 4), which makes its tile 128, 64
-// or 32 rows.
+// The form of a launch: whether it streams rows (gemm_rows.hip), for experts with
+// few rows; else the waves of a workgroup that split K (1, 2 or 4), which makes
+// its tile 128, 64 or 32 rows.
+inline bool grouped_streams(int64_t R, int64_t E) { return R <= 16 * E; }
 inline int grouped_k_waves(int64_t R, int64_t E)
 {
     return R >= 96 * E ? 1 : R >= 40 * E ? 2 : 4;
 }
-// Workgroups of the launch stay below 2^24 (kMaxGridThreads).
-inline bool grouped_fits(int64_t M, int64_t R, int64_t E, bool swiglu)
+// How the streaming form splits the weight rows: tiles of 16 (SwiGLU: 8) rows,
+// tiles_per_wave to each of a workgroup's eight waves.  A wave has `depth` units
+// in flight, which divide a tile's units as evenly as they can.
+struct RowsPlan {
+    int tiles_per_wave, depth;
+    int64_t m_tiles;
+};
+inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
+    RowsPlan p = {1, 8, 0};
+    const int64_t kpu = type == W_Q8_0 ? 64 : 128, units = (K + kpu - 1) / kpu;
+    const int64_t tiles = (M + (swiglu ? 8 : 16) - 1) / (swiglu ? 8 : 16);
+    if (units % 8 != 0 && units < 32) p.depth = 4;
+    // one workgroup's tiles share its activations: as many as still give every CU
+    // two workgroups, in one pass over K
+    const int64_t used = E < R ? E : R;
+    if (K <= 2048)
+        while (p.tiles_per_wave < 4 && used * tiles >= 8 * 2 * cus * 2 * p.tiles_per_wave) p.tiles_per_wave *= 2;
+    p.m_tiles = (tiles + 8 * p.tiles_per_wave - 1) / (8 * p.tiles_per_wave);
+    return p;
+}
+// Threads of the launch stay below 2^32 (kMaxGridThreads).
+inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+{
+    const bool rows = grouped_streams(R, E);
     const int kp = grouped_k_waves(R, E), bm = (swiglu ? 64 : 128) / kp;
-    const int64_t m = (M + bm - 1) / bm, n = grouped_row_tiles(R, E, 128 / kp), most = (int64_t)(kMaxGridThreads / 256) - 1;
+    const int64_t m = rows ? plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles : (M + bm - 1) / bm;
+    const int64_t n = grouped_row_tiles(R, E, rows ? 16 : 128 / kp), most = (int64_t)(kMaxGridThreads / 512) - 1;
     return m <= most && n <= most && m * n <= most;
 }
 hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const ActView &x, const int32_t *offsets,
                                const int32_t *order, int top_k, const GroupedOut &y, hipStream_t stream);
 
-// Slots grouped by expert (moe_group.hip): S ids of E experts.  Workgroups: one
-// up to kGroupSlots slots, whose counts need no workspace.
-constexpr int64_t kGroupSlots = 16384;
-inline int64_t moe_group_chunks(int64_t S)
-{
-    const int64_t n = (S + kGroupSlots / 2 - 1) / (kGroupSlots / 2);
-    return S <= kGroupSlots ? 1 : n < 64 ? n : 64;
-}
+// Slots grouped by expert (moe_group.hip): S ids of E experts.  One launch up to
+// kGroupAll slots (one workgroup up to kGroupWhole); then two, of kGroupChunks
+// workgroups whose counts lie in the workspace.
+constexpr int64_t kGroupWhole = 4096, kGroupAll = 65536, kGroupChunks = 64;
 inline uint64_t moe_group_workspace(int64_t S, int64_t E)
 {
-    const int64_t n = moe_group_chunks(S);
-    return n > 1 ? (uint64_t)(n * (E + 1)) * 4 : 0;
+    return S > kGroupAll ? (uint64_t)(kGroupChunks * (E + 1)) * 4 : 0;
 }
 hipError_t launch_moe_group(const int32_t *ids, int64_t S, int64_t E, int32_t *offsets, int32_t *order, int32_t *place,
                             void *ws, hipStream_t stream);

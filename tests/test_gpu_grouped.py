@@ -23,7 +23,8 @@ def _dev(a):
 # ---------------------------------------------------------------- grouping
 
 @pytest.mark.parametrize("S,E", [(1, 1), (2, 1024), (63, 3), (64, 2), (65, 8), (1024, 1023), (1025, 1024), (4097, 128),
-                                 (16384, 7), (16385, 7), (40000, 1024), (70000, 1), (200003, 300)])
+                                 (2048, 5), (2049, 5), (4096, 11), (8192, 7), (40000, 1024), (65536, 2), (65537, 2), (70000, 1),
+                                 (131072, 9), (131073, 9), (200003, 300), (524288, 3), (600001, 64)])
 def test_group(S, E):
     print(f"[case] group S {S} E {E}", flush=True)
     rng = np.random.default_rng(S + E)
@@ -72,13 +73,13 @@ def _check(y, ref, bound, what):
 
 
 # counts of rows per expert: tiles of 32, 64 and 128 rows, whole and cut
-COUNTS = {"one": [1], "few": [3, 0, 1, 33, 0, 2], "mid": [64, 0, 41, 130, 63], "many": [128, 5, 0, 300, 129],
+COUNTS = {"one": [1], "some": [25, 40, 0, 33], "few": [3, 0, 1, 33, 0, 2], "mid": [64, 0, 41, 130, 63], "many": [128, 5, 0, 300, 129],
           "ends": [0, 0, 257, 0]}
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("counts", list(COUNTS))
-@pytest.mark.parametrize("K,M", [(64, 1), (128, 130), (320, 70), (1088, 33)])
+@pytest.mark.parametrize("K,M", [(64, 1), (128, 130), (320, 70), (1088, 33), (4224, 40)])
 def test_gemm_grouped(kind, counts, K, M):
     """Rows in order, tail rows outside all groups, then the same rows picked by an order."""
     n = COUNTS[counts]
@@ -109,7 +110,7 @@ def test_gemm_grouped(kind, counts, K, M):
 
 
 @pytest.mark.parametrize("kind,E,n,K,M", [("mxfp4", 64, 5, 160, 40), ("q4_0", 200, 2, 96, 64), ("q8_0", 1024, 1, 64, 32),
-                                          ("q4_b64", 65, 3, 64, 16), ("q8_0", 3, 700, 64, 300), ("mxfp4", 2, 600, 4128, 140)])
+                                          ("q4_b64", 65, 3, 64, 16), ("mxfp4", 40, 9, 2048, 530), ("q4_0", 48, 7, 1408, 600), ("q8_0", 3, 700, 64, 300), ("mxfp4", 2, 600, 4128, 140)])
 def test_gemm_grouped_many(kind, E, n, K, M):
     """More experts than lanes, more tiles than XCDs, long rows."""
     print(f"[case] grouped {kind} E {E} rows {n} K {K} M {M}", flush=True)
