@@ -111,9 +111,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
     // that rows read together fall in different banks.  Rows outside the
     // group, tokens outside x and chunks past K read zeros.
     const int steps = (a.K + BK - 1) / BK;
-    const uint32_t x_bytes = a.order ? (uint32_t)(((uint64_t)(a.N > 0 ? a.N - 1 : 0) * a.x_pitch + a.K) * 2)
-                                     : (uint32_t)(((uint64_t)(toks - 1) * a.x_pitch + a.K) * 2);
-    const ll_i32x4 xres = ll_rsrc(a.order ? a.x : a.x + (uint64_t)n0 * a.x_pitch, a.N > 0 ? x_bytes : 0);
+    const uint32_t x_bytes = (uint32_t)(((uint64_t)((a.order ? a.N : toks) - 1) * a.x_pitch + a.K) * 2);
+    const ll_i32x4 xres = ll_rsrc(a.order ? a.x : a.x + (uint64_t)n0 * a.x_pitch, a.K > 0 ? x_bytes : 0);
     uint32_t xoff[T::TOK_LOADS];
     int xk[T::TOK_LOADS];
 #pragma unroll
@@ -407,7 +406,7 @@ hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const 
     a.y = y.data;
     a.y_pitch = y.pitch_elems;
     a.M = w.w.M;
-    a.K = (int32_t)w.w.K;
+    a.K = x.N > 0 ? (int32_t)w.w.K : 0;         // without tokens every row is zeros
     a.qoff = (int32_t)quant_offset(w.w.K, w.w.scale_shift);
     a.E = (int32_t)w.E;
     a.top_k = top_k;

@@ -105,19 +105,25 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
     uint8_t *const scales = lds + kScales + wave * kScaleLds;
     GroupTile tile;
     if (!find_tile<kRows>(a, tile)) return;
-
     for (int i = tid; i < kZeros / 16; i += kThreads) reinterpret_cast<uint4 *>(lds + kImage)[i] = make_uint4(0, 0, 0, 0);
     const int blocks = a.K / 32, code_bytes = F::BB * blocks, row_bytes = a.qoff + code_bytes;
     const int C = a.tiles_per_wave;
     constexpr int TILE = SW ? 8 : 16;                   // weight rows (of each matrix) of a tile
     const bool upper = SW && j >= 8;
     const int64_t tile0 = ((int64_t)tile.mt * kWaves + wave) * C;
-    auto row_of = [&](int c) {                          // the lane's weight row of tile c
-        int64_t r = (tile0 + c) * TILE + (SW ? j & 7 : j);
-        r = r < a.M ? r : a.M - 1;
-        return upper ? a.w2 + (uint64_t)tile.e * a.expert2 + (uint64_t)r * a.pitch2
-                     : a.w + (uint64_t)tile.e * a.expert + (uint64_t)r * a.pitch;
+    // the lane's matrix and weight row of tile c
+    const uint8_t *const matrix = upper ? a.w2 + (uint64_t)tile.e * a.expert2 : a.w + (uint64_t)tile.e * a.expert;
+    const uint64_t pitch = upper ? a.pitch2 : a.pitch;
+    auto row_of = [&](int c) {
+        const int64_t r = (tile0 + c) * TILE + (SW ? j & 7 : j);
+        return matrix + (uint64_t)(r < a.M ? r : a.M - 1) * pitch;
     };
+    // this thread's share of the activations: of one grouped row, every 32nd piece
+    // of eight values
+    constexpr int PIECES = kImage / (kThreads * 16);
+    const int xt = tid / 32, xp = tid % 32;
+    const int token = xt < tile.rows ? token_of(a, tile.n0 + xt) : -1;
+    const uint16_t *const x = a.x + (uint64_t)(token > 0 ? token : 0) * a.x_pitch;
     const int units = (blocks + MF - 1) / MF, pass_units = kImage / (MF * kBlockBytes);
     Unit<WT, SS> z[D];
     ScaleWindow<WT, SS, false, D> window;
@@ -144,7 +150,18 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
     for (int u0 = 0; u0 < units; u0 += pass_units) {
         const int len = units - u0 < pass_units ? units - u0 : pass_units;
         const int groups = (len + D - 1) / D, total = groups * C;
-        // ---- the first units of weights, then the activations ----
+        // ---- the activations, then the first units of weights: loads complete in
+        // order, and the activations are needed first ----
+        uint2 v0[PIECES], v1[PIECES];
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int b = u0 * MF + 8 * i + (xp >> 2);
+            // without a branch, at a place that is there
+            const uint16_t *const p = x + 32 * (b < blocks ? b : 0);
+            v0[i] = *reinterpret_cast<const uint2 *>(p + run0<WT>(xp & 3));
+            v1[i] = *reinterpret_cast<const uint2 *>(p + run1<WT>(xp & 3));
+        }
+        __builtin_amdgcn_sched_barrier(0);
         const uint8_t *row = row_of(0);
         window.load(row, row_bytes, u0, g, false);
         __builtin_amdgcn_sched_barrier(0);
@@ -153,27 +170,22 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
             __builtin_amdgcn_sched_barrier(0);
         });
         if (u0 > 0) __syncthreads();                    // the last image is no longer read
-        const int per_row = len * MF * 4;               // pieces of eight values
-        for (int i = tid; i < tile.rows * per_row; i += kThreads) {
-            const int t = i / per_row, p = i - t * per_row, b = u0 * MF + (p >> 2), q = p & 3;
-            uint2 v0 = make_uint2(0, 0), v1 = v0;
-            const int token = token_of(a, tile.n0 + t);
-            if (token >= 0 && b < blocks) {
-                const uint16_t *x = a.x + (uint64_t)token * a.x_pitch + 32 * b;
-                v0 = *reinterpret_cast<const uint2 *>(x + run0<WT>(q));
-                v1 = *reinterpret_cast<const uint2 *>(x + run1<WT>(q));
+        if (xt < tile.rows) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                uint4 v;
+                if (WT == W_Q8_0) {
+                    v = make_uint4(v0[i].x, v0[i].y, v1[i].x, v1[i].y);
+                } else {                                // the two runs' values in turn
+                    v.x = __builtin_amdgcn_perm(v1[i].x, v0[i].x, 0x05040100u);
+                    v.y = __builtin_amdgcn_perm(v1[i].x, v0[i].x, 0x07060302u);
+                    v.z = __builtin_amdgcn_perm(v1[i].y, v0[i].y, 0x05040100u);
+                    v.w = __builtin_amdgcn_perm(v1[i].y, v0[i].y, 0x07060302u);
+                }
+                const int lb = 8 * i + (xp >> 2), q = xp & 3;       // block within the image, quarter
+                if (token < 0 || u0 * MF + lb >= blocks) v = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(lds + image_step<WT>(lb, q) * kBlockBytes + image_group<WT>(lb, q) * (kRows * 16) + xt * 16) = v;
             }
-            uint4 v;
-            if (WT == W_Q8_0) {
-                v = make_uint4(v0.x, v0.y, v1.x, v1.y);
-            } else {                                    // the two runs' values in turn
-                v.x = __builtin_amdgcn_perm(v1.x, v0.x, 0x05040100u);
-                v.y = __builtin_amdgcn_perm(v1.x, v0.x, 0x07060302u);
-                v.z = __builtin_amdgcn_perm(v1.y, v0.y, 0x05040100u);
-                v.w = __builtin_amdgcn_perm(v1.y, v0.y, 0x07060302u);
-            }
-            const int lb = p >> 2;                      // block within the image
-            *reinterpret_cast<uint4 *>(lds + image_step<WT>(lb, q) * kBlockBytes + image_group<WT>(lb, q) * (kRows * 16) + t * 16) = v;
         }
         __syncthreads();
         // ---- the units ----

@@ -151,6 +151,17 @@ def test_gemm_grouped_wild_offsets_and_orders():
             _check(y[r:r + 1], ref, bound, str(r))
 
 
+@pytest.mark.parametrize("R", [4, 200])
+def test_gemm_grouped_without_tokens(R):
+    """Rows picked from an x without rows are zeros."""
+    print(f"[case] grouped no tokens R {R}", flush=True)
+    w, _ = _experts(np.random.default_rng(6), "q4_0", 2, 20, 64)
+    y = Q.gemm_grouped(w, torch.empty((0, 64), dtype=torch.bfloat16, device=DEV),
+                       torch.tensor([0, R // 2, R], dtype=torch.int32, device=DEV),
+                       order=torch.arange(R, dtype=torch.int32, device=DEV))
+    assert y.shape == (R, 20) and (y == 0).all()
+
+
 def test_gemm_grouped_special_values_stay_in_their_row():
     print("[case] grouped special values", flush=True)
     rng = np.random.default_rng(4)
