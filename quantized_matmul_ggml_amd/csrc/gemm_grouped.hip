@@ -20,8 +20,8 @@
 //   KP = 4:  32 x 32, steps of 256
 // so that a step is 16 KB of activations and 128 x 64 weights in all three,
 // and a wave multiplies 32 weight rows by the tile's rows over 64 of K.  Steps
-// go from memory to LDS with direct-to-LDS loads, kStages - 1 ahead, one barrier
-// each; two workgroups share a CU, so that one's matrix instructions run
+// go from memory to LDS with direct-to-LDS loads one or two steps ahead, one barrier
+// each; two or three workgroups share a CU, so that one's matrix instructions run
 // beside the other's waits, unpacking and epilogue.
 #include "gemm_common.h"
 #include "grouped_tile.h"
@@ -31,7 +31,6 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStages = 3;
 constexpr int kTokBytes = 16 * 1024;       // of one stage
 constexpr int kScaleBytes = 1024;
 
@@ -54,9 +53,13 @@ struct GrpTile {
     static constexpr int LOADS = TOK_LOADS + CODE_LOADS + 1;   // per wave and step
     static constexpr int CODE_OFF = kTokBytes, SCALE_OFF = CODE_OFF + CODE_BYTES;
     static constexpr int STAGE = SCALE_OFF + kScaleBytes;
-    static constexpr int LDS_BYTES = kStages * STAGE;
+    // With two stages three workgroups share a CU, which the large tiles' products
+    // want (4096 tokens, gate and up of 5632 x 2048 Q4_0: 501 us, 543 with three
+    // stages and two workgroups); the small tiles' loads want the third.
+    static constexpr int STAGES = KP == 1 ? 2 : 3;
+    static constexpr int LDS_BYTES = STAGES * STAGE;
     static_assert(BN * BK * 2 == kTokBytes && CODE_BYTES == CODE_LOADS * 16 * kThreads, "whole loads");
-    static_assert(2 * LDS_BYTES <= 160 * 1024, "two workgroups per CU");
+    static_assert((KP == 1 ? 3 : 2) * LDS_BYTES <= 160 * 1024, "workgroups per CU");
     static_assert(KP == 1 || 4 * 64 * TT * 16 * 4 <= LDS_BYTES, "the waves' sums fit the ring");
 };
 
@@ -90,7 +93,7 @@ __device__ inline uint32_t unpack_pair(u32x2 c0, u32x2 c1, float scale)
 __device__ inline float grp_swish(float z) { return z / (1.0f + expf(-z)); }
 
 template <int WT, int SS, int KP, bool SW>
-__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs a)
+__global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel(const GrpArgs a)
 {
     using T = GrpTile<WT, KP>;
     constexpr int TT = T::TT, BN = T::BN, BK = T::BK;
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
         for (int r = 0; r < 16; ++r)
             if (r >= from && r < to) acc[j][r] = fmaf(sum[decltype(U)::value & 1][r], d, acc[j][r]);
     };
-    // step s from its stage, and the loads of step s + kStages - 1 into another
+    // step s from its stage, and the loads of step s + T::STAGES - 1 into another
     auto multiply = [&](auto FAST, const uint8_t *st, int s, int next) {
         u32x2 c0[2], c1[2];
         float d[2];
@@ -278,7 +281,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
             constexpr int per = (T::LOADS + MI - 1) / MI, gap = per > 1 ? 1 : MI / T::LOADS;
             static_for<per>([&](auto I) {
                 constexpr int l = k / gap * per + decltype(I)::value;
-                if constexpr (k % gap == 0 && l < T::LOADS) load(FAST, std::integral_constant<int, l>{}, s + kStages - 1, next);
+                if constexpr (k % gap == 0 && l < T::LOADS) load(FAST, std::integral_constant<int, l>{}, s + T::STAGES - 1, next);
             });
             __builtin_amdgcn_sched_barrier(0);
             // the second block's pairs, before the first instruction that takes them
@@ -298,20 +301,20 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_kernel(const GrpArgs
             if constexpr (UNITS == 1) add(std::integral_constant<int, 0>{}, 0, 16, pending);
         }
     };
-    for (int s = 0; s < kStages - 1; ++s)
+    for (int s = 0; s < T::STAGES - 1; ++s)
         static_for<T::LOADS>([&](auto L) { load(std::false_type{}, L, s, s); });
-    int stage = 0, next = kStages - 1;
+    int stage = 0, next = T::STAGES - 1;
     auto run_steps = [&](auto FAST, int s, int to) {
         for (; s < to; ++s) {
-            ll_wait<T::LOADS * (kStages - 2)>();         // this wave's loads of step s have landed
+            ll_wait<T::LOADS * (T::STAGES - 2)>();         // this wave's loads of step s have landed
             // every wave's have, and the stage of step s - 1 is free
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             multiply(FAST, lds + stage * T::STAGE, s, next);
             next = stage;
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+            stage = stage + 1 == T::STAGES ? 0 : stage + 1;
         }
     };
-    const int fast_to = full - (kStages - 1) > 0 ? full - (kStages - 1) : 0;
+    const int fast_to = full - (T::STAGES - 1) > 0 ? full - (T::STAGES - 1) : 0;
     run_steps(std::true_type{}, 0, fast_to);
     run_steps(std::false_type{}, fast_to, steps);
     if constexpr (SCALED && UNITS > 1) add(std::integral_constant<int, UNITS - 1>{}, 0, 16, pending);
@@ -414,8 +417,8 @@ hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const 
     a.R = (int32_t)y.R;
     a.bf16_out = y.bf16;
     const bool sw = up != nullptr;
-    if (grouped_streams(y.R, w.E)) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
-    const int kp = grouped_k_waves(y.R, w.E);
+    const int kp = grouped_form(a.M, w.w.K, y.R, w.E, w.w.type, sw, device_cus());
+    if (kp == 0) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
     if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, kp, sw, stream);
     if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, kp, sw, stream) : launch_type<W_Q4_0, 0>(a, kp, sw, stream);
     if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, kp, sw, stream) : launch_type<W_Q8_0, 0>(a, kp, sw, stream);

@@ -191,15 +191,29 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const CombineArgs a)
         const int64_t n = i / a.quads;
         const int64_t m = (i - n * a.quads) * 4;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int c = 0; c < a.k; ++c) {
-            const int32_t p = a.place[n * a.k + c];
-            if (p < 0) continue;
-            const float w = a.weights[n * a.k + c];
-            const float4 v = *reinterpret_cast<const float4 *>(a.d + (uint64_t)p * a.d_pitch + m);
-            s.x = fmaf(w, v.x, s.x);
-            s.y = fmaf(w, v.y, s.y);
-            s.z = fmaf(w, v.z, s.z);
-            s.w = fmaf(w, v.w, s.w);
+        // eight slots at a time, their loads in flight together (one after the other
+        // 64 tokens of eight slots took 5.2 us, so CCC)
+        for (int c0 = 0; c0 < a.k; c0 += 8) {
+            int32_t p[8];
+            float w[8];
+            float4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int64_t at = n * a.k + (c0 + c < a.k ? c0 + c : c0);
+                p[c] = c0 + c < a.k ? a.place[at] : -1;
+                w[c] = a.weights[at];
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (p[c] >= 0) v[c] = *reinterpret_cast<const float4 *>(a.d + (uint64_t)p[c] * a.d_pitch + m);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (p[c] < 0) continue;
+                s.x = fmaf(w[c], v[c].x, s.x);
+                s.y = fmaf(w[c], v[c].y, s.y);
+                s.z = fmaf(w[c], v[c].z, s.z);
+                s.w = fmaf(w[c], v[c].w, s.w);
+            }
         }
         const uint64_t o = (uint64_t)n * a.y_pitch + m;
         const float v[4] = {s.x, s.y, s.z, s.w};

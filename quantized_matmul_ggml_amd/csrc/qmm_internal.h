@@ -186,14 +186,6 @@ inline int64_t grouped_row_tiles(int64_t R, int64_t E, int bn)
     const int64_t used = E < R ? E : R;
     return (R + used * (bn - 1)) / bn;
 }
-// The form of a launch: whether it streams rows (gemm_rows.hip), for experts with
-// few rows; else the waves of a workgroup that split K (1, 2 or 4), which makes
-// its tile 128, 64 or 32 rows.
-inline bool grouped_streams(int64_t R, int64_t E) { return R <= 16 * E; }
-inline int grouped_k_waves(int64_t R, int64_t E)
-{
-    return R >= 96 * E ? 1 : R >= 40 * E ? 2 : 4;
-}
 // How the streaming form splits the weight rows: tiles of 16 (SwiGLU: 8) rows,
 // tiles_per_wave to each of a workgroup's eight waves.  A wave has `depth` units
 // in flight, which divide a tile's units as evenly as they can.
@@ -215,13 +207,48 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
     p.m_tiles = (tiles + 8 * p.tiles_per_wave - 1) / (8 * p.tiles_per_wave);
     return p;
 }
+// The form of a launch by its estimated time: 0, rows streamed (gemm_rows.hip); else
+// the waves of a workgroup that split K (1, 2 or 4), which makes its tile 128,
+// 64 or 32 rows.  Only R and E are known here, not the groups, so that each
+// group counts half a tile more than its share of R.
+//  * Tiles: two share a CU and take `both` us for 2048 of K, a CU's only one
+//    `one` us (Q4_0; 8 experts of 2048 x 2048 with 512 rows each: 128-row tiles
+//    64 us, 64-row ones 77, 32-row ones 126; with 128 rows each 36, 29 and 37; with
+//    64 rows each 34, 19 and 22).
+//  * Rows: what the unpacking takes of 16-row tiles' weights, 4.2 bytes a ns, and
+//    5 us before the first product (64 experts of 2048 x 1024 Q4_0 with 16 rows
+//    each: 30 us, 38 with 64-row tiles; with 24 rows each 39 with 64-row tiles, 53
+//    with 32-row ones).
+inline int grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+{
+    const double used = (double)(E < R ? E : R);
+    auto row_tiles = [&](int bn) {
+        const double t = (double)R / bn + used / 2;
+        return t < used ? used : t;
+    };
+    const double bytes = (double)M * (double)K * (type == W_Q8_0 ? 1.06 : 0.55) * (swiglu ? 2 : 1);
+    int best = 0;
+    double least = 5 + row_tiles(16) * bytes / 4.2e6;
+    static constexpr struct { int kp; double both, one; } forms[] = {{1, 41, 33}, {2, 16, 12}, {4, 7.6, 6.5}};
+    for (const auto &f : forms) {
+        const int64_t bm = (swiglu ? 64 : 128) / f.kp;
+        const double groups = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm), slots = 2.0 * (double)cus;
+        const double rounds = (double)(int64_t)(groups / slots < 1e9 ? groups / slots : 1e9), rest = groups - rounds * slots;
+        const double t = 3 + (double)K / 2048 * (rounds * f.both + (rest > slots / 2 ? f.both : rest > 0 ? f.one : 0));
+        if (t < least) {
+            least = t;
+            best = f.kp;
+        }
+    }
+    return best;
+}
 // Threads of the launch stay below 2^32 (kMaxGridThreads).
 inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
-    const bool rows = grouped_streams(R, E);
-    const int kp = grouped_k_waves(R, E), bm = (swiglu ? 64 : 128) / kp;
-    const int64_t m = rows ? plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles : (M + bm - 1) / bm;
-    const int64_t n = grouped_row_tiles(R, E, rows ? 16 : 128 / kp), most = (int64_t)(kMaxGridThreads / 512) - 1;
+    const int kp = grouped_form(M, K, R, E, type, swiglu, cus);
+    const int64_t bm = kp ? (swiglu ? 64 : 128) / kp : 0;
+    const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles;
+    const int64_t n = grouped_row_tiles(R, E, kp ? 128 / kp : 16), most = (int64_t)(kMaxGridThreads / 512) - 1;
     return m <= most && n <= most && m * n <= most;
 }
 hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const ActView &x, const int32_t *offsets,
