@@ -490,11 +490,11 @@ QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up
  * and pitch) and overlaps no other operand.
  * Products are exact, their sums and the product with s_a round in binary32; a
  * token's result depends on no other token.
- * workspace: qmm_lora_workspace_size bytes (fewer: QMM_ERR_SCRATCH), 16-byte
+ * workspace: qmm_lora_workspace_size bytes (0 for a few tokens; fewer: QMM_ERR_SCRATCH), 16-byte
  * aligned, scratch for this call alone until its kernels have run. */
 #define QMM_LORA_MAX_RANK 128
 #define QMM_LORA_MAX_TOKENS (1 << 24)
-QMM_API size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *x);
+QMM_API size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x);
 QMM_API int qmm_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x, const int32_t *ids, const float *scales,
                      const qmm_tensor *base_f32, qmm_tensor *y_f32, void *workspace, size_t workspace_bytes, void *stream);
 

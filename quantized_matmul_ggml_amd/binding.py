@@ -137,7 +137,7 @@ def lib() -> ctypes.CDLL:
         h.qmm_moe_gemm_workspace_size.restype = S
         h.qmm_moe_gemm_swiglu.argtypes = [P, P, P, P, V, V, I, P, V, S, V]
         h.qmm_moe_gemm_swiglu.restype = ctypes.c_int
-        h.qmm_lora_workspace_size.argtypes = [P, P]
+        h.qmm_lora_workspace_size.argtypes = [P, P, P]
         h.qmm_lora_workspace_size.restype = S
         h.qmm_lora.argtypes = [P, P, P, V, V, P, P, V, S, V]
         h.qmm_lora.restype = ctypes.c_int
@@ -730,9 +730,9 @@ def _adapters(t: torch.Tensor) -> bytes:
     return _PACK(BF16, 3, cols, rows, L, 1, 2, 2 * pitch, 2 * apart, 2 * apart * L, t.data_ptr())
 
 
-def lora_workspace_size(a: torch.Tensor, x: torch.Tensor) -> int:
-    """Bytes of workspace qmm_lora needs for these shapes."""
-    return int(lib().qmm_lora_workspace_size(_adapters(a), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)))
+def lora_workspace_size(a: torch.Tensor, b: torch.Tensor, x: torch.Tensor) -> int:
+    """Bytes of workspace qmm_lora needs for these shapes (0 for a few tokens)."""
+    return int(lib().qmm_lora_workspace_size(_adapters(a), _adapters(b), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)))
 
 
 def lora(a: torch.Tensor, b: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, *, scales: torch.Tensor | None = None,
@@ -745,7 +745,7 @@ def lora(a: torch.Tensor, b: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, *
     lora_workspace_size bytes, or None to allocate one (graph-capture safe)."""
     if _ints(ids, "ids").dim() != 1 or x.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError("ids must be (N)")
-    ad, xd = _adapters(a), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)
+    ad, bd, xd = _adapters(a), _adapters(b), _dense(x, BF16 if x.dtype == torch.bfloat16 else F32)
     tensors = [a, b, x, ids]
     if scales is not None:
         if scales.dtype != torch.float32 or scales.shape != (a.shape[0],) or not scales.is_contiguous():
@@ -755,14 +755,17 @@ def lora(a: torch.Tensor, b: torch.Tensor, x: torch.Tensor, ids: torch.Tensor, *
         tensors.append(base)
     if out is None:
         out = _output(stream, x.device, torch.float32, x.shape[0], b.shape[1])
-    if workspace is None:
-        workspace = _workspace(stream, x.device, int((_lib or lib()).qmm_lora_workspace_size(ad, xd)))
-    else:
+    if workspace is not None:
         _need_bytes(workspace, 0, "workspace")
-    dev = _need_gpu(*tensors, out, workspace)
-    _launch(dev, stream, "qmm_lora", ad, _adapters(b), xd, ids.data_ptr(), None if scales is None else scales.data_ptr(),
-            None if base is None else _dense(base, F32), _dense(out, F32), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    elif need := int((_lib or lib()).qmm_lora_workspace_size(ad, bd, xd)):
+        workspace = _workspace(stream, x.device, need)
+    ws, size = None, 0
+    if workspace is not None:
+        tensors.append(workspace)
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _need_gpu(*tensors, out)
+    _launch(dev, stream, "qmm_lora", ad, bd, xd, ids.data_ptr(), None if scales is None else scales.data_ptr(),
+            None if base is None else _dense(base, F32), _dense(out, F32), ws, size)
     return out
 
 

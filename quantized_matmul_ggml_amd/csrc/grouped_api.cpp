@@ -139,28 +139,33 @@ int check_adapters(const qmm_tensor *t)
 }
 
 // The shape rules of the adapters and x.
-int check_lora(const qmm_tensor *a, const qmm_tensor *x)
+int check_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x)
 {
-    if (!a || !x) return QMM_ERR_NULL;
+    if (!a || !b || !x) return QMM_ERR_NULL;
     int rc = check_adapters(a);
+    if (rc) return rc;
+    rc = check_adapters(b);
     if (rc) return rc;
     rc = check_tensor(x, x->type == QMM_TYPE_BF16 ? 16 : 4);
     if (rc) return rc;
     if (x->type != QMM_TYPE_F32 && x->type != QMM_TYPE_BF16) return QMM_ERR_TYPE;
     const int64_t K = a->ne[0], r = a->ne[1];
     if (x->ne[0] != K || K % 32 != 0 || r < 8 || r % 8 != 0 || r > QMM_LORA_MAX_RANK) return QMM_ERR_SHAPE;
-    if (K > kMaxDim || x->ne[1] > QMM_LORA_MAX_TOKENS) return QMM_ERR_UNSUPPORTED;
+    if (b->ne[0] != r || b->ne[2] != a->ne[2]) return QMM_ERR_SHAPE;
+    // 32 rows of x and 128 rows of A and B are reached with 32-bit offsets
+    if (x->ne[1] > QMM_LORA_MAX_TOKENS || pitch_elems(x) >= kMaxPitch || pitch_elems(a) >= kMaxPitch / 2 ||
+        pitch_elems(b) >= kMaxPitch / 2 || b->ne[1] >= (int64_t)kMaxPitch)
+        return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }
 
-// What either form of the first launch needs, so that it does not depend on
-// where x lies.
-uint64_t lora_workspace(int64_t N, int64_t K, int64_t r)
+// What the call needs wherever x lies.
+uint64_t lora_workspace(int64_t N, int64_t K, int64_t M, int64_t r)
 {
     uint64_t most = 0;
     for (const bool wide : {false, true}) {
-        const qmm::LoraPlan p = qmm::plan_lora(N, K, 1, r, wide, qmm::device_cus());
-        const uint64_t bytes = (uint64_t)p.chunks * (uint64_t)N * 16 * (uint64_t)p.rt * 4;
+        const qmm::LoraPlan p = qmm::plan_lora(N, K, M, r, wide, qmm::device_cus());
+        const uint64_t bytes = p.single ? 0 : (uint64_t)p.chunks * (uint64_t)N * 16 * (uint64_t)p.rt * 4;
         most = bytes > most ? bytes : most;
     }
     return most;
@@ -258,39 +263,35 @@ int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const 
     return status_of(e);
 }
 
-size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *x)
+size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x)
 {
-    if (check_lora(a, x) || x->ne[1] == 0) return 0;
-    return (size_t)lora_workspace(x->ne[1], a->ne[0], a->ne[1]);
+    if (check_lora(a, b, x) || x->ne[1] == 0 || b->ne[1] == 0) return 0;
+    return (size_t)lora_workspace(x->ne[1], a->ne[0], b->ne[1], a->ne[1]);
 }
 
 int qmm_lora(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x, const int32_t *ids, const float *scales,
              const qmm_tensor *base, qmm_tensor *y, void *workspace, size_t workspace_bytes, void *stream)
 {
-    int rc = check_lora(a, x);
-    if (rc) return rc;
-    rc = check_adapters(b);
+    int rc = check_lora(a, b, x);
     if (rc) return rc;
     rc = check_tensor(y, 4);
     if (rc) return rc;
     if (y->type != QMM_TYPE_F32) return QMM_ERR_TYPE;
     const int64_t K = a->ne[0], r = a->ne[1], L = a->ne[2], M = b->ne[1], N = x->ne[1];
-    if (b->ne[0] != r || b->ne[2] != L || y->ne[0] != M || y->ne[1] != N) return QMM_ERR_SHAPE;
+    if (y->ne[0] != M || y->ne[1] != N) return QMM_ERR_SHAPE;
     if (base) {
         rc = check_tensor(base, 4);
         if (rc) return rc;
         if (base->type != QMM_TYPE_F32) return QMM_ERR_TYPE;
         if (base->ne[0] != M || base->ne[1] != N) return QMM_ERR_SHAPE;
     }
-    // 32 rows of x, base and y and 128 rows of A and B are reached with 32-bit offsets
-    if (pitch_elems(x) >= kMaxPitch || pitch_elems(a) >= kMaxPitch / 2 || pitch_elems(b) >= kMaxPitch / 2) return QMM_ERR_UNSUPPORTED;
-    if (M > kMaxDim || pitch_elems(y) >= kMaxPitch || (base && pitch_elems(base) >= kMaxPitch)) return QMM_ERR_UNSUPPORTED;
+    if (pitch_elems(y) >= kMaxPitch || (base && pitch_elems(base) >= kMaxPitch)) return QMM_ERR_UNSUPPORTED;
     if (N == 0 || M == 0) return QMM_OK;
     const bool f32x = x->type == QMM_TYPE_F32;
     const qmm::LoraPlan p = qmm::plan_lora(N, K, M, r, qmm::lora_wide(x->data, pitch_elems(x), f32x), qmm::device_cus());
     const int64_t most = (int64_t)(qmm::kMaxGridThreads / 256) - 1;
     if (2 * p.blocks1 > most || p.blocks2 > most) return QMM_ERR_UNSUPPORTED;
-    const uint64_t need = lora_workspace(N, K, r);
+    const uint64_t need = lora_workspace(N, K, M, r);
     if (!ids || (need && !workspace)) return QMM_ERR_NULL;
     if (((uintptr_t)ids | (uintptr_t)scales) % 4 != 0 || (need && (uintptr_t)workspace % 16 != 0)) return QMM_ERR_LAYOUT;
     if (workspace_bytes < need) return QMM_ERR_SCRATCH;

@@ -10,7 +10,7 @@
 // second makes base + B_a (s_a u) for 32 tokens and tiles of 128 outputs.  In
 // both, each adapter's products are made for all tokens of the tile and kept for
 // its own, so no token's values meet another's; where there are few tiles,
-// workgroups share a tile's adapters.
+// workgroups share a tile's adapters.  One or a few tokens take one launch.
 //
 // Arithmetic: binary32 values (x when it is F32, and s_a u) enter the matrix
 // cores as three bf16 parts whose sum is exact (row_tiles.h), so every product
@@ -76,13 +76,63 @@ __device__ inline rt_bf16x8 load8(const uint16_t *p)
     return __builtin_bit_cast(rt_bf16x8, *reinterpret_cast<const uint4 *>(p));
 }
 
+// A wave's part k_from .. k_to - 1 of u for the sixteen tokens whose rows (elements
+// from x on) its lanes hold: token c, rank 16 t + c of the adapter at `rows`.
+template <bool F32X, int RT>
+__device__ inline void shrink_steps(const LoraArgs &a, uint64_t row, const uint16_t *rows, int k_from, int k_to, int c, int g,
+                                    rt_f32x4 (&acc)[RT])
+{
+    constexpr int PARTS = F32X ? 3 : 1, U = RT == 8 ? 2 : 4;
+    // S steps of 32 from k0 on: all loads, then all products
+    auto steps = [&](auto count, int k0) {
+        constexpr int S = decltype(count)::value;
+        rt_f32x4u v[S][F32X ? 2 : 1];
+        rt_bf16x8 w[S][RT];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const int k = k0 + 32 * i + 8 * g;
+            if constexpr (F32X) {
+                const float *p = static_cast<const float *>(a.x) + row + k;
+                v[i][0] = *reinterpret_cast<const rt_f32x4u *>(p);
+                v[i][1] = *reinterpret_cast<const rt_f32x4u *>(p + 4);
+            } else {
+                v[i][0] = __builtin_bit_cast(rt_f32x4, load8(static_cast<const uint16_t *>(a.x) + row + k));
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const int r = 16 * t + c < a.r ? 16 * t + c : a.r - 1;
+                w[i][t] = load8(rows + (uint64_t)r * a.a_pitch + k);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            uint4 xp[PARTS];
+            if constexpr (F32X) {
+                const float f[8] = {v[i][0][0], v[i][0][1], v[i][0][2], v[i][0][3], v[i][1][0], v[i][1][1], v[i][1][2], v[i][1][3]};
+                split_parts(f, xp);
+            } else {
+                xp[0] = __builtin_bit_cast(uint4, (rt_f32x4)v[i][0]);
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(rt_bf16x8, xp[p]), w[i][t], acc[t], 0, 0, 0);
+        }
+    };
+    int k0 = k_from;
+    for (; k0 + 32 * U <= k_to; k0 += 32 * U) steps(std::integral_constant<int, U>{}, k0);
+    for (; k0 < k_to; k0 += 32) steps(std::integral_constant<int, 1>{}, k0);
+}
+
 // The first launch for few tokens: a tile of 16, each wave a part of K, loads
 // straight to registers (they are few, and all in flight at once).  The waves'
 // sums lie in LDS in register order, [wave][rank tile][register][lane].
 template <bool F32X, int RT>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a)
 {
-    constexpr int PARTS = F32X ? 3 : 1, U = RT == 8 ? 2 : 4, REGS = RT * 4;
+    constexpr int REGS = RT * 4;
     extern __shared__ __attribute__((aligned(16))) float red[];
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -100,47 +150,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a)
     for_adapters(id, 0xFFFF, j, a.j1, [&](int ad, uint64_t mask) {
         const uint16_t *rows = a.a + (uint64_t)ad * a.a_adapter;
         rt_f32x4 acc[RT] = {};
-        // S steps of 32 from k0 on: all loads, then all products
-        auto steps = [&](auto count, int k0) {
-            constexpr int S = decltype(count)::value;
-            rt_f32x4u v[S][F32X ? 2 : 1];
-            rt_bf16x8 w[S][RT];
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const int k = k0 + 32 * i + 8 * g;
-                if constexpr (F32X) {
-                    const float *p = static_cast<const float *>(a.x) + row + k;
-                    v[i][0] = *reinterpret_cast<const rt_f32x4u *>(p);
-                    v[i][1] = *reinterpret_cast<const rt_f32x4u *>(p + 4);
-                } else {
-                    v[i][0] = __builtin_bit_cast(rt_f32x4, load8(static_cast<const uint16_t *>(a.x) + row + k));
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const int r = 16 * t + c < a.r ? 16 * t + c : a.r - 1;
-                    w[i][t] = load8(rows + (uint64_t)r * a.a_pitch + k);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                uint4 xp[PARTS];
-                if constexpr (F32X) {
-                    const float f[8] = {v[i][0][0], v[i][0][1], v[i][0][2], v[i][0][3], v[i][1][0], v[i][1][1], v[i][1][2], v[i][1][3]};
-                    split_parts(f, xp);
-                } else {
-                    xp[0] = __builtin_bit_cast(uint4, (rt_f32x4)v[i][0]);
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(rt_bf16x8, xp[p]), w[i][t], acc[t], 0, 0, 0);
-            }
-        };
-        int k0 = k_from;
-        for (; k0 + 32 * U <= k_to; k0 += 32 * U) steps(std::integral_constant<int, U>{}, k0);
-        for (; k0 < k_to; k0 += 32) steps(std::integral_constant<int, 1>{}, k0);
+        shrink_steps<F32X, RT>(a, row, rows, k_from, k_to, c, g, acc);
         if (again) __syncthreads();            // the last adapter's sums are no longer read
         again = true;
 #pragma unroll
@@ -431,6 +441,60 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a)
     ll_wait<0>();
 }
 
+// One launch for one or a few tokens: a workgroup per token and 512 outputs, which
+// makes all of the token's u for itself (its adapter's A then comes from the L2
+// for all workgroups but the first) and has its rows of B in flight meanwhile.
+// The outputs are one thread's sums over the ranks, exact products in binary32.
+template <bool F32X, int RT>
+__global__ __launch_bounds__(512) void lora_token_kernel(const LoraArgs a)
+{
+    __shared__ float part[kShrinkWaves][16 * RT];
+    __shared__ __attribute__((aligned(16))) float us[16 * RT];
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t n = blockIdx.y, m = (int64_t)blockIdx.x * 512 + tid;
+    const int ad = __builtin_amdgcn_readfirstlane(a.ids[n]);
+    const bool live = ad >= 0 && ad < a.L;
+    float out = a.base && m < a.M ? a.base[(uint64_t)n * a.base_pitch + m] : 0.0f;
+    if (live) {
+        const uint16_t *b = a.b + (uint64_t)ad * a.b_adapter + (uint64_t)(m < a.M ? m : a.M - 1) * a.b_pitch;
+        uint4 w[2 * RT];
+#pragma unroll
+        for (int q = 0; q < 2 * RT; ++q) w[q] = *reinterpret_cast<const uint4 *>(b + (8 * q < a.r ? 8 * q : 0));
+        const int per = (a.K / 32 + kShrinkWaves - 1) / kShrinkWaves * 32;
+        const int k_from = wave * per, k_to = k_from + per < a.K ? k_from + per : a.K;
+        rt_f32x4 acc[RT] = {};
+        shrink_steps<F32X, RT>(a, (uint64_t)n * a.x_pitch, a.a + (uint64_t)ad * a.a_adapter, k_from, k_to, c, g, acc);
+        // all sixteen tokens of D are this one
+        if (g == 0) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) part[wave][16 * t + c] = acc[t][0];
+        }
+        __syncthreads();
+        if (tid < 16 * RT) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kShrinkWaves; ++q) s += part[q][tid];
+            if (a.scales) s *= a.scales[ad];
+            us[tid] = s;
+        }
+        __syncthreads();
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 2 * RT; ++q) {
+            if (8 * q >= a.r) break;
+            const uint32_t d[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum = fmaf(__builtin_bit_cast(float, d[i] << 16), us[8 * q + 2 * i], sum);
+                sum = fmaf(__builtin_bit_cast(float, d[i] & 0xFFFF0000u), us[8 * q + 2 * i + 1], sum);
+            }
+        }
+        out += sum;
+    }
+    if (m < a.M) a.y[(uint64_t)n * a.y_pitch + m] = out;
+}
+
 template <bool F32X, int RT>
 hipError_t launch_shrink(const LoraArgs &a, const LoraPlan &p, hipStream_t stream)
 {
@@ -447,6 +511,12 @@ hipError_t launch_shrink(const LoraArgs &a, const LoraPlan &p, hipStream_t strea
 template <int RT>
 hipError_t launch_rank(const LoraArgs &a, const LoraPlan &p, bool f32x, hipStream_t stream)
 {
+    if (p.single) {
+        const dim3 grid((unsigned)((a.M + 511) / 512), (unsigned)a.N);
+        if (f32x) hipLaunchKernelGGL((lora_token_kernel<true, RT>), grid, dim3(512), 0, stream, a);
+        else hipLaunchKernelGGL((lora_token_kernel<false, RT>), grid, dim3(512), 0, stream, a);
+        return hipGetLastError();
+    }
     if (p.blocks1) {                   // without K every sum is empty
         const hipError_t e = f32x ? launch_shrink<true, RT>(a, p, stream) : launch_shrink<false, RT>(a, p, stream);
         if (e != hipSuccess) return e;

@@ -12,6 +12,7 @@ constexpr int kMostParts = 4;        // of K
 
 struct LoraPlan {
     int rt;              // 16-rank tiles: 1, 2, 4 or 8
+    bool single;         // one launch, which needs no workspace
     bool tiled;          // the first launch: tiles of 32 tokens through LDS (else of 16, through registers)
     int chunk, chunks;   // K per workgroup of the first launch (a multiple of 64), and its parts
     int j1, j2;          // workgroups (of each launch) that share a tile's adapters
@@ -30,6 +31,12 @@ inline LoraPlan plan_lora(int64_t N, int64_t K, int64_t M, int64_t r, bool wide,
 {
     LoraPlan p = {};
     p.rt = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8;
+    // Every workgroup of the one launch (a token and 512 outputs) reads all of its
+    // token's A: worth it while that is little (us in a graph, one launch against two;
+    // rank 16, 2048 x 2048: one token 5.2 / 7.8, 64 tokens 5.6 / 12.2, 128 tokens
+    // 8.4 / 12.7; 2048 x 5632: 64 tokens 11.4 / 13.9, 128 tokens 19.3 / 16.7; rank 16
+    // of 5632 for one token 9.6 / 8.3, rank 64 of 2048 12.2 / 11.0).
+    p.single = N <= 256 && r * K <= 1 << 16 && N * ((M + 511) / 512) * r * K <= 1 << 25;
     // Few tokens are decoded ones, which may all have different adapters:
     // workgroups share a tile's until there are `want` of them.  Prompts' tiles
     // have one, or two where one prompt ends: with one workgroup for both such a
