@@ -451,7 +451,9 @@ QMM_API int qmm_moe_group(const int32_t *ids, int64_t n_slots, int32_t n_experts
  * BF16 y, once) round.  Block scales must be finite.
  * Limits (else QMM_ERR_UNSUPPORTED): K, M <= 2^28, R and N < 2^31, weight pitches
  * below 2^24 bytes, N (or, without an order, 128) rows of x below 2^31 bytes, fewer
- * than 2^24 tiles. */
+ * than 2^23 tiles of 32 x 32 outputs or more (a whole group's rows at least 16).
+ * A block's sum is scaled after it is made: it must itself be finite, as it is with
+ * activations below 2^113 in magnitude. */
 QMM_API int qmm_gemm_grouped(const qmm_tensor *w, const qmm_tensor *x_bf16, const int32_t *offsets, const int32_t *order,
                              int32_t top_k, qmm_tensor *y, void *stream);
 
@@ -482,16 +484,18 @@ QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up
  *   y[n] = base[n] + s_a B_a (A_a x[n]),  a = ids[n].
  * a: BF16 ne = [K, r, L] (n_dims 3), b: BF16 ne = [r, M, L], each matrix and row
  * 16-byte aligned;  K % 32 = 0, r % 8 = 0, 8 <= r <= QMM_LORA_MAX_RANK (else
- * QMM_ERR_SHAPE);  x: F32 or BF16 (16-byte aligned rows) ne = [K, N], N <=
- * QMM_LORA_MAX_TOKENS, M and the pitches of x, base and y below 2^24 elements, those of a and b below 2^23;  ids: N values, read on the device: a token
- * whose id is negative or not below L has no adapter, its y is base;  scales: L
- * values s_a, or NULL for 1;  base: F32 ne = [M, N] (the shared projection's
- * output), or NULL for 0;  y: F32 ne = [M, N], which may be base itself (same data
- * and pitch) and overlaps no other operand.
+ * QMM_ERR_SHAPE);  x: F32 or BF16 (16-byte aligned rows) ne = [K, N];  ids: N
+ * values, read on the device: a token whose id is negative or not below L has no
+ * adapter, its y is base;  scales: L values s_a, or NULL for 1;  base: F32 ne =
+ * [M, N] (the shared projection's output), or NULL for 0;  y: F32 ne = [M, N], which
+ * may be base itself (same data and pitch) and overlaps no other operand.
+ * Limits (else QMM_ERR_UNSUPPORTED): N <= QMM_LORA_MAX_TOKENS, M and the pitches of
+ * x, base and y below 2^24 elements, those of a and b below 2^23.
  * Products are exact, their sums and the product with s_a round in binary32; a
  * token's result depends on no other token.
- * workspace: qmm_lora_workspace_size bytes (0 for a few tokens; fewer: QMM_ERR_SCRATCH), 16-byte
- * aligned, scratch for this call alone until its kernels have run. */
+ * workspace: qmm_lora_workspace_size bytes (0 for a few tokens; fewer:
+ * QMM_ERR_SCRATCH), 16-byte aligned, overlapping no operand; scratch for this call
+ * alone until its kernels have run. */
 #define QMM_LORA_MAX_RANK 128
 #define QMM_LORA_MAX_TOKENS (1 << 24)
 QMM_API size_t qmm_lora_workspace_size(const qmm_tensor *a, const qmm_tensor *b, const qmm_tensor *x);

@@ -42,27 +42,30 @@ struct GroupTile {
 // a workgroup for every tile of BN rows that R rows of E groups can need, in an
 // order (expert, weight tile, row tile) whose consecutive tiles share weights;
 // the eight XCDs (workgroup b runs on XCD b mod 8) take contiguous parts of the
-// tiles that there are.  Each lane counts the row tiles of a run of experts.
+// tiles that there are.  Each lane counts the row tiles of a run of experts, without
+// sign: descending offsets can make groups that overlap, whose tiles the count may
+// not hold; then too no tile lies outside the operands.
 template <int BN>
 __device__ inline bool find_tile(const GrpArgs &a, GroupTile &t)
 {
     const int lane = threadIdx.x & 63;
     const int run = (a.E + 63) / 64;
-    int mine = 0;
+    uint32_t counted = 0;
     for (int i = 0; i < run; ++i) {
         const int e = lane * run + i;
         if (e < a.E) {
             int first, end;
             group_rows(a.offsets, e, a.R, first, end);
-            mine += (end - first + BN - 1) / BN;
+            counted += (uint32_t)(end - first + BN - 1) / BN;
         }
     }
-    int upto = mine;
+    const int mine = (int)counted;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_up(upto, m);
-        upto += lane >= m ? o : 0;
+        const uint32_t o = __shfl_up(counted, m);
+        counted += lane >= m ? o : 0;
     }
+    const int upto = (int)counted;
     const int64_t total = (int64_t)__builtin_amdgcn_readlane(upto, 63) * a.m_tiles;
     if ((int64_t)blockIdx.x >= total) return false;
     const int nwg = (int)(total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x);
@@ -71,8 +74,10 @@ __device__ inline bool find_tile(const GrpArgs &a, GroupTile &t)
     const int row_tile = at / a.m_tiles;
     const int owner = __builtin_ctzll(__ballot(upto > row_tile));
     int before = __builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner);
+    if (before < 0 || before > row_tile) return false;
     int e = owner * run, first = 0, end = 0, tiles = 0;
     for (;; ++e) {
+        if (e >= a.E) return false;
         group_rows(a.offsets, e, a.R, first, end);
         tiles = (end - first + BN - 1) / BN;
         if (row_tile < before + tiles) break;
