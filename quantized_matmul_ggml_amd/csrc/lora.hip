@@ -44,7 +44,7 @@ struct LoraArgs {
     int32_t L, K, r, rp;
     int32_t chunk, chunks;             // K per part, parts
     int32_t j1, j2;                    // workgroups that share a tile's adapters
-    int32_t mt;                        // 128-output tiles per workgroup of the second launch
+    int32_t mt;                        // output tiles per workgroup: 128 (second launch), 512 (the one launch)
     int64_t m_blocks;                  // workgroups along M of the second launch
 };
 
@@ -441,10 +441,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a)
     ll_wait<0>();
 }
 
-// One launch for one or a few tokens: a workgroup per token and 512 outputs, which
-// makes all of the token's u for itself (its adapter's A then comes from the L2
-// for all workgroups but the first) and has its rows of B in flight meanwhile.
-// The outputs are one thread's sums over the ranks, exact products in binary32.
+// One launch for few tokens: a workgroup takes one token and mt tiles of 512
+// outputs.  It makes all of the token's u for itself (its adapter's A then comes
+// from the L2 for all workgroups but the first) and has its first rows of B in
+// flight meanwhile.  The outputs are one thread's sums over the ranks, exact
+// products in binary32.
 template <bool F32X, int RT>
 __global__ __launch_bounds__(512) void lora_token_kernel(const LoraArgs a)
 {
@@ -452,15 +453,22 @@ __global__ __launch_bounds__(512) void lora_token_kernel(const LoraArgs a)
     __shared__ __attribute__((aligned(16))) float us[16 * RT];
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n = blockIdx.y, m = (int64_t)blockIdx.x * 512 + tid;
+    const int64_t n = blockIdx.y, m_first = (int64_t)blockIdx.x * a.mt * 512 + tid;
+    const int tiles = a.M - (m_first - tid) > (int64_t)(a.mt - 1) * 512 ? a.mt : (int)((a.M - (m_first - tid) + 511) / 512);
     const int ad = __builtin_amdgcn_readfirstlane(a.ids[n]);
     const bool live = ad >= 0 && ad < a.L;
-    float out = a.base && m < a.M ? a.base[(uint64_t)n * a.base_pitch + m] : 0.0f;
-    if (live) {
-        const uint16_t *b = a.b + (uint64_t)ad * a.b_adapter + (uint64_t)(m < a.M ? m : a.M - 1) * a.b_pitch;
-        uint4 w[2 * RT];
+    const uint16_t *const b = a.b + (live ? (uint64_t)ad * a.b_adapter : 0);
+    uint4 w[2 * RT];
+    float out = 0.0f;
+    auto load = [&](int64_t m) {
+        const uint16_t *const p = b + (uint64_t)(m < a.M ? m : a.M - 1) * a.b_pitch;
+        if (live)
 #pragma unroll
-        for (int q = 0; q < 2 * RT; ++q) w[q] = *reinterpret_cast<const uint4 *>(b + (8 * q < a.r ? 8 * q : 0));
+            for (int q = 0; q < 2 * RT; ++q) w[q] = *reinterpret_cast<const uint4 *>(p + (8 * q < a.r ? 8 * q : 0));
+        out = a.base && m < a.M ? a.base[(uint64_t)n * a.base_pitch + m] : 0.0f;
+    };
+    load(m_first);
+    if (live) {
         const int per = (a.K / 32 + kShrinkWaves - 1) / kShrinkWaves * 32;
         const int k_from = wave * per, k_to = k_from + per < a.K ? k_from + per : a.K;
         rt_f32x4 acc[RT] = {};
@@ -479,20 +487,27 @@ __global__ __launch_bounds__(512) void lora_token_kernel(const LoraArgs a)
             us[tid] = s;
         }
         __syncthreads();
-        float sum = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 2 * RT; ++q) {
-            if (8 * q >= a.r) break;
-            const uint32_t d[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum = fmaf(__builtin_bit_cast(float, d[i] << 16), us[8 * q + 2 * i], sum);
-                sum = fmaf(__builtin_bit_cast(float, d[i] & 0xFFFF0000u), us[8 * q + 2 * i + 1], sum);
-            }
-        }
-        out += sum;
     }
-    if (m < a.M) a.y[(uint64_t)n * a.y_pitch + m] = out;
+    for (int i = 0; i < tiles; ++i) {
+        const int64_t m = m_first + 512 * i;
+        float y = out;
+        if (live) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 2 * RT; ++q) {
+                if (8 * q >= a.r) break;
+                const uint32_t d[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum = fmaf(__builtin_bit_cast(float, d[j] << 16), us[8 * q + 2 * j], sum);
+                    sum = fmaf(__builtin_bit_cast(float, d[j] & 0xFFFF0000u), us[8 * q + 2 * j + 1], sum);
+                }
+            }
+            y += sum;
+        }
+        if (i + 1 < tiles) load(m + 512);
+        if (m < a.M) a.y[(uint64_t)n * a.y_pitch + m] = y;
+    }
 }
 
 template <bool F32X, int RT>
@@ -512,7 +527,7 @@ template <int RT>
 hipError_t launch_rank(const LoraArgs &a, const LoraPlan &p, bool f32x, hipStream_t stream)
 {
     if (p.single) {
-        const dim3 grid((unsigned)((a.M + 511) / 512), (unsigned)a.N);
+        const dim3 grid((unsigned)((a.M + 512 * a.mt - 1) / (512 * a.mt)), (unsigned)a.N);
         if (f32x) hipLaunchKernelGGL((lora_token_kernel<true, RT>), grid, dim3(512), 0, stream, a);
         else hipLaunchKernelGGL((lora_token_kernel<false, RT>), grid, dim3(512), 0, stream, a);
         return hipGetLastError();

@@ -16,7 +16,7 @@ struct LoraPlan {
     bool tiled;          // the first launch: tiles of 32 tokens through LDS (else of 16, through registers)
     int chunk, chunks;   // K per workgroup of the first launch (a multiple of 64), and its parts
     int j1, j2;          // workgroups (of each launch) that share a tile's adapters
-    int mt;              // 128-output tiles per workgroup of the second launch: 1, 2, 4 or 8
+    int mt;              // output tiles per workgroup: of 128 in the second launch (1, 2, 4 or 8), of 512 in the one
     int64_t m_blocks;    // workgroups along the outputs of the second launch
     int64_t blocks1, blocks2;
 };
@@ -31,12 +31,28 @@ inline LoraPlan plan_lora(int64_t N, int64_t K, int64_t M, int64_t r, bool wide,
 {
     LoraPlan p = {};
     p.rt = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8;
-    // Every workgroup of the one launch (a token and 512 outputs) reads all of its
-    // token's A: worth it while that is little (us in a graph, one launch against two;
-    // rank 16, 2048 x 2048: one token 5.2 / 7.8, 64 tokens 5.6 / 12.2, 128 tokens
-    // 8.4 / 12.7; 2048 x 5632: 64 tokens 11.4 / 13.9, 128 tokens 19.3 / 16.7; rank 16
-    // of 5632 for one token 9.6 / 8.3, rank 64 of 2048 12.2 / 11.0).
-    p.single = N <= 256 && r * K <= 1 << 16 && N * ((M + 511) / 512) * r * K <= 1 << 25;
+    // The one launch: a workgroup per CU where the tokens allow it (64 tokens of rank
+    // 16, 2048 x 5632: 6.5 us, 11.6 with a workgroup for each 512 outputs, 14.0 with two
+    // launches).  Each token's workgroups read all of its A, so that its time goes
+    // with r K and the rounds of tokens; two launches read a matrix once for the
+    // tokens of a tile that share it, but go through a tile's adapters one after
+    // the other, and which tokens share one is not known here.  us in a graph, one
+    // launch, then two with 24 adapters in turn / with four prompts:
+    //   256 tokens, rank 16, 2048 x 2048    6.9   17.4 / 12.3
+    //   256 tokens, rank 64, 2048 x 2048   19.7   31.3 / 14.0
+    //   256 tokens, rank 64, 5632 x 4096   43.1   61.3 / 17.7
+    //  1024 tokens, rank 16, 2048 x 2048   18.3   80.1 / 13.8
+    //  1024 tokens, rank 64, 2048 x 2048   69.1  126.4 / 19.0
+    //    16 tokens, rank 64, 2048 x 2048   12.6   14.2
+    //     1 token,  rank 64, 2048 x 2048   12.3   11.0
+    //     1 token,  rank 16, 5632 x 2048    9.7    8.2
+    //     1 token,  rank 16, 2048 x 2048    5.3    7.9
+    p.single = N <= 4 * cus && r * K * ((N + cus - 1) / cus) <= (N < 16 ? 1 << 16 : 1 << 17);
+    if (p.single) {
+        const int64_t tiles = (M + 511) / 512, groups = N < cus ? cus / N : 1;
+        p.mt = (int)((tiles + groups - 1) / groups);
+        return p;
+    }
     // Few tokens are decoded ones, which may all have different adapters:
     // workgroups share a tile's until there are `want` of them.  Prompts' tiles
     // have one, or two where one prompt ends: with one workgroup for both such a

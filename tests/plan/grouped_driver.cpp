@@ -21,7 +21,10 @@ static const char *check(const LoraPlan &p, int64_t N, int64_t K, int64_t M, int
 {
     auto power = [](int64_t v, int64_t most) { return v >= 1 && v <= most && (v & (v - 1)) == 0; };
     if (!power(p.rt, 8) || 16 * p.rt < r || (p.rt > 1 && 8 * p.rt >= r)) return "rank tiles";
-    if (p.single) return N <= 256 ? nullptr : "tokens of one launch";
+    if (p.single) {
+        if (N > 65535) return "tokens of one launch";
+        return p.mt >= 1 && (int64_t)(p.mt - 1) * 512 < M ? nullptr : "outputs of one launch";
+    }
     if (p.tiled && !wide) return "tiles of unaligned rows";
     if (K == 0) {
         if (p.chunks != 0 || p.blocks1 != 0) return "parts of nothing";

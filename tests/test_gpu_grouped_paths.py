@@ -54,10 +54,11 @@ def test_streamed(shape):
 
 
 # tokens, adapters, rank, K, M, activations, aligned rows of x
-ADAPTERS = [(1, 1, 128, 512, 700, "f32", 1), (256, 9, 64, 64, 513, "bf16", 1), (1, 2, 128, 1056, 33, "bf16", 1), (2, 2, 40, 2080, 33, "f32", 1),
-            (3, 3, 16, 4128, 130, "f32", 0), (257, 300, 8, 32, 33, "bf16", 1), (600, 40, 24, 4128, 33, "f32", 0), (1500, 500, 16, 96, 33, "f32", 0),
-            (4100, 3, 8, 32, 1000, "f32", 0), (513, 4, 8, 32, 33, "bf16", 1), (513, 3, 128, 2080, 130, "f32", 1), (600, 100, 64, 4128, 65, "bf16", 1),
-            (4100, 5, 24, 4128, 130, "f32", 1), (4100, 2, 16, 64, 2050, "bf16", 1), (4100, 3, 8, 32, 4100, "f32", 1), (520, 2, 32, 1056, 300, "f32", 1)]
+ADAPTERS = [(1, 1, 128, 512, 700, "f32", 1), (256, 9, 64, 64, 513, "bf16", 1), (3, 2, 8, 32, 1100, "bf16", 1), (70, 9, 32, 96, 2100, "f32", 0),
+            (1000, 300, 16, 256, 1300, "f32", 0), (1, 2, 128, 1056, 33, "bf16", 1), (2, 2, 40, 2080, 33, "f32", 1), (3, 3, 16, 4128, 130, "f32", 0),
+            (17, 20, 128, 1056, 33, "bf16", 1), (513, 4, 16, 4128, 33, "f32", 0), (600, 40, 24, 4128, 33, "f32", 0), (1500, 500, 16, 96, 33, "f32", 0),
+            (4100, 3, 8, 32, 1000, "f32", 0), (513, 4, 16, 4128, 33, "bf16", 1), (513, 3, 128, 2080, 130, "f32", 1), (600, 100, 64, 4128, 65, "bf16", 1),
+            (4100, 5, 24, 4128, 130, "f32", 1), (4100, 2, 16, 64, 2050, "bf16", 1), (4100, 3, 8, 32, 4100, "f32", 1), (1100, 2, 32, 1056, 300, "f32", 1)]
 
 
 @pytest.mark.parametrize("runs", [False, True], ids=["mixed", "prompts"])
@@ -87,19 +88,19 @@ BUSY = 40_000_000           # clock cycles, some 20 ms
 
 def _calls(rng):
     """Calls with their own operands: one of each kind and form of workspace."""
-    E, k, K, F, N, L, r = 12, 3, 256, 96, 150, 6, 16
+    E, k, K, F, N, L, r = 12, 3, 256, 96, 150, 6, 128
     (g, u, d), _ = _layer(rng, "q4_0", E, K, F, K)
     x, _ = _x(rng, N, K)
     ids, w = _dev(rng.integers(-1, E, (N, k)).astype(np.int32)), torch.rand((N, k), device=DEV)
     many = _dev(rng.integers(-1, E, 70000).astype(np.int32))
     offsets, order, _ = Q.moe_group(ids, E)
-    a, _, b, _, xf, _, aid, s, base = _case(rng, 700, L, r, K, 300, "f32")
+    a, _, b, _, xf, _, aid, s, base = _case(rng, 1100, L, r, 1056, 300, "f32")
     aid, s, base = _dev(aid), _dev(s), _dev(base)
     return {"group": lambda **q: Q.moe_group(many, E, **q)[0],
             "products": lambda **q: Q.gemm_grouped_swiglu(g, u, x, offsets, order=order, top_k=k, out=torch.zeros((N * k, F), device=DEV), **q),
             "layer": lambda **q: Q.moe_gemm_swiglu(g, u, d, x, ids, w, **q),
-            "one launch": lambda **q: Q.lora(a, b, xf[:5], aid[:5], scales=s, base=base[:5], **q),
-            "few": lambda **q: Q.lora(a, b, xf[:300], aid[:300], scales=s, base=base[:300], **q),
+            "one launch": lambda **q: Q.lora(a[:, :16, :256], b[:, :, :16], xf[:300, :256], aid[:300], scales=s, base=base[:300], **q),
+            "few": lambda **q: Q.lora(a, b, xf[:30], aid[:30], scales=s, base=base[:30], **q),
             "prompt": lambda **q: Q.lora(a, b, xf, aid, scales=s, base=base, **q)}
 
 
@@ -165,7 +166,7 @@ def test_given_workspaces():
     (g, u, d), _ = _layer(rng, "mxfp4", E, K, F, 40)
     x, _ = _x(rng, N, K)
     ids, w = _dev(rng.integers(-1, E, (N, k)).astype(np.int32)), torch.rand((N, k), device=DEV)
-    a, _, b, _, xf, _, aid, s, base = _case(rng, 600, 5, 24, 64, 70, "bf16")
+    a, _, b, _, xf, _, aid, s, base = _case(rng, 1030, 5, 24, 64, 70, "bf16")
     many = _dev(rng.integers(0, E, 66000).astype(np.int32))
     for name, need, call in (("layer", Q.moe_gemm_workspace_size(g, d, x, k), lambda ws: Q.moe_gemm_swiglu(g, u, d, x, ids, w, workspace=ws)),
                              ("lora", Q.lora_workspace_size(a, b, xf), lambda ws: Q.lora(a, b, xf, _dev(aid), scales=_dev(s), workspace=ws)),

@@ -196,7 +196,7 @@ def test_layer_rejects(qmm_lib):
 
 @no_gpu
 def test_lora_rejects(qmm_lib):
-    K, M, r, L, N = 256, 70, 16, 5, 600
+    K, M, r, L, N = 256, 70, 16, 5, 1100
     h = qmm_lib.lib()
 
     def call(a=None, b=None, x=None, base=None, y=None, ids=IDS, scales=WTS, ws=WS, size=1 << 24):

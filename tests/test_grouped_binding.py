@@ -130,13 +130,13 @@ def test_allocations_belong_to_the_stream(monkeypatch, qmm_lib):
     o, g, d = _ops(), _experts(K, F), _experts(F, M)
     ids, p = torch.zeros((N, k), dtype=I32), torch.zeros((N, k))
     a, b = torch.zeros((4, 16, K), dtype=BF16), torch.zeros((4, M, 16), dtype=BF16)
-    many, x, few = torch.zeros(66000, dtype=I32), torch.zeros((600, K)), torch.zeros((2, K))
+    many, x, few = torch.zeros(66000, dtype=I32), torch.zeros((1100, K)), torch.zeros((2, K))
     calls = {
         "group": (3, lambda s: Q.moe_group(ids, E, stream=s)), "group of many": (4, lambda s: Q.moe_group(many, E, stream=s)),
         "grouped": (1, lambda s: Q.gemm_grouped(o["w"], o["x"], o["offsets"], stream=s)),
         "swiglu": (1, lambda s: Q.gemm_grouped_swiglu(g, g, o["x"], o["offsets"], order=o["order"], top_k=k, stream=s)),
         "layer": (2, lambda s: Q.moe_gemm_swiglu(g, g, d, o["x"], ids, p, stream=s)),
-        "adapters": (2, lambda s: Q.lora(a, b, x, many[:600], stream=s)),
+        "adapters": (2, lambda s: Q.lora(a, b, x, many[:1100], stream=s)),
         "adapters of few": (1, lambda s: Q.lora(a, b, few, many[:2], stream=s)),
     }
     for name, (made, call) in calls.items():

@@ -73,6 +73,9 @@ def test_gpu_adapters_take_every_form(plan):
     plans = plan([f"lora 256 {N} {K} {M} {r} {wide}" for N, L, r, K, M, kind, wide in P.ADAPTERS])
     forms = {(p["single"], p["tiled"] if p["single"] == "0" else "-") for p in plans}
     assert forms == {("1", "-"), ("0", "0"), ("0", "1")}
+    one = [(p, s) for p, s in zip(plans, P.ADAPTERS) if p["single"] == "1"]
+    assert {s[2] for _, s in one} >= {8, 16, 32, 64, 128} and {s[5] for _, s in one} == {"f32", "bf16"}
+    assert {p["mt"] for p, _ in one} >= {"1", "2", "3"} and max(s[0] for _, s in one) > 256
     two = [(p, s[5]) for p, s in zip(plans, P.ADAPTERS) if p["single"] == "0"]
     for tiled in "01":
         these = [(p, kind) for p, kind in two if p["tiled"] == tiled]
