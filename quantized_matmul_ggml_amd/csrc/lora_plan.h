@@ -75,7 +75,11 @@ inline LoraPlan plan_lora(int64_t N, int64_t K, int64_t M, int64_t r, bool wide,
     p.blocks1 = tiles1 * p.chunks * p.j1;
     const int64_t tiles2 = (N + 31) / 32, m_tiles = (M + 127) / 128;
     p.mt = 1;
-    while (p.mt < 8 && tiles2 * ((m_tiles + 2 * p.mt - 1) / (2 * p.mt)) >= 2 * cus) p.mt *= 2;
+    // As many as leave a workgroup with work per CU: each first joins the parts of
+    // u, which takes longer for high ranks (both launches, us in a graph, with 1, 2, 4
+    // and 8 tiles each: 1021 tokens, rank 128, 2048 outputs 25.4, 21.4, 22.6, 29.3;
+    // 4093 tokens, rank 128 61.4, 45.8, 38.7, 35.2, rank 16 26.4, 23.0, 21.9, 24.6).
+    while (p.mt < (p.rt < 4 ? 4 : 8) && tiles2 * ((m_tiles + 2 * p.mt - 1) / (2 * p.mt)) >= cus) p.mt *= 2;
     p.m_blocks = (m_tiles + p.mt - 1) / p.mt;
     p.j2 = p.tiled ? 2 : share(tiles2 * p.m_blocks, 2 * cus, N < 32 ? N : 32);
     p.blocks2 = tiles2 * p.m_blocks * p.j2;

@@ -58,7 +58,7 @@ ADAPTERS = [(1, 1, 128, 512, 700, "f32", 1), (256, 9, 64, 64, 513, "bf16", 1), (
             (1000, 300, 16, 256, 1300, "f32", 0), (1, 2, 128, 1056, 33, "bf16", 1), (2, 2, 40, 2080, 33, "f32", 1), (3, 3, 16, 4128, 130, "f32", 0),
             (17, 20, 128, 1056, 33, "bf16", 1), (513, 4, 16, 4128, 33, "f32", 0), (600, 40, 24, 4128, 33, "f32", 0), (1500, 500, 16, 96, 33, "f32", 0),
             (4100, 3, 8, 32, 1000, "f32", 0), (513, 4, 16, 4128, 33, "bf16", 1), (513, 3, 128, 2080, 130, "f32", 1), (600, 100, 64, 4128, 65, "bf16", 1),
-            (4100, 5, 24, 4128, 130, "f32", 1), (4100, 2, 16, 64, 2050, "bf16", 1), (4100, 3, 8, 32, 4100, "f32", 1), (1100, 2, 32, 1056, 300, "f32", 1)]
+            (4100, 5, 24, 4128, 130, "f32", 1), (4100, 2, 16, 64, 2050, "bf16", 1), (4100, 3, 40, 32, 4100, "f32", 1), (1100, 2, 32, 1056, 2000, "f32", 1)]
 
 
 @pytest.mark.parametrize("runs", [False, True], ids=["mixed", "prompts"])
