@@ -210,31 +210,35 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
 // The form of a launch by its estimated time: 0, rows streamed (gemm_rows.hip); else
 // the waves of a workgroup that split K (1, 2 or 4), which makes its tile 128,
 // 64 or 32 rows.  Only R and E are known here, not the groups, so that each
-// group counts half a tile more than its share of R.
-//  * Tiles: two share a CU and take `both` us for 2048 of K, a CU's only one
-//    `one` us (Q4_0; 8 experts of 2048 x 2048 with 512 rows each: 128-row tiles
-//    64 us, 64-row ones 77, 32-row ones 126; with 128 rows each 36, 29 and 37; with
-//    64 rows each 34, 19 and 22).
-//  * Rows: what the unpacking takes of 16-row tiles' weights, 4.2 bytes a ns, and
-//    5 us before the first product (64 experts of 2048 x 1024 Q4_0 with 16 rows
-//    each: 30 us, 38 with 64-row tiles; with 24 rows each 39 with 64-row tiles, 53
-//    with 32-row ones).
+// group counts half a tile more than its share of R, and a tenth of the groups one
+// tile more than the others.
+//  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
+//    workgroups overlap, a CU's only one 1.4 times that.
+//  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
+//    bytes a ns, and before it `lone` us for 2048 of K, the way through a row.
+// 150 launches over types, K, M, experts and even and uneven groups, each timed in
+// all four forms: the one taken here is 1.5 % slower than the best on average and 30 %
+// at most (sixteen experts with eight rows on average, 1 to 17 in fact).  In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
+// Q4_0, 256 rows 71 / 63 / 52 / 64, 1024 rows 206 / 175 / 105 / 93, 4096 rows 758 /
+// 638 / 354 / 271; the same MXFP4, 512 uneven rows 77 / 89 / 58 / 80.
 inline int grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
-    const double used = (double)(E < R ? E : R);
+    const double used = (double)(E < R ? E : R), k1024 = (double)K / 1024;
     auto row_tiles = [&](int bn) {
         const double t = (double)R / bn + used / 2;
-        return t < used ? used : t;
+        return t < 1.1 * used ? 1.1 * used : t;
     };
+    const double rate = type == W_Q4_0 ? 4.3 : 6.5, unpack = type == W_MXFP4 ? 0.85 : type == W_Q4_0 ? 1.0 : 1.07;
+    const double lone = type == W_MXFP4 ? 4.2 : 7;
     const double bytes = (double)M * (double)K * (type == W_Q8_0 ? 1.06 : 0.55) * (swiglu ? 2 : 1);
     int best = 0;
-    double least = 5 + row_tiles(16) * bytes / 4.2e6;
-    static constexpr struct { int kp; double both, one; } forms[] = {{1, 41, 33}, {2, 16, 12}, {4, 7.6, 6.5}};
+    double least = 4 + lone * (double)K / 2048 + row_tiles(16) * bytes / (1e6 * rate);
+    static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.6, 9.2}, {2, 1.6, 3.0}, {4, 1.35, 1.1}};
     for (const auto &f : forms) {
         const int64_t bm = (swiglu ? 64 : 128) / f.kp;
-        const double groups = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm), slots = 2.0 * (double)cus;
-        const double rounds = (double)(int64_t)(groups / slots < 1e9 ? groups / slots : 1e9), rest = groups - rounds * slots;
-        const double t = 3 + (double)K / 2048 * (rounds * f.both + (rest > slots / 2 ? f.both : rest > 0 ? f.one : 0));
+        const double share = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm) / (double)cus;
+        const double rounds = share <= 1 ? 1.4 : share < 1e9 ? (double)((int64_t)share + ((double)(int64_t)share < share)) : share;
+        const double t = 3 + unpack * (f.fixed + f.k1024 * k1024) * rounds;
         if (t < least) {
             least = t;
             best = f.kp;

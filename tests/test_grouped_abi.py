@@ -132,8 +132,7 @@ def test_grouped_rejects(qmm_lib, pair):
     wide = (1 << 28) + 32
     assert call(w=_ex(wide, 1, 1, W), up=_ex(wide, 1, 1, U), x=_dense(B.BF16, wide, 1, X), y=_dense(B.F32, 1, 1, Y), order=0) == B.ERR_UNSUPPORTED
     tall = dict(w=_ex(32, 1 << 28, 1, W), up=_ex(32, 1 << 28, 1, U))
-    # tiles of 128 (pair: 64) weight rows x 128 rows, fewer than 2^23
-    for n, status in ((128 if pair else 384, B.ERR_DEVICE), (256 if pair else 512, B.ERR_UNSUPPORTED), (1 << 16, B.ERR_UNSUPPORTED)):
+    for n, status in ((64, B.ERR_DEVICE), (1024, B.ERR_UNSUPPORTED), (1 << 16, B.ERR_UNSUPPORTED)):       # 2^23 tiles of 128 x 128
         assert call(**tall, x=_dense(B.BF16, 32, n, X), y=_dense(B.F32, 1 << 28, n, Y + (1 << 48)), order=0) == status, n
     # nothing to do, and what is left to the GPU
     assert call(y=_dense(B.F32, M, 0, 0), off=0, order=0, x=_dense(B.BF16, K, 0, 0)) == B.OK
