@@ -216,7 +216,7 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
 //    workgroups overlap, a CU's only one 1.4 times that.
 //  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
 //    bytes a ns, and before it `lone` us for 2048 of K, the way through a row.
-// 150 launches over types, K, M, experts and even and uneven groups, each timed in
+// 164 launches over types, K, M, experts and even and uneven groups, each timed in
 // all four forms: the one taken here is 1.5 % slower than the best on average and 30 %
 // at most (sixteen experts with eight rows on average, 1 to 17 in fact).  In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
 // Q4_0, 256 rows 71 / 63 / 52 / 64, 1024 rows 206 / 175 / 105 / 93, 4096 rows 758 /
