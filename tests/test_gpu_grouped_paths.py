@@ -177,3 +177,60 @@ def test_given_workspaces():
         assert (ws[need:] == 0xA5).all(), name
         with pytest.raises(Q.QmmError):
             call(ws[:need - 16])
+
+
+# ------------------------------------------------------ beyond 32-bit offsets
+
+def _rows_of(w, W_of, x, y, rows, expert_of, what):
+    """Rows of y against float64 products of a few experts, dequantized one at a time."""
+    for r in rows:
+        ref, bound = G.product(W_of(expert_of(r)), x[r:r + 1].double().cpu().numpy())
+        _check(y[r:r + 1], ref, bound, f"{what} row {r}")
+
+
+@pytest.mark.parametrize("K,M,R", [(8192, 40, 270001), (64, 8200, 140001)], ids=["x", "y"])
+def test_more_than_four_gigabytes_of_rows(K, M, R):
+    print(f"[case] large rows K {K} M {M} R {R}", flush=True)
+    rng = np.random.default_rng(K)
+    w, W = _experts(rng, "q8_0", 2, M, K)
+    x = torch.randn((R, K), device=DEV, dtype=torch.bfloat16)
+    cut = R - 77
+    y = Q.gemm_grouped(w, x, torch.tensor([0, cut, R], dtype=torch.int32, device=DEV))
+    _rows_of(w, lambda e: W[e], x, y, [0, 1, R // 2, cut - 1, cut, R - 1], lambda r: int(r >= cut), "large")
+    if K == 64:                                            # picked rows read x from its start
+        order = torch.arange(R - 1, -1, -1, dtype=torch.int32, device=DEV)
+        z = Q.gemm_grouped(w, x, torch.tensor([0, R, R], dtype=torch.int32, device=DEV), order=order)
+        for r in (0, R // 2, R - 1):
+            ref, bound = G.product(W[0], x[R - 1 - r:R - r].double().cpu().numpy())
+            _check(z[r:r + 1], ref, bound, f"picked row {r}")
+
+
+@pytest.mark.parametrize("rows", [1, 40], ids=["streamed", "tiles"])
+def test_more_than_four_gigabytes_of_experts(rows):
+    E, M, K = 1024, 1040, 8192
+    print(f"[case] large experts rows {rows}", flush=True)
+    data = torch.randint(0, 256, (E, M, Q.row_size(Q.MXFP4, K)), dtype=torch.uint8, device=DEV)
+    data[:, :, :K // 32] = torch.randint(118, 124, (E, M, K // 32), dtype=torch.uint8, device=DEV)
+    assert data.numel() > 1 << 32
+    w = Q.Experts(data, Q.MXFP4, K, M)
+    counts = torch.full((E,), rows, dtype=torch.int32, device=DEV)
+    counts[::3] = 0
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int32, device=DEV), counts.cumsum(0).int()])
+    n = int(offsets[-1])
+    x = torch.randn((n, K), device=DEV, dtype=torch.bfloat16)
+    y = Q.gemm_grouped(w, x, offsets)
+    owner = torch.repeat_interleave(torch.arange(E, device=DEV), counts.long()).cpu().numpy()
+    _rows_of(w, lambda e: R.values(data[e].cpu().numpy(), "mxfp4", K), x, y, [0, n // 2, n - 1], lambda r: int(owner[r]), "experts")
+
+
+def test_more_than_four_gigabytes_of_outputs_of_adapters():
+    N, M, K, r, L = 140001, 8200, 32, 16, 3
+    print("[case] large adapters", flush=True)
+    rng = np.random.default_rng(31)
+    a, A, b, Bm, x, X, ids, s, _ = _case(rng, N, L, r, K, 4, "bf16")
+    b = torch.randn((L, M, r), device=DEV).bfloat16()
+    base = torch.full((N, M), 0.5, device=DEV)
+    y = Q.lora(a, b, x, _dev(ids), scales=_dev(s), base=base, out=base)
+    for n in (0, N // 2, N - 2, N - 1):
+        ref, bound = G.lora(A, b.double().cpu().numpy(), X[n:n + 1], ids[n:n + 1], s, np.full((1, M), 0.5, np.float32))
+        _check(y[n:n + 1], ref, bound, f"token {n}")
