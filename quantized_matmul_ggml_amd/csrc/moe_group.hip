@@ -9,13 +9,14 @@
 // the lanes before.  A scan over (expert, wave) turns the counts into places, and
 // no place depends on which wave is faster.
 //
-// One launch, of a workgroup up to kGroupWhole slots and of one for 2048 slots up
+// One launch, of a workgroup up to kGroupWhole slots and of one for 1024 slots up
 // to kGroupAll; each of those counts all the others' slots too, with LDS
 // additions spread over eight counters per expert, which costs less than the
 // second launch, the workspace and the wait between (32744 slots over 128 experts
-// through the binding: 10.2 us, 14.5 with two launches).  More slots go to 64
-// workgroups which count in a first launch and add up the workgroups before them
-// in a second one.  Bound by launches and a few dependent passes over LDS.
+// through the binding: 9.4 us, 14.5 with two launches; the kernel 9.6, and 10.6 with
+// workgroups of 2048 slots, of which 4 are the count of the others' slots).  More
+// slots go to 64 workgroups which count in a first launch and add up the workgroups
+// before them in a second one.  Bound by launches and a few dependent passes over LDS.
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -265,10 +266,10 @@ hipError_t launch_moe_group(const int32_t *ids, int64_t S, int64_t E, int32_t *o
     while (E >> a.bits) ++a.bits;
     constexpr int64_t few = 2 * kThreads, many = 8 * kThreads;
     if (S <= kGroupAll) {
-        a.chunk = S <= few || S > kGroupWhole ? few : many;
+        a.chunk = S <= few ? few : S <= kGroupWhole ? many : kThreads;
         if (S <= few) return launch_step<kWhole, 2, true>(a, 1, stream);
         if (S <= kGroupWhole) return launch_step<kWhole, 8, true>(a, 1, stream);
-        return launch_step<kAll, 2, true>(a, (unsigned)((S + few - 1) / few), stream);
+        return launch_step<kAll, 1, true>(a, (unsigned)((S + kThreads - 1) / kThreads), stream);
     }
     const int64_t per = (S + kGroupChunks - 1) / kGroupChunks;
     a.chunk = (int32_t)((per + many - 1) / many * many);
