@@ -286,7 +286,11 @@ __global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel
             else if constexpr (k % PU == 0) sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, f32x16{}, 0, 0, 0);
             else sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, sum[u & 1], 0, 0, 0);
             if constexpr (k + AHEAD < MI) x[k % AHEAD] = frag(std::integral_constant<int, k + AHEAD>{});
-            constexpr int per = (T::LOADS + MI - 1) / MI, gap = per > 1 ? 1 : MI / T::LOADS;
+            // one load behind each of the first instructions where only one stage is
+            // ahead, else spread over the step (4096 rows, MXFP4 pair of 5632 x 2048 with
+            // large tiles: 230 us, spread 238; 1024 rows, Q4_0 2048 x 2048 with small
+            // ones: 29.8 and 29.3)
+            constexpr int per = (T::LOADS + MI - 1) / MI, gap = per > 1 || T::STAGES == 2 ? 1 : MI / T::LOADS;
             static_for<per>([&](auto I) {
                 constexpr int l = k / gap * per + decltype(I)::value;
                 if constexpr (k % gap == 0 && l < T::LOADS) load(FAST, std::integral_constant<int, l>{}, s + T::STAGES - 1, next);
