@@ -46,7 +46,7 @@ template <> struct GrpFmt<W_Q4_0> { static constexpr int QB = 16; };
 template <> struct GrpFmt<W_MXFP4> { static constexpr int QB = 16; };
 template <> struct GrpFmt<W_Q8_0> { static constexpr int QB = 32; };
 
-template <int WT, int KP>
+template <int WT, int KP, int NST>
 struct GrpTile {
     static constexpr int QB = GrpFmt<WT>::QB;      // code bytes of a 32-block
     static constexpr int RG = 4 / KP;              // waves along the weight rows
@@ -60,11 +60,13 @@ struct GrpTile {
     static constexpr int LOADS = TOK_LOADS + CODE_LOADS + 1;   // per wave and step
     static constexpr int CODE_OFF = kTokBytes, SCALE_OFF = CODE_OFF + CODE_BYTES;
     static constexpr int STAGE = SCALE_OFF + kScaleBytes;
-    // With two stages three workgroups share a CU, which the large tiles' products
-    // want (4096 tokens, gate and up of 5632 x 2048 Q4_0: 501 us, 543 with three
-    // stages and two workgroups; their down product 268 and 249); the small tiles'
-    // loads want the third.
-    static constexpr int STAGES = KP == 1 ? 2 : 3;
+    // With two stages three workgroups share a CU, with three two.  Where there are
+    // enough tiles the workgroup is worth more than the stage (gate and up of 4096 rows,
+    // 5632 x 2048 Q4_0, two and three stages: 64-row tiles 349 and 376 us, 32-row ones
+    // 565 and 670; 7372 rows, 128-row tiles 501 and 543); up to two tiles a CU the
+    // stage is (486 rows, pair of 321 x 3584 Q4_0 17.4 and 15.6, 137 rows, layer of
+    // three Q8_0 experts 2176 -> 3648 48.9 and 45.4).
+    static constexpr int STAGES = NST;
     static constexpr int LDS_BYTES = STAGES * STAGE;
     static_assert(BN * BK * 2 == kTokBytes && CODE_BYTES == CODE_LOADS * 16 * kThreads, "whole loads");
     static_assert((KP == 1 ? 3 : 2) * LDS_BYTES <= 160 * 1024, "workgroups per CU");
@@ -100,10 +102,10 @@ __device__ inline uint32_t unpack_pair(u32x2 c0, u32x2 c1, float scale)
 
 __device__ inline float grp_swish(float z) { return z / (1.0f + expf(-z)); }
 
-template <int WT, int SS, int KP, bool SW>
-__global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel(const GrpArgs a)
+template <int WT, int SS, int KP, bool SW, int NST>
+__global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kernel(const GrpArgs a)
 {
-    using T = GrpTile<WT, KP>;
+    using T = GrpTile<WT, KP, NST>;
     constexpr int TT = T::TT, BN = T::BN, BK = T::BK;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel
     // scale): its matrix instructions start from zero and their sums are scaled
     // and added while the next unit's run.  Each matrix instruction is followed
     // by its share of that, of the second block's unpacking and of the fragment
-    // and LDS loads, in this order: with the two waves of a SIMD out of step, one's
+    // and LDS loads, in this order: with the waves of a SIMD out of step, one's
     // vector work runs beside the other's matrix work (all loads of a step issued
     // together took 367 us instead of 354 for 8186 rows x 2048 x 5632 Q8_0).
     constexpr bool SCALED = WT != W_MXFP4;
@@ -286,10 +288,9 @@ __global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel
             else if constexpr (k % PU == 0) sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, f32x16{}, 0, 0, 0);
             else sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, sum[u & 1], 0, 0, 0);
             if constexpr (k + AHEAD < MI) x[k % AHEAD] = frag(std::integral_constant<int, k + AHEAD>{});
-            // one load behind each of the first instructions where only one stage is
-            // ahead, else spread over the step (4096 rows, MXFP4 pair of 5632 x 2048 with
-            // large tiles: 230 us, spread 238; 1024 rows, Q4_0 2048 x 2048 with small
-            // ones: 29.8 and 29.3)
+            // with one stage ahead a load behind each of the first instructions, so that
+            // they have the rest of the step to land (spread over the step, a pair of
+            // 5632 x 2048 MXFP4 for 4096 rows took 238 us instead of 230), else spread
             constexpr int per = (T::LOADS + MI - 1) / MI, gap = per > 1 || T::STAGES == 2 ? 1 : MI / T::LOADS;
             static_for<per>([&](auto I) {
                 constexpr int l = k / gap * per + decltype(I)::value;
@@ -381,23 +382,28 @@ __global__ __launch_bounds__(kThreads, KP == 1 ? 3 : 2) void gemm_grouped_kernel
     }
 }
 
-template <int WT, int SS, int KP, bool SW>
+template <int WT, int SS, int KP, bool SW, int NST>
 hipError_t launch_tile(GrpArgs &a, hipStream_t stream)
 {
-    using T = GrpTile<WT, KP>;
+    using T = GrpTile<WT, KP, NST>;
     a.m_tiles = (int32_t)((a.M + (SW ? T::BM / 2 : T::BM) - 1) / (SW ? T::BM / 2 : T::BM));
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&gemm_grouped_kernel<WT, SS, KP, SW>), T::LDS_BYTES);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&gemm_grouped_kernel<WT, SS, KP, SW, NST>), T::LDS_BYTES);
     if (e != hipSuccess) return e;
     const int64_t blocks = grouped_row_tiles(a.R, a.E, T::BN) * a.m_tiles;
-    hipLaunchKernelGGL((gemm_grouped_kernel<WT, SS, KP, SW>), dim3((unsigned)blocks), dim3(kThreads), T::LDS_BYTES, stream, a);
+    hipLaunchKernelGGL((gemm_grouped_kernel<WT, SS, KP, SW, NST>), dim3((unsigned)blocks), dim3(kThreads), T::LDS_BYTES, stream, a);
     return hipGetLastError();
 }
-template <int WT, int SS>
-hipError_t launch_type(GrpArgs &a, int kp, bool sw, hipStream_t stream)
+template <int WT, int SS, bool SW>
+hipError_t launch_form(GrpArgs &a, GroupedForm f, hipStream_t stream)
 {
-    if (kp == 1) return sw ? launch_tile<WT, SS, 1, true>(a, stream) : launch_tile<WT, SS, 1, false>(a, stream);
-    if (kp == 2) return sw ? launch_tile<WT, SS, 2, true>(a, stream) : launch_tile<WT, SS, 2, false>(a, stream);
-    return sw ? launch_tile<WT, SS, 4, true>(a, stream) : launch_tile<WT, SS, 4, false>(a, stream);
+    if (f.kp == 1) return launch_tile<WT, SS, 1, SW, 2>(a, stream);
+    if (f.kp == 2) return f.deep ? launch_tile<WT, SS, 2, SW, 3>(a, stream) : launch_tile<WT, SS, 2, SW, 2>(a, stream);
+    return f.deep ? launch_tile<WT, SS, 4, SW, 3>(a, stream) : launch_tile<WT, SS, 4, SW, 2>(a, stream);
+}
+template <int WT, int SS>
+hipError_t launch_type(GrpArgs &a, GroupedForm f, bool sw, hipStream_t stream)
+{
+    return sw ? launch_form<WT, SS, true>(a, f, stream) : launch_form<WT, SS, false>(a, f, stream);
 }
 
 }  // namespace
@@ -429,11 +435,11 @@ hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const 
     a.R = (int32_t)y.R;
     a.bf16_out = y.bf16;
     const bool sw = up != nullptr;
-    const int kp = grouped_form(a.M, w.w.K, y.R, w.E, w.w.type, sw, device_cus());
-    if (kp == 0) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
-    if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, kp, sw, stream);
-    if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, kp, sw, stream) : launch_type<W_Q4_0, 0>(a, kp, sw, stream);
-    if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, kp, sw, stream) : launch_type<W_Q8_0, 0>(a, kp, sw, stream);
+    const GroupedForm f = grouped_form(a.M, w.w.K, y.R, w.E, w.w.type, sw, device_cus());
+    if (f.kp == 0) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
+    if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, f, sw, stream);
+    if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, f, sw, stream) : launch_type<W_Q4_0, 0>(a, f, sw, stream);
+    if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, f, sw, stream) : launch_type<W_Q8_0, 0>(a, f, sw, stream);
     return hipErrorInvalidValue;
 }
 

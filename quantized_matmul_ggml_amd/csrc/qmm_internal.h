@@ -207,41 +207,48 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
     p.m_tiles = (tiles + 8 * p.tiles_per_wave - 1) / (8 * p.tiles_per_wave);
     return p;
 }
-// The form of a launch by its estimated time: 0, rows streamed (gemm_rows.hip); else
-// the waves of a workgroup that split K (1, 2 or 4), which makes its tile 128,
-// 64 or 32 rows.  Only R and E are known here, not the groups, so that each
+// The form of a launch: 0, rows streamed (gemm_rows.hip); else the waves of a
+// workgroup that split K (1, 2 or 4), which makes its tile 128, 64 or 32 rows; the
+// small ones deep (three stages of loads) where a CU has two tiles or fewer.
+struct GroupedForm {
+    int kp;
+    bool deep;
+};
+// It is chosen by its estimated time.  Only R and E are known here, not the groups, so that each
 // group counts half a tile more than its share of R, and a tenth of the groups one
 // tile more than the others.
 //  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
-//    workgroups overlap, a CU's only one 1.4 times that.
+//    workgroups overlap, a CU's only one 1.8 times that.
 //  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
-//    bytes a ns, and before it `lone` us for 2048 of K, the way through a row.
+//    bytes a ns (less for rows longer than the image), and before it `lone` us for
+//    2048 of K, the way through a row.
 // 164 launches over types, K, M, experts and even and uneven groups, each timed in
-// all four forms: the one taken here is 1.5 % slower than the best on average and 30 %
-// at most (sixteen experts with eight rows on average, 1 to 17 in fact).  In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
-// Q4_0, 256 rows 71 / 63 / 52 / 64, 1024 rows 206 / 175 / 105 / 93, 4096 rows 758 /
-// 638 / 354 / 271; the same MXFP4, 512 uneven rows 77 / 89 / 58 / 80.
-inline int grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+// all four forms: the one taken here is 1.2 % slower than the best on average and 30 %
+// at most (sixteen experts with eight rows on average, 1 to 17 in fact).  In us
+// as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048 Q4_0, 256
+// rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 / 349 /
+// 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80.
+inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
     const double used = (double)(E < R ? E : R), k1024 = (double)K / 1024;
     auto row_tiles = [&](int bn) {
         const double t = (double)R / bn + used / 2;
         return t < 1.1 * used ? 1.1 * used : t;
     };
-    const double rate = type == W_Q4_0 ? 4.3 : 6.5, unpack = type == W_MXFP4 ? 0.85 : type == W_Q4_0 ? 1.0 : 1.07;
-    const double lone = type == W_MXFP4 ? 4.2 : 7;
+    const double rate = type == W_Q4_0 ? 4.3 : type == W_MXFP4 ? 6.7 : 6.9, unpack = type == W_MXFP4 ? 0.85 : type == W_Q4_0 ? 1.0 : 1.07;
+    const double lone = type == W_MXFP4 ? 2.6 : 4.3;
     const double bytes = (double)M * (double)K * (type == W_Q8_0 ? 1.06 : 0.55) * (swiglu ? 2 : 1);
-    int best = 0;
-    double least = 4 + lone * (double)K / 2048 + row_tiles(16) * bytes / (1e6 * rate);
-    static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.6, 9.2}, {2, 1.6, 3.0}, {4, 1.35, 1.1}};
+    GroupedForm best = {0, false};
+    double least = 4 + lone * (double)K / 2048 + row_tiles(16) * bytes / (1e6 * rate) * (K > 2048 ? 1.15 : 1.0);
+    static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.4, 8.0}, {2, 0.95, 2.8}, {4, 0.75, 1.2}};
     for (const auto &f : forms) {
         const int64_t bm = (swiglu ? 64 : 128) / f.kp;
         const double share = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm) / (double)cus;
-        const double rounds = share <= 1 ? 1.4 : share < 1e9 ? (double)((int64_t)share + ((double)(int64_t)share < share)) : share;
+        const double rounds = share <= 1 ? 1.8 : share < 1e9 ? (double)((int64_t)share + ((double)(int64_t)share < share)) : share;
         const double t = 3 + unpack * (f.fixed + f.k1024 * k1024) * rounds;
         if (t < least) {
             least = t;
-            best = f.kp;
+            best = GroupedForm{f.kp, f.kp > 1 && share <= 2};
         }
     }
     return best;
@@ -249,7 +256,7 @@ inline int grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bo
 // Threads of the launch stay below 2^32 (kMaxGridThreads).
 inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
-    const int kp = grouped_form(M, K, R, E, type, swiglu, cus);
+    const int kp = grouped_form(M, K, R, E, type, swiglu, cus).kp;
     const int64_t bm = kp ? (swiglu ? 64 : 128) / kp : 0;
     const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles;
     const int64_t n = grouped_row_tiles(R, E, kp ? 128 / kp : 16), most = (int64_t)(kMaxGridThreads / 512) - 1;

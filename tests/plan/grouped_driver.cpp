@@ -47,7 +47,8 @@ int main()
         long long cus, type, pair, M, K, R, E, N, r, wide;
         if (sscanf(line, "grouped %lld %lld %lld %lld %lld %lld %lld", &cus, &type, &pair, &M, &K, &R, &E) == 7) {
             const int w = type == 0 ? W_MXFP4 : type == 1 ? W_Q4_0 : W_Q8_0;
-            const int kp = grouped_form(M, K, R, E, w, pair, cus);
+            const GroupedForm form = grouped_form(M, K, R, E, w, pair, cus);
+            const int kp = form.kp;
             const RowsPlan p = plan_grouped_rows(M, K, R, E, w, pair, cus);
             if (kp != 0 && kp != 1 && kp != 2 && kp != 4) return bad(line, "form");
             const int64_t tile = pair ? 8 : 16, rows = 8 * p.tiles_per_wave * tile;
@@ -62,7 +63,7 @@ int main()
             const bool fits = grouped_fits(M, K, R, E, w, pair, cus);
             const int64_t bm = kp ? (pair ? 64 : 128) / kp : 0, m = kp ? (M + bm - 1) / bm : p.m_tiles;
             if (fits && (double)m * (double)grouped_row_tiles(R, E, bn) * (kp ? 256 : 512) >= 4294967296.0) return bad(line, "threads");
-            printf("form=%d depth=%d tiles=%d passes=%d fits=%d\n", kp, p.depth, p.tiles_per_wave, K > 2048, fits);
+            printf("form=%d%s depth=%d tiles=%d passes=%d fits=%d\n", kp, form.deep ? "deep" : "", p.depth, p.tiles_per_wave, K > 2048, fits);
         } else if (sscanf(line, "lora %lld %lld %lld %lld %lld %lld", &cus, &N, &K, &M, &r, &wide) == 6) {
             const LoraPlan p = plan_lora(N, K, M, r, wide, cus);
             if (const char *rule = check(p, N, K, M, r, wide)) return bad(line, rule);

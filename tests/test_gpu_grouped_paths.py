@@ -15,9 +15,10 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 # pair, M, K, rows, experts
-PRODUCTS = [(0, 600, 352, 6000, 8), (1, 270, 352, 6000, 8), (0, 400, 352, 2000, 8), (1, 130, 352, 3000, 8), (0, 200, 1056, 33, 2),
-            (1, 130, 1056, 33, 1), (0, 70, 2080, 150, 5), (1, 33, 2080, 70, 3), (0, 130, 5632, 300, 3), (0, 530, 1024, 64, 64), (0, 200, 96, 130, 64), (1, 129, 1024, 64, 64),
-            (1, 65, 1056, 64, 64)]
+PRODUCTS = [(0, 600, 352, 6000, 8), (1, 400, 352, 6000, 8), (0, 400, 352, 6000, 8), (0, 400, 352, 4000, 8), (1, 270, 352, 4000, 8),
+            (1, 200, 352, 4000, 8), (0, 130, 1056, 4000, 8), (0, 600, 352, 300, 8), (1, 130, 1056, 2000, 8), (1, 270, 352, 300, 8),
+            (0, 270, 352, 700, 1), (0, 70, 2080, 150, 5), (1, 33, 2080, 70, 3), (0, 130, 5632, 300, 3), (0, 530, 1024, 64, 64),
+            (0, 200, 96, 130, 64), (1, 129, 1024, 64, 64), (1, 65, 1056, 64, 64)]
 # streamed rows with several tiles to a wave, whose types are said
 STREAMED = [("mxfp4", 0, 2050, 128, 64, 64), ("q4_0", 0, 1030, 96, 256, 256), ("q4_b64", 1, 1030, 128, 64, 64), ("mxfp4", 1, 2050, 128, 64, 64),
             ("q8_0", 0, 1030, 512, 256, 256), ("q8_b64", 1, 1030, 512, 64, 64), ("q4_0", 1, 1030, 1024, 64, 64)]

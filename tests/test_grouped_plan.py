@@ -60,7 +60,7 @@ def test_gpu_shapes_take_every_form(plan):
             launches.append(f"grouped 256 {TYPE[kind]} {pair} {M} {K} {rows} {E}")
             kinds.append((kind, pair))
     got = {(*k, p["form"]) for k, p in zip(kinds, plan(launches))}
-    assert got == {(k, pair, form) for k in TYPE for pair in (0, 1) for form in "0124"}
+    assert got == {(k, pair, form) for k in TYPE for pair in (0, 1) for form in ("0", "1", "2", "2deep", "4", "4deep")}
     depths = {(*k, p["depth"]) for k, p in zip(kinds, plan(launches)) if p["form"] == "0"}
     assert {d for *_, d in depths} == {"4", "8"}
     plans = plan([f"grouped 256 {TYPE[k]} {pair} {M} {K} {rows} {E}" for k, pair, M, K, rows, E in P.STREAMED])
