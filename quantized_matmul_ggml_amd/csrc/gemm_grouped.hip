@@ -63,7 +63,7 @@ struct GrpTile {
     // With two stages three workgroups share a CU, with three two.  Where there are
     // enough tiles the workgroup is worth more than the stage (gate and up of 4096 rows,
     // 5632 x 2048 Q4_0, two and three stages: 64-row tiles 349 and 376 us, 32-row ones
-    // 565 and 670; 7372 rows, 128-row tiles 501 and 543); up to two tiles a CU the
+    // 565 and 670; 7372 rows, 128-row tiles 501 and 543); with few tiles a CU the
     // stage is (486 rows, pair of 321 x 3584 Q4_0 17.4 and 15.6, 137 rows, layer of
     // three Q8_0 experts 2176 -> 3648 48.9 and 45.4).
     static constexpr int STAGES = NST;
