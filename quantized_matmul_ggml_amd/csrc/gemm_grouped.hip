@@ -26,10 +26,11 @@
 //
 // Bound by the vector work beside the matrix instructions (one multiply-add per
 // output and block, and the unpacking) at the clock that it leaves: 8186 rows x
-// 2048 x 5632 Q8_0 over 8 experts took 349 us (541 TFLOP/s), 615 thousand cycles at
-// 1.74 GHz (2.3 GHz with operands of zeros) of which the matrix cores were busy 193
-// thousand and the vector units 326 thousand; a matrix instruction costs two waves
-// of a SIMD about 8 issue cycles, other vector ones 4 to 5.
+// 2048 x 5632 Q8_0 over 8 experts take 299 us a call (632 TFLOP/s; 307 to 345 under
+// the profiler, 615 thousand cycles at 1.74 GHz, 2.3 GHz with operands of zeros), of
+// which the matrix cores are busy 193 thousand and the vector units 326 thousand; a
+// matrix instruction costs the waves of a SIMD about 8 issue cycles, other vector
+// ones 4 to 5.
 #include "gemm_common.h"
 #include "grouped_tile.h"
 #include "lds_load.h"

@@ -210,15 +210,15 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
 // The form of a launch: 0, rows streamed (gemm_rows.hip); else the waves of a
 // workgroup that split K (1, 2 or 4), which makes its tile 128, 64 or 32 rows; the
 // small ones deep (three stages of loads, two workgroups on a CU instead of three)
-// where a CU has two tiles or fewer, or four: two rounds of two, else three and one (32
-// rows of four experts, pair of 3623 x 1792 Q8_0: 18.3 and 19.4 us).
+// where a CU has two tiles or fewer, or four: two rounds of two, else three and one
+// (32 rows of four experts, pair of 3623 x 1792 Q8_0: 18.3 and 19.4 us).
 struct GroupedForm {
     int kp;
     bool deep;
 };
-// It is chosen by its estimated time.  Only R and E are known here, not the groups, so that each
-// group counts half a tile more than its share of R, and a tenth of the groups one
-// tile more than the others.
+// It is chosen by its estimated time.  Only R and E are known here, not the groups,
+// so that each group counts half a tile more than its share of R, and a tenth of
+// the groups one tile more than the others.
 //  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
 //    workgroups overlap, a CU's only one 1.8 times that.
 //  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
