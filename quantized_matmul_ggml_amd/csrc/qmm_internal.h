@@ -210,8 +210,11 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
 // The form of a launch: 0, rows streamed (gemm_rows.hip); else the waves of a
 // workgroup that split K (1, 2 or 4), which makes its tile 128, 64 or 32 rows; the
 // small ones deep (three stages of loads, two workgroups on a CU instead of three)
-// where a CU has two tiles or fewer, or four: two rounds of two, else three and one
-// (32 rows of four experts, pair of 3623 x 1792 Q8_0: 18.3 and 19.4 us).
+// where a CU has two tiles or fewer (162 launches of K from 512 on, deep against not:
+// 64-row tiles 4 to 11 % faster, 32-row ones the same), or four: two rounds of two,
+// else three and one (90 launches, 64-row tiles 2 % faster, 32-row ones 1 % slower; 32
+// rows of four experts, pair of 3623 x 1792 Q8_0: 18.3 and 19.4 us).  With more of
+// them, or three, deep ones are 4 and 9 to 13 % slower.
 struct GroupedForm {
     int kp;
     bool deep;
@@ -222,14 +225,14 @@ struct GroupedForm {
 //  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
 //    workgroups overlap, a CU's only one 1.8 times that.
 //  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
-//    bytes a ns (less for rows longer than the image), and before it `lone` us for
-//    2048 of K, the way through a row.
-// 164 launches over types, K, M, experts and even and uneven groups, each timed in
-// all four forms: the one taken here is 1.2 % slower than the best on average and 30 %
-// at most (sixteen experts with eight rows on average, 1 to 17 in fact).  In us
-// as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048 Q4_0, 256
-// rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 / 349 /
-// 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80.
+//    bytes a ns (less for rows longer than the image), or, where that takes longer,
+//    the workgroups' own time: 7 us for two on each CU, whatever K and M are, as
+//    each finds its tile, fills the whole image and then waits for its weights.
+//    Before it `lone` us for 2048 of K, the way through a row.
+// In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
+// Q4_0, 256 rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 /
+// 349 / 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80; 64 x 64 Q4_0, 32768 rows
+// 40 / 14 / 8.5 / 10.7, a million rows 1041 / 306 / 131 / 107.
 inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
     const double used = (double)(E < R ? E : R), k1024 = (double)K / 1024;
@@ -241,7 +244,9 @@ inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int 
     const double lone = type == W_MXFP4 ? 2.6 : 4.3;
     const double bytes = (double)M * (double)K * (type == W_Q8_0 ? 1.06 : 0.55) * (swiglu ? 2 : 1);
     GroupedForm best = {0, false};
-    double least = 4 + lone * (double)K / 2048 + row_tiles(16) * bytes / (1e6 * rate) * (K > 2048 ? 1.15 : 1.0);
+    const double streams = row_tiles(16) * bytes / (1e6 * rate) * (K > 2048 ? 1.15 : 1.0);
+    const double starts = 7 * row_tiles(16) * (double)plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles / (2 * (double)cus);
+    double least = 4 + lone * (double)K / 2048 + (streams > starts ? streams : starts);
     static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.4, 8.0}, {2, 0.95, 2.8}, {4, 0.75, 1.2}};
     for (const auto &f : forms) {
         const int64_t bm = (swiglu ? 64 : 128) / f.kp;
