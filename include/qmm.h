@@ -451,9 +451,10 @@ QMM_API int qmm_moe_group(const int32_t *ids, int64_t n_slots, int32_t n_experts
  * BF16 y, once) round.  Block scales must be finite.
  * Limits (else QMM_ERR_UNSUPPORTED): K, M <= 2^28, R and N < 2^31, weight pitches
  * below 2^24 bytes, N (or, without an order, 128) rows of x below 2^31 bytes, fewer
- * than 2^23 tiles (each of 32 x 32 outputs or more, or of 16 rows and at least 64
- * outputs).  A block's sum is scaled after it is made: it must itself be finite, as it
- * is with activations below 2^113 in magnitude. */
+ * than 2^23 tiles of 128 rows and 128 (the pair: 64) outputs, (R + 127 min(E, R)) / 128
+ * times M / 128 (64), each up to whole tiles.  A block's sum is scaled after it is
+ * made: it must itself be finite, as it is with activations below 2^113 in
+ * magnitude. */
 QMM_API int qmm_gemm_grouped(const qmm_tensor *w, const qmm_tensor *x_bf16, const int32_t *offsets, const int32_t *order,
                              int32_t top_k, qmm_tensor *y, void *stream);
 

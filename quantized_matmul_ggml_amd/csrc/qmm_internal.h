@@ -207,6 +207,15 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
     p.m_tiles = (tiles + 8 * p.tiles_per_wave - 1) / (8 * p.tiles_per_wave);
     return p;
 }
+// Whether one grid takes a launch's tiles in a form (kp as in GroupedForm): its
+// threads stay below 2^32 (kMaxGridThreads).
+inline bool grouped_grid_fits(int kp, int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+{
+    const int64_t bm = kp ? (swiglu ? 64 : 128) / kp : 0;
+    const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles;
+    const int64_t n = grouped_row_tiles(R, E, kp ? 128 / kp : 16), most = (int64_t)(kMaxGridThreads / 512) - 1;
+    return m <= most && n <= most && m * n <= most;
+}
 // The form of a launch: 0, rows streamed (gemm_rows.hip); else the waves of a
 // workgroup that split K (1, 2 or 4), which makes its tile 128, 64 or 32 rows; the
 // small ones deep (three stages of loads, two workgroups on a CU instead of three)
@@ -219,7 +228,7 @@ struct GroupedForm {
     int kp;
     bool deep;
 };
-// It is chosen by its estimated time.  Only R and E are known here, not the groups,
+// It is chosen by its estimated time, among those whose tiles fit one grid.  Only R and E are known here, not the groups,
 // so that each group counts half a tile more than its share of R, and a tenth of
 // the groups one tile more than the others.
 //  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
@@ -247,8 +256,10 @@ inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int 
     const double streams = row_tiles(16) * bytes / (1e6 * rate) * (K > 2048 ? 1.15 : 1.0);
     const double starts = 7 * row_tiles(16) * (double)plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles / (2 * (double)cus);
     double least = 4 + lone * (double)K / 2048 + (streams > starts ? streams : starts);
+    if (!grouped_grid_fits(0, M, K, R, E, type, swiglu, cus)) least = 1e300;      // and stays the answer if none fits
     static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.4, 8.0}, {2, 0.95, 2.8}, {4, 0.75, 1.2}};
     for (const auto &f : forms) {
+        if (!grouped_grid_fits(f.kp, M, K, R, E, type, swiglu, cus)) continue;
         const int64_t bm = (swiglu ? 64 : 128) / f.kp;
         const double share = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm) / (double)cus;
         const double rounds = share <= 1 ? 1.8 : share < 1e9 ? (double)((int64_t)share + ((double)(int64_t)share < share)) : share;
@@ -260,14 +271,10 @@ inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int 
     }
     return best;
 }
-// Threads of the launch stay below 2^32 (kMaxGridThreads).
+// Whether any form takes the launch.
 inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
 {
-    const int kp = grouped_form(M, K, R, E, type, swiglu, cus).kp;
-    const int64_t bm = kp ? (swiglu ? 64 : 128) / kp : 0;
-    const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles;
-    const int64_t n = grouped_row_tiles(R, E, kp ? 128 / kp : 16), most = (int64_t)(kMaxGridThreads / 512) - 1;
-    return m <= most && n <= most && m * n <= most;
+    return grouped_grid_fits(grouped_form(M, K, R, E, type, swiglu, cus).kp, M, K, R, E, type, swiglu, cus);
 }
 hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const ActView &x, const int32_t *offsets,
                                const int32_t *order, int top_k, const GroupedOut &y, hipStream_t stream);

@@ -15,3 +15,17 @@ def test_many_rows_of_few_outputs_are_not_streamed(plan, kind):  # noqa: F811
     shapes += [(pair, M, K, R, E) for pair, M, K, R, E in more.FEW_OUTPUTS]
     plans = plan([f"grouped 256 {TYPE[kind]} {p} {M} {K} {R} {E}" for p, M, K, R, E in shapes])
     assert [s for s, p in zip(shapes, plans) if p["form"] == "0"] == []
+
+
+def test_no_launch_is_refused_that_some_form_takes(plan):  # noqa: F811
+    """The header's limit: fewer than 2^23 tiles of 128 rows and 128 (the pair: 64)
+    outputs, whichever form is estimated to be the fastest."""
+    shapes = [(p, M, K, R, E) for p in (0, 1) for M in (16, 64, 65, 2048, 1 << 20, 1 << 26) for K in (32, 64, 256, 2048)
+              for R in (1, 1000, 1 << 20, 1 << 27, 1 << 28, 1 << 29, (1 << 30) - 1, 1 << 30, (1 << 31) - 1) for E in (1, 8, 1024)]
+    shapes += [(p, M, K, R, E) for p, M, K, R, E, *_ in more.MOST_ROWS]
+    for kind in ("mxfp4", "q4_0", "q8_0"):
+        plans = plan([f"grouped 256 {TYPE[kind]} {p} {M} {K} {R} {E}" for p, M, K, R, E in shapes])
+        for (p, M, K, R, E), q in zip(shapes, plans):
+            rows, bm = (R + 127 * min(E, R)) // 128, 64 if p else 128
+            if rows * -(-M // bm) < 1 << 23:
+                assert q["fits"] == "1", (kind, p, M, K, R, E)
