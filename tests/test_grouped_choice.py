@@ -2,6 +2,7 @@
 host alone), where one form is many times slower than another."""
 import pytest
 
+import test_gpu_grouped_contents as contents
 import test_gpu_grouped_more as more
 from test_grouped_plan import TYPE, plan  # noqa: F401 (a fixture)
 
@@ -29,3 +30,11 @@ def test_no_launch_is_refused_that_some_form_takes(plan):  # noqa: F811
             rows, bm = (R + 127 * min(E, R)) // 128, 64 if p else 128
             if rows * -(-M // bm) < 1 << 23:
                 assert q["fits"] == "1", (kind, p, M, K, R, E)
+
+
+def test_shapes_of_the_contents_tests_take_every_form(plan):  # noqa: F811
+    for form, shapes in contents.SHAPES.items():
+        assert [s[0] for s in shapes] == [0, 1]
+        for kind in TYPE:
+            got = plan([f"grouped 256 {TYPE[kind]} {p} {M} {K} {R} {contents.E}" for p, M, K, R in shapes])
+            assert [p["form"] for p in got] == [form, form], (kind, form)
