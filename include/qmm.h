@@ -492,8 +492,11 @@ QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up
  * may be base itself (same data and pitch) and overlaps no other operand.
  * Limits (else QMM_ERR_UNSUPPORTED): N <= QMM_LORA_MAX_TOKENS, M and the pitches of
  * x, base and y below 2^24 elements, those of a and b below 2^23.
- * Products are exact, their sums and the product with s_a round in binary32; a
- * token's result depends on no other token.
+ * Products are exact, their sums and the product with s_a round in binary32.  No
+ * other token's values enter a token's result, but the order of its sums may change
+ * with N and with the alignment of x, and so their rounding.  (An infinite value of
+ * an adapter may give NaN where the formula gives an infinity, in the outputs that
+ * it reaches.)
  * workspace: qmm_lora_workspace_size bytes (0 for a few tokens; fewer:
  * QMM_ERR_SCRATCH), 16-byte aligned, overlapping no operand; scratch for this call
  * alone until its kernels have run. */

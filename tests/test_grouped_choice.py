@@ -4,6 +4,7 @@ import pytest
 
 import test_gpu_grouped_contents as contents
 import test_gpu_grouped_more as more
+import test_gpu_lora_contents as adapters
 from test_grouped_plan import TYPE, plan  # noqa: F401 (a fixture)
 
 
@@ -38,3 +39,10 @@ def test_shapes_of_the_contents_tests_take_every_form(plan):  # noqa: F811
         for kind in TYPE:
             got = plan([f"grouped 256 {TYPE[kind]} {p} {M} {K} {R} {contents.E}" for p, M, K, R in shapes])
             assert [p["form"] for p in got] == [form, form], (kind, form)
+
+
+def test_shapes_of_the_adapters_contents_tests_take_every_form(plan):  # noqa: F811
+    shapes = adapters.SHAPES.values()
+    plans = plan([f"lora 256 {N} {K} {M} {r} 1" for N, L, r, K, M in shapes])
+    got = ["one launch" if p["single"] == "1" else "tiles" if p["tiled"] == "1" else "registers" for p in plans]
+    assert got == list(adapters.SHAPES)
