@@ -469,12 +469,16 @@ QMM_API int qmm_gemm_grouped_swiglu(const qmm_tensor *w_gate, const qmm_tensor *
  *   y[n] = sum_s weights[n][s] Wd_e (Swish(Wg_e x[n]) * (Wu_e x[n])), e = ids[n][s],
  * as qmm_moe_swiglu, with x BF16 ne = [K, N] and y F32 or BF16 ne = [M, N]; empty
  * slots, experts named twice and tokens without experts as there.  It groups the
- * slots and runs the two grouped products; between them h is BF16 (the activation
- * type of every product of many tokens), the sum over a token's slots is
- * binary32.  Limits as in qmm_gemm_grouped, with R = N top_k and F < 2^23.
+ * slots and runs the two grouped products; the sum over a token's slots is binary32.
+ * Between the products h is BF16 (the activation type of every product of many
+ * tokens; y is then the same as from the parts' calls), which alone makes y, whatever
+ * its type, off by about 2e-3 of its norm.  With 2 R F + 256 bytes of workspace more
+ * than are needed, and F < 2^22, h is held in two bf16 parts, within 2^-16 of each
+ * value.
+ * Limits as in qmm_gemm_grouped, with R = N top_k and F < 2^23.
  * workspace: qmm_moe_gemm_workspace_size bytes (about R (2 F + 4 M); fewer:
- * QMM_ERR_SCRATCH) of device memory, 16-byte aligned, overlapping no operand;
- * scratch for this call alone until its kernels have run. */
+ * QMM_ERR_SCRATCH) of device memory or more, 16-byte aligned, all workspace_bytes
+ * overlapping no operand; scratch for this call alone until its kernels have run. */
 QMM_API size_t qmm_moe_gemm_workspace_size(const qmm_tensor *w_gate, const qmm_tensor *w_down, const qmm_tensor *x_bf16,
                                            int32_t top_k);
 QMM_API int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const qmm_tensor *w_down,

@@ -690,9 +690,15 @@ def gemm_grouped_swiglu(w_gate: Experts, w_up: Experts, x: torch.Tensor, offsets
     return _grouped("qmm_gemm_grouped_swiglu", (w_gate, w_up), x, offsets, order, top_k, out, dtype, stream)
 
 
-def moe_gemm_workspace_size(w_gate: Experts, w_down: Experts, x: torch.Tensor, top_k: int) -> int:
-    """Bytes of workspace qmm_moe_gemm_swiglu needs for these shapes."""
-    return int(lib().qmm_moe_gemm_workspace_size(w_gate._desc(), w_down._desc(), _dense(x, BF16), top_k))
+def moe_gemm_workspace_size(w_gate: Experts, w_down: Experts, x: torch.Tensor, top_k: int, split: bool = False) -> int:
+    """Bytes of workspace qmm_moe_gemm_swiglu needs for these shapes; split: with room
+    to hold h in two bf16 parts."""
+    need = int(lib().qmm_moe_gemm_workspace_size(w_gate._desc(), w_down._desc(), _dense(x, BF16), top_k))
+    return need + _split_bytes(x.shape[0], top_k, w_gate.M) if split and need else need
+
+
+def _split_bytes(tokens: int, top_k: int, F: int) -> int:
+    return 2 * tokens * top_k * F + 256
 
 
 def moe_gemm_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Tensor, ids: torch.Tensor,
@@ -701,7 +707,9 @@ def moe_gemm_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Te
     """y (N, M): moe_swiglu for any number of tokens, x (N, K) bf16; ids (int32) and
     weights (fp32) (N, top_k), contiguous.  dtype: float32 or bfloat16, of the y
     made here.  workspace: a uint8 device tensor of at least
-    moe_gemm_workspace_size bytes, or None to allocate one (graph-capture safe)."""
+    moe_gemm_workspace_size bytes, or None to allocate one (graph-capture safe).
+    With that of split=True, which None allocates for a bf16 y, h is held in two bf16
+    parts between the products, else in one (and y is what the parts' calls give)."""
     if weights.dtype != torch.float32 or ids.dim() != 2 or x.dim() != 2 or ids.shape != weights.shape \
             or ids.shape[0] != x.shape[0] or not weights.is_contiguous():
         raise ValueError("ids (int32) and weights (float32) must be contiguous and (N, top_k)")
@@ -709,7 +717,10 @@ def moe_gemm_swiglu(w_gate: Experts, w_up: Experts, w_down: Experts, x: torch.Te
     gd, dd, xd = w_gate._desc(), w_down._desc(), _dense(x, BF16)
     out, yd = _dense_out(out, stream, x.device, dtype, x.shape[0], w_down.M)
     if workspace is None:
-        workspace = _workspace(stream, x.device, int(lib().qmm_moe_gemm_workspace_size(gd, dd, xd, top_k)))
+        need = int((_lib or lib()).qmm_moe_gemm_workspace_size(gd, dd, xd, top_k))
+        if need and out.dtype is torch.bfloat16:
+            need += _split_bytes(x.shape[0], top_k, w_gate.M)
+        workspace = _workspace(stream, x.device, need)
     else:
         _need_bytes(workspace, 0, "workspace")
     dev = _need_gpu(w_gate.data, w_up.data, w_down.data, x, ids, weights, out, workspace)

@@ -18,7 +18,8 @@
 //   KP = 1: 128 weight rows x 128 grouped rows, K in steps of 64
 //   KP = 2:  64 x 64, steps of 128
 //   KP = 4:  32 x 32, steps of 256
-// so that a step is 16 KB of activations and 128 x 64 weights in all three,
+// so that a step is 16 KB of activations and 128 x 64 weights in all three (of rows in
+// two bf16 parts, P = 2, half as many weights),
 // and a wave multiplies 32 weight rows by the tile's rows over 64 of K.  Steps
 // go from memory to LDS with direct-to-LDS loads one or two steps ahead, one barrier
 // each; two or three workgroups share a CU, so that one's matrix instructions run
@@ -47,7 +48,7 @@ template <> struct GrpFmt<W_Q4_0> { static constexpr int QB = 16; };
 template <> struct GrpFmt<W_MXFP4> { static constexpr int QB = 16; };
 template <> struct GrpFmt<W_Q8_0> { static constexpr int QB = 32; };
 
-template <int WT, int KP, int NST>
+template <int WT, int KP, int NST, int P>
 struct GrpTile {
     static constexpr int QB = GrpFmt<WT>::QB;      // code bytes of a 32-block
     static constexpr int RG = 4 / KP;              // waves along the weight rows
@@ -59,8 +60,12 @@ struct GrpTile {
     static constexpr int TPR = BK * 2 / 16;        // 16-byte chunks per grouped row and step
     static constexpr int TOK_LOADS = kTokBytes / (16 * kThreads);
     static constexpr int LOADS = TOK_LOADS + CODE_LOADS + 1;   // per wave and step
-    static constexpr int CODE_OFF = kTokBytes, SCALE_OFF = CODE_OFF + CODE_BYTES;
-    static constexpr int STAGE = SCALE_OFF + kScaleBytes;
+    // With P = 2 a row's step of 64 KP values is of half as many weights, and the weights
+    // of two such steps are loaded together, to one of two places of their own (loaded
+    // with each step, the layer of 4096 tokens took 921 us, so 858).
+    static constexpr int STAGE = kTokBytes + (P == 1 ? CODE_BYTES + kScaleBytes : 0);
+    static constexpr int CODE_OFF = P == 1 ? kTokBytes : NST * kTokBytes, SCALE_OFF = CODE_OFF + CODE_BYTES;
+    static constexpr int W_STAGE = P == 1 ? STAGE : CODE_BYTES + kScaleBytes;      // between weights' places
     // With two stages three workgroups share a CU, with three two.  Where there are
     // enough tiles the workgroup is worth more than the stage (gate and up of 4096 rows,
     // 5632 x 2048 Q4_0, two and three stages: 64-row tiles 349 and 376 us, 32-row ones
@@ -68,7 +73,7 @@ struct GrpTile {
     // stage is (486 rows, pair of 321 x 3584 Q4_0 17.4 and 15.6, 137 rows, layer of
     // three Q8_0 experts 2176 -> 3648 48.9 and 45.4).
     static constexpr int STAGES = NST;
-    static constexpr int LDS_BYTES = STAGES * STAGE;
+    static constexpr int LDS_BYTES = STAGES * STAGE + (P == 1 ? 0 : 2 * W_STAGE);
     static_assert(BN * BK * 2 == kTokBytes && CODE_BYTES == CODE_LOADS * 16 * kThreads, "whole loads");
     static_assert((KP == 1 ? 3 : 2) * LDS_BYTES <= 160 * 1024, "workgroups per CU");
     static_assert(KP == 1 || 4 * 64 * TT * 16 * 4 <= LDS_BYTES, "the waves' sums fit the ring");
@@ -103,10 +108,11 @@ __device__ inline uint32_t unpack_pair(u32x2 c0, u32x2 c1, float scale)
 
 __device__ inline float grp_swish(float z) { return z / (1.0f + expf(-z)); }
 
-template <int WT, int SS, int KP, bool SW, int NST>
+template <int WT, int SS, int KP, bool SW, int NST, int P>
 __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kernel(const GrpArgs a)
 {
-    using T = GrpTile<WT, KP, NST>;
+    using T = GrpTile<WT, KP, NST, P>;
+    static_assert(P == 1 || !SW, "split rows are the pair's own output");
     constexpr int TT = T::TT, BN = T::BN, BK = T::BK;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(lds);
@@ -124,8 +130,8 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     // TPR-chunk rows; chunk slot s of row t holds chunk s ^ (t's low bits), so
     // that rows read together fall in different banks.  Rows outside the
     // group, tokens outside x and chunks past K read zeros.
-    const int steps = (a.K + BK - 1) / BK;
-    const uint32_t x_bytes = (uint32_t)(((uint64_t)((a.order ? a.N : toks) - 1) * a.x_pitch + a.K) * 2);
+    const int steps = (P * a.K + BK - 1) / BK;
+    const uint32_t x_bytes = (uint32_t)(((uint64_t)((a.order ? a.N : toks) - 1) * a.x_pitch + P * a.K) * 2);
     const ll_i32x4 xres = ll_rsrc(a.order ? a.x : a.x + (uint64_t)n0 * a.x_pitch, a.K > 0 ? x_bytes : 0);
     uint32_t xoff[T::TOK_LOADS];
     int xk[T::TOK_LOADS];
@@ -135,7 +141,7 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
         const int q = u % T::TPR ^ (T::TPR >= 16 ? t & 15 : t >> 1 & 7);
         const int row = t >= toks ? -1 : a.order ? token_of(a, n0 + t) : t;
         xoff[i] = row >= 0 ? (uint32_t)((uint64_t)row * a.x_pitch * 2) + 16u * q : OUT_OF_RANGE;
-        xk[i] = row >= 0 ? a.K - 8 * q : INT32_MIN;      // the chunk of step s is in K iff BK s < xk
+        xk[i] = row >= 0 ? P * a.K - 8 * q : INT32_MIN;      // the chunk of step s is in K iff BK s < xk
     }
     // Codes: the same with the tile's weight rows; with SW rows 0 .. BM / 2 - 1
     // are of the gate matrix and the rest the same rows of the up matrix.
@@ -170,27 +176,28 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     const uint32_t soff = lane < SROWS * DPR && smr < rows
                               ? (uint32_t)(smr * (scale_upper ? a.pitch2 : a.pitch)) + 4u * (lane % DPR) : OUT_OF_RANGE;
     const int sk = (a.K / 32 * 2 >> SS) - 4 * (lane % DPR);
-    const int full = a.K / BK;                           // steps wholly in K
-    // Load L of a wave for step s.  FAST: the step is wholly in K, its offset goes
-    // in as a scalar; else every lane is checked against K (past the last step
-    // all read zeros).
+    const int full = P * (a.K / BK);                     // steps wholly in K, with their weights
+    // Load L of a wave for step s, weights (with P = 2 every other step has some) to
+    // place w.  FAST: the step is wholly in K, its offset goes in as a scalar; else every
+    // lane is checked against K (past the last step all read zeros).
     auto load = [&](auto FAST, auto L, int s, int stage) {
         constexpr int l = decltype(L)::value;
         constexpr bool fast = decltype(FAST)::value;
-        const uint32_t base = lds0 + (uint32_t)(stage * T::STAGE) + 1024u * wave;
+        const int ws = s / P, w = P == 1 ? stage : ws & 1;
+        if (P == 2 && l >= T::TOK_LOADS && s % 2) return;
         if constexpr (l < T::TOK_LOADS) {
-            const uint32_t dst = base + 4096u * l, o = 2u * BK * s;
+            const uint32_t dst = lds0 + (uint32_t)(stage * T::STAGE) + 1024u * wave + 4096u * l, o = 2u * BK * s;
             if constexpr (fast) ll_load_at<16>(xres, dst, xoff[l], o);
             else ll_load<16>(xres, dst, BK * s < xk[l] ? xoff[l] + o : OUT_OF_RANGE);
         } else if constexpr (l < T::TOK_LOADS + T::CODE_LOADS) {
             constexpr int i = l - T::TOK_LOADS;
-            const uint32_t dst = base + T::CODE_OFF + 4096u * i, o = 16u * T::UPR * s;
+            const uint32_t dst = lds0 + (uint32_t)(w * T::W_STAGE + T::CODE_OFF) + 1024u * wave + 4096u * i, o = 16u * T::UPR * ws;
             const ll_i32x4 &res = code_upper(i) ? ures : wres;
             if constexpr (fast) ll_load_at<16>(res, dst, coff[i], o);
             else ll_load<16>(res, dst, (int)o < ck[i] && coff[i] != OUT_OF_RANGE ? coff[i] + o : OUT_OF_RANGE);
         } else {
-            const uint32_t dst = lds0 + (uint32_t)(stage * T::STAGE + T::SCALE_OFF) + 256u * wave;
-            const uint32_t o = (uint32_t)(STEP_SCALES * s) & ~3u;
+            const uint32_t dst = lds0 + (uint32_t)(w * T::W_STAGE + T::SCALE_OFF) + 256u * wave;
+            const uint32_t o = (uint32_t)(STEP_SCALES * ws) & ~3u;
             const ll_i32x4 &res = scale_upper ? ures : wres;
             if constexpr (fast) ll_load_at<4>(res, dst, soff, o);
             else ll_load<4>(res, dst, (int)o < sk && soff != OUT_OF_RANGE ? soff + o : OUT_OF_RANGE);
@@ -229,7 +236,8 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     // vector work runs beside the other's matrix work (all loads of a step issued
     // together took 367 us instead of 354 for 8186 rows x 2048 x 5632 Q8_0).
     constexpr bool SCALED = WT != W_MXFP4;
-    constexpr int PER = SCALED && SS ? 2 : 1;            // blocks of a unit
+    constexpr int PER = SCALED && (SS || P == 2) ? 2 : 1;       // blocks (or parts of one) of a unit
+    constexpr int NB = P == 2 ? 1 : 2;                   // weight blocks of a step and wave
     constexpr int UNITS = 2 / PER * TT, PU = 2 * PER;    // units per step, instructions per unit
     constexpr int MI = UNITS * PU, AHEAD = MI < 4 ? MI : 4;
     f32x16 sum[2] = {};                                  // of the units at hand
@@ -242,24 +250,27 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     };
     // step s from its stage, and the loads of step s + T::STAGES - 1 into another
     auto multiply = [&](auto FAST, const uint8_t *st, int s, int next) {
+        // its weights' step and place, and the first block there
+        const int ws = s / P, first = P == 1 ? NB * par : KP * (s % P) + par;
+        const uint8_t *const wst = P == 1 ? st : lds + (ws & 1) * T::W_STAGE;
         u32x2 c0[2], c1[2];
         float d[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int bi = 2 * par + b;                  // block of the step
+        for (int b = 0; b < NB; ++b) {
+            const int bi = first + b;                    // block of the step
             if constexpr (T::QB == 16) {
-                c0[b] = c1[b] = *reinterpret_cast<const u32x2 *>(st + code_at(bi));
+                c0[b] = c1[b] = *reinterpret_cast<const u32x2 *>(wst + code_at(bi));
             } else {
-                c0[b] = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi));
-                c1[b] = *reinterpret_cast<const u32x2 *>(st + code_at(2 * bi + 1));
+                c0[b] = *reinterpret_cast<const u32x2 *>(wst + code_at(2 * bi));
+                c1[b] = *reinterpret_cast<const u32x2 *>(wst + code_at(2 * bi + 1));
             }
         }
         uint32_t raw[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int bi = 2 * par + b;
-            if constexpr (WT == W_MXFP4) raw[b] = st[s_row + (KP == 1 ? 2 * (s & 1) : 0) + bi];
-            else raw[b] = *reinterpret_cast<const uint16_t *>(st + s_row + (SS ? (KP == 1 ? 2 * (s & 1) : 2 * (bi >> 1)) : 2 * bi));
+        for (int b = 0; b < NB; ++b) {
+            const int bi = first + b;
+            if constexpr (WT == W_MXFP4) raw[b] = wst[s_row + (KP == 1 ? 2 * (ws & 1) : 0) + bi];
+            else raw[b] = *reinterpret_cast<const uint16_t *>(wst + s_row + (SS ? (KP == 1 ? 2 * (ws & 1) : 2 * (bi >> 1)) : 2 * bi));
         }
         // instruction k: block b, tile j, chunk c of the block
         auto frag = [&](auto K) {
@@ -271,20 +282,20 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
         static_for<AHEAD>([&](auto K) { x[decltype(K)::value] = frag(K); });
         if constexpr (SCALED && UNITS > 1) add(std::integral_constant<int, UNITS - 1>{}, 0, 16, pending);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
             // a block past K gets a zero scale (a mask: no branch between the products)
-            raw[b] &= 2 * KP * s + 2 * par + b < blocks ? 0xFFFFu : 0u;
+            raw[b] &= 2 * KP * ws + first + b < blocks ? 0xFFFFu : 0u;
             if constexpr (WT == W_MXFP4) d[b] = __builtin_bit_cast(float, raw[b] << 23);
             else d[b] = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[b]) * (WT == W_Q4_0 ? 0.0625f : 1.0f);
         }
         u32x4 w[2][2];
-        static_for<8>([&](auto P) {
-            constexpr int p = decltype(P)::value;
+        static_for<8>([&](auto I) {
+            constexpr int p = decltype(I)::value;
             w[0][p / 4][p % 4] = unpack_pair<WT, p>(c0[0], c1[0], d[0]);
         });
         static_for<MI>([&](auto K) {
             constexpr int k = decltype(K)::value, u = k / PU, b = PER == 2 ? k % PU / 2 : u / TT, j = u % TT, c = k % 2;
-            const bf16x8 wf = __builtin_bit_cast(bf16x8, w[b][c]), xf = x[k % AHEAD];
+            const bf16x8 wf = __builtin_bit_cast(bf16x8, w[P == 2 ? 0 : b][c]), xf = x[k % AHEAD];
             if constexpr (!SCALED) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, acc[j], 0, 0, 0);
             else if constexpr (k % PU == 0) sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, f32x16{}, 0, 0, 0);
             else sum[u & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf, sum[u & 1], 0, 0, 0);
@@ -302,7 +313,7 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
             constexpr int B1 = PER == 2 ? 2 : MI / 2, n = (8 + B1 - 1) / B1;
             static_for<n>([&](auto I) {
                 constexpr int p = k * n + decltype(I)::value;
-                if constexpr (k < B1 && p < 8) w[1][p / 4][p % 4] = unpack_pair<WT, p>(c0[1], c1[1], d[1]);
+                if constexpr (P == 1 && k < B1 && p < 8) w[1][p / 4][p % 4] = unpack_pair<WT, p>(c0[1], c1[1], d[1]);
             });
             // the unit before
             constexpr int share = 16 / PU;
@@ -320,7 +331,10 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     int stage = 0, next = T::STAGES - 1;
     auto run_steps = [&](auto FAST, int s, int to) {
         for (; s < to; ++s) {
-            ll_wait<T::LOADS * (T::STAGES - 2)>();         // this wave's loads of step s have landed
+            // this wave's loads of step s have landed (with three stages, those of the next
+            // step may be pending, with or without weights)
+            if (P == 1 || T::STAGES == 2 || s % 2) ll_wait<T::LOADS * (T::STAGES - 2)>();
+            else ll_wait<T::TOK_LOADS * (T::STAGES - 2)>();
             // every wave's have, and the stage of step s - 1 is free
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             multiply(FAST, lds + stage * T::STAGE, s, next);
@@ -361,7 +375,8 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     auto store = [&](int t, int64_t m, float v) {
         if (t < toks && m < a.M) {
             const uint64_t p = (uint64_t)(n0 + t) * a.y_pitch + m;
-            if (a.bf16_out) static_cast<uint16_t *>(a.y)[p] = (uint16_t)pack_bf16(v, 0.0f);
+            if (SW && a.split_out) store_split(static_cast<uint16_t *>(a.y) + (uint64_t)(n0 + t) * a.y_pitch, m, v);
+            else if (a.bf16_out) static_cast<uint16_t *>(a.y)[p] = (uint16_t)pack_bf16(v, 0.0f);
             else static_cast<float *>(a.y)[p] = v;
         }
     };
@@ -383,28 +398,29 @@ __global__ __launch_bounds__(kThreads, NST == 2 ? 3 : 2) void gemm_grouped_kerne
     }
 }
 
-template <int WT, int SS, int KP, bool SW, int NST>
+template <int WT, int SS, int KP, bool SW, int NST, int P>
 hipError_t launch_tile(GrpArgs &a, hipStream_t stream)
 {
-    using T = GrpTile<WT, KP, NST>;
+    using T = GrpTile<WT, KP, NST, P>;
     a.m_tiles = (int32_t)((a.M + (SW ? T::BM / 2 : T::BM) - 1) / (SW ? T::BM / 2 : T::BM));
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&gemm_grouped_kernel<WT, SS, KP, SW, NST>), T::LDS_BYTES);
+    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(&gemm_grouped_kernel<WT, SS, KP, SW, NST, P>), T::LDS_BYTES);
     if (e != hipSuccess) return e;
     const int64_t blocks = grouped_row_tiles(a.R, a.E, T::BN) * a.m_tiles;
-    hipLaunchKernelGGL((gemm_grouped_kernel<WT, SS, KP, SW, NST>), dim3((unsigned)blocks), dim3(kThreads), T::LDS_BYTES, stream, a);
+    hipLaunchKernelGGL((gemm_grouped_kernel<WT, SS, KP, SW, NST, P>), dim3((unsigned)blocks), dim3(kThreads), T::LDS_BYTES, stream, a);
     return hipGetLastError();
 }
-template <int WT, int SS, bool SW>
+template <int WT, int SS, bool SW, int P>
 hipError_t launch_form(GrpArgs &a, GroupedForm f, hipStream_t stream)
 {
-    if (f.kp == 1) return launch_tile<WT, SS, 1, SW, 2>(a, stream);
-    if (f.kp == 2) return f.deep ? launch_tile<WT, SS, 2, SW, 3>(a, stream) : launch_tile<WT, SS, 2, SW, 2>(a, stream);
-    return f.deep ? launch_tile<WT, SS, 4, SW, 3>(a, stream) : launch_tile<WT, SS, 4, SW, 2>(a, stream);
+    if (f.kp == 1) return launch_tile<WT, SS, 1, SW, 2, P>(a, stream);
+    if (f.kp == 2) return f.deep ? launch_tile<WT, SS, 2, SW, 3, P>(a, stream) : launch_tile<WT, SS, 2, SW, 2, P>(a, stream);
+    return f.deep ? launch_tile<WT, SS, 4, SW, 3, P>(a, stream) : launch_tile<WT, SS, 4, SW, 2, P>(a, stream);
 }
 template <int WT, int SS>
-hipError_t launch_type(GrpArgs &a, GroupedForm f, bool sw, hipStream_t stream)
+hipError_t launch_type(GrpArgs &a, GroupedForm f, bool sw, int parts, hipStream_t stream)
 {
-    return sw ? launch_form<WT, SS, true>(a, f, stream) : launch_form<WT, SS, false>(a, f, stream);
+    if (sw) return launch_form<WT, SS, true, 1>(a, f, stream);
+    return parts == 2 ? launch_form<WT, SS, false, 2>(a, f, stream) : launch_form<WT, SS, false, 1>(a, f, stream);
 }
 
 }  // namespace
@@ -435,12 +451,15 @@ hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const 
     a.N = (int32_t)x.N;
     a.R = (int32_t)y.R;
     a.bf16_out = y.bf16;
+    a.split_out = y.split;
     const bool sw = up != nullptr;
-    const GroupedForm f = grouped_form(a.M, w.w.K, y.R, w.E, w.w.type, sw, device_cus());
-    if (f.kp == 0) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, stream);
-    if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, f, sw, stream);
-    if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, f, sw, stream) : launch_type<W_Q4_0, 0>(a, f, sw, stream);
-    if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, f, sw, stream) : launch_type<W_Q8_0, 0>(a, f, sw, stream);
+    const int parts = x.split ? 2 : 1;
+    if (sw && parts != 1) return hipErrorInvalidValue;
+    const GroupedForm f = grouped_form(a.M, w.w.K, y.R, w.E, w.w.type, sw, device_cus(), parts);
+    if (f.kp == 0) return launch_gemm_rows(a, w.w.type, w.w.scale_shift, sw, parts, stream);
+    if (w.w.type == W_MXFP4) return launch_type<W_MXFP4, 1>(a, f, sw, parts, stream);
+    if (w.w.type == W_Q4_0) return w.w.scale_shift ? launch_type<W_Q4_0, 1>(a, f, sw, parts, stream) : launch_type<W_Q4_0, 0>(a, f, sw, parts, stream);
+    if (w.w.type == W_Q8_0) return w.w.scale_shift ? launch_type<W_Q8_0, 1>(a, f, sw, parts, stream) : launch_type<W_Q8_0, 0>(a, f, sw, parts, stream);
     return hipErrorInvalidValue;
 }
 

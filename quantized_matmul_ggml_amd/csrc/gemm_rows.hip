@@ -12,7 +12,8 @@
 //
 // A workgroup of eight waves takes one row tile of an expert and 8 C tiles of
 // sixteen weight rows (SwiGLU: eight gate rows and the same eight up rows), C to a
-// wave, one after the other without a gap in the loads.
+// wave, one after the other without a gap in the loads.  Rows in two bf16 parts (P = 2,
+// GroupedOut) take two instructions and twice the image per 32 of k.
 //
 // 32 experts, gate and up 1408 x 2048 MXFP4, 33 tokens of four: 21.6 us, 4.5 TB/s of
 // weights; 64 experts with eight rows each, 142 MB of MXFP4: 30.3 us, 4.7 TB/s (34.3
@@ -29,21 +30,22 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 16;                       // grouped rows of a tile
 constexpr int kBlockBytes = kRows * 64;         // LDS bytes of a 32-block's activations
-constexpr int kImage = 64 * 1024;               // LDS of the activations: 2048 of K at a time
-constexpr int kZeros = 4 * kBlockBytes;         // and of a unit of zeros
-constexpr int kScales = kImage + kZeros;        // the waves' scales
+constexpr int kImage = 64 * 1024;               // LDS of the activations: 2048 / P of K at a time
+constexpr int kScales = kImage;                 // the waves' scales
 constexpr int kLds = kScales + kWaves * kScaleLds;
 static_assert(2 * kLds <= 160 * 1024, "two workgroups per CU");
 
 // Multiplies unit q of the rows (as multiply_unit of row_tiles.h) with the fragments
 // at img, adds to acc: columns are the 16 weight rows, rows the grouped ones.
-template <int WT, int SS>
+template <int WT, int SS, int P>
 __device__ inline void multiply_rows(const Unit<WT, SS> &z, const uint8_t *img, int left, int g, rt_f32x4 &acc)
 {
     using F = RowFmt<WT, SS>;
-    rt_bf16x8 fr[F::MF];
+    rt_bf16x8 fr[F::MF][P];
 #pragma unroll
-    for (int t = 0; t < F::MF; ++t) fr[t] = *reinterpret_cast<const rt_bf16x8 *>(img + t * kBlockBytes);
+    for (int t = 0; t < F::MF; ++t)
+#pragma unroll
+        for (int p = 0; p < P; ++p) fr[t][p] = *reinterpret_cast<const rt_bf16x8 *>(img + (t * P + p) * kBlockBytes);
     uint32_t d[4] = {z.q.x, z.q.y, z.q.z, z.q.w};
     if constexpr (WT == W_MXFP4) {
         uint32_t e = (z.s[0] >> (8 * g)) & 0xFFu;
@@ -56,7 +58,9 @@ __device__ inline void multiply_rows(const Unit<WT, SS> &z, const uint8_t *img, 
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 1)),
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 2)),
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[t], f, 3)));
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[t], __builtin_bit_cast(rt_bf16x8, bw), acc, 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[t][p], __builtin_bit_cast(rt_bf16x8, bw), acc, 0, 0, 0);
         }
     } else {
         rt_swap32(d[0], d[2]);
@@ -83,7 +87,9 @@ __device__ inline void multiply_rows(const Unit<WT, SS> &z, const uint8_t *img, 
                     bw = make_uint4(rt_pack(rt_sbyte<0>(p), rt_sbyte<1>(p)), rt_pack(rt_sbyte<2>(p), rt_sbyte<3>(p)),
                                     rt_pack(rt_sbyte<0>(q), rt_sbyte<1>(q)), rt_pack(rt_sbyte<2>(q), rt_sbyte<3>(q)));
                 }
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[t], __builtin_bit_cast(rt_bf16x8, bw), sum, 0, 0, 0);
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fr[t][p], __builtin_bit_cast(rt_bf16x8, bw), sum, 0, 0, 0);
             }
             const int sh = t0 >> SS;                    // the scale (a half) within the unit
             const uint32_t sb = (sh & 1) ? z.s[sh / 2] >> 16 : z.s[sh / 2] & 0xFFFFu;
@@ -104,11 +110,12 @@ __device__ inline void multiply_rows(const Unit<WT, SS> &z, const uint8_t *img, 
 // together in the stream, which memory serves better, and other waves cover the
 // wait (64 experts, 142 MB with 8 rows each: 32.2 us place by place, 30.3 at once;
 // Q4_0, 16 experts of 37 MB: 14.7 and 15.5).
-template <int WT, int SS, bool SW, int D>
-__global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
+// P: the parts of x's rows, or with SW those of h's values.
+template <int WT, int SS, bool SW, int D, int P>
+__global__ __launch_bounds__(kThreads, 4) void gemm_rows_kernel(const GrpArgs a)
 {
     using F = RowFmt<WT, SS>;
-    constexpr int MF = F::MF;
+    constexpr int MF = F::MF, XP = SW ? 1 : P;
     constexpr bool AT_ONCE = WT == W_MXFP4;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
@@ -116,7 +123,6 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
     uint8_t *const scales = lds + kScales + wave * kScaleLds;
     GroupTile tile;
     if (!find_tile<kRows>(a, tile)) return;
-    for (int i = tid; i < kZeros / 16; i += kThreads) reinterpret_cast<uint4 *>(lds + kImage)[i] = make_uint4(0, 0, 0, 0);
     const int blocks = a.K / 32, code_bytes = F::BB * blocks, row_bytes = a.qoff + code_bytes;
     const int C = a.tiles_per_wave;
     constexpr int TILE = SW ? 8 : 16;                   // weight rows (of each matrix) of a tile
@@ -135,7 +141,8 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
     const int xt = tid / 32, xp = tid % 32;
     const int token = xt < tile.rows ? token_of(a, tile.n0 + xt) : -1;
     const uint16_t *const x = a.x + (uint64_t)(token > 0 ? token : 0) * a.x_pitch;
-    const int units = (blocks + MF - 1) / MF, pass_units = kImage / (MF * kBlockBytes);
+    const int units = (blocks + MF - 1) / MF, pass_units = kImage / (MF * XP * kBlockBytes);
+    static_assert(kImage / (MF * XP * kBlockBytes) % D == 0, "whole groups fit the image");
     Unit<WT, SS> z[D];
     ScaleWindow<WT, SS, false, D> window;
     rt_f32x4 acc = {0, 0, 0, 0};
@@ -152,7 +159,8 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
             const int t = 4 * g + r;
             if (t < tile.rows && m < a.M && !upper) {
                 const uint64_t p = (uint64_t)(tile.n0 + t) * a.y_pitch + m;
-                if (a.bf16_out) static_cast<uint16_t *>(a.y)[p] = (uint16_t)rt_pack(v, 0.0f);
+                if constexpr (SW && P == 2) store_split(static_cast<uint16_t *>(a.y) + (uint64_t)(tile.n0 + t) * a.y_pitch, m, v);
+                else if (a.bf16_out) static_cast<uint16_t *>(a.y)[p] = (uint16_t)rt_pack(v, 0.0f);
                 else static_cast<float *>(a.y)[p] = v;
             }
             acc[r] = 0.0f;
@@ -166,9 +174,9 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
         uint2 v0[PIECES], v1[PIECES];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int b = u0 * MF + 8 * i + (xp >> 2);
+            const int b = u0 * MF + 8 * (i / XP) + (xp >> 2);
             // without a branch, at a place that is there
-            const uint16_t *const p = x + 32 * (b < blocks ? b : 0);
+            const uint16_t *const p = x + 32 * (XP * (b < blocks ? b : 0) + i % XP);
             v0[i] = *reinterpret_cast<const uint2 *>(p + run0<WT>(xp & 3));
             v1[i] = *reinterpret_cast<const uint2 *>(p + run1<WT>(xp & 3));
         }
@@ -193,9 +201,9 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
                     v.z = __builtin_amdgcn_perm(v1[i].y, v0[i].y, 0x05040100u);
                     v.w = __builtin_amdgcn_perm(v1[i].y, v0[i].y, 0x07060302u);
                 }
-                const int lb = 8 * i + (xp >> 2), q = xp & 3;       // block within the image, quarter
+                const int lb = 8 * (i / XP) + (xp >> 2), q = xp & 3; // block within the image, quarter
                 if (token < 0 || u0 * MF + lb >= blocks) v = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(lds + image_step<WT>(lb, q) * kBlockBytes + image_group<WT>(lb, q) * (kRows * 16) + xt * 16) = v;
+                *reinterpret_cast<uint4 *>(lds + (image_step<WT>(lb, q) * XP + i % XP) * kBlockBytes + image_group<WT>(lb, q) * (kRows * 16) + xt * 16) = v;
             }
         }
         __syncthreads();
@@ -220,9 +228,9 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
             static_steps<D>([&](auto d) {
                 const int u = q + (int)d.value;
                 window.get(z[d.value], scales, d.value, j);
-                // units past the pass: zero activations and scales
-                multiply_rows<WT, SS>(z[d.value], img + (u < len ? u * MF * kBlockBytes : kImage),
-                                      u < len ? blocks - (u0 + u) * MF : 0, g, acc);
+                // units past the pass: zero activations and scales (whole groups fit the
+                // image, which is zeros past the row)
+                multiply_rows<WT, SS, XP>(z[d.value], img + u * MF * XP * kBlockBytes, u < len ? blocks - (u0 + u) * MF : 0, g, acc);
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (!AT_ONCE) load_codes<WT, SS>(z[d.value], row, a.qoff, code_bytes, u0 + qn + (int)d.value, g);
                 __builtin_amdgcn_sched_barrier(0);
@@ -244,34 +252,35 @@ __global__ __launch_bounds__(kThreads) void gemm_rows_kernel(const GrpArgs a)
         for (int c = 0; c < C; ++c) finish(c);
 }
 
-template <int WT, int SS, bool SW>
+template <int WT, int SS, bool SW, int P>
 hipError_t launch_rows(GrpArgs &a, int depth, hipStream_t stream)
 {
-    const void *fn = depth == 8 ? reinterpret_cast<const void *>(&gemm_rows_kernel<WT, SS, SW, 8>)
-                                : reinterpret_cast<const void *>(&gemm_rows_kernel<WT, SS, SW, 4>);
+    const void *fn = depth == 8 ? reinterpret_cast<const void *>(&gemm_rows_kernel<WT, SS, SW, 8, P>)
+                                : reinterpret_cast<const void *>(&gemm_rows_kernel<WT, SS, SW, 4, P>);
     const hipError_t e = allow_dynamic_lds(fn, kLds);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(grouped_row_tiles(a.R, a.E, kRows) * a.m_tiles)), block(kThreads);
-    if (depth == 8) hipLaunchKernelGGL((gemm_rows_kernel<WT, SS, SW, 8>), grid, block, kLds, stream, a);
-    else hipLaunchKernelGGL((gemm_rows_kernel<WT, SS, SW, 4>), grid, block, kLds, stream, a);
+    if (depth == 8) hipLaunchKernelGGL((gemm_rows_kernel<WT, SS, SW, 8, P>), grid, block, kLds, stream, a);
+    else hipLaunchKernelGGL((gemm_rows_kernel<WT, SS, SW, 4, P>), grid, block, kLds, stream, a);
     return hipGetLastError();
 }
 template <int WT, int SS>
-hipError_t launch_rows(GrpArgs &a, int depth, bool sw, hipStream_t stream)
+hipError_t launch_rows(GrpArgs &a, int depth, bool sw, int parts, hipStream_t stream)
 {
-    return sw ? launch_rows<WT, SS, true>(a, depth, stream) : launch_rows<WT, SS, false>(a, depth, stream);
+    if (sw) return a.split_out ? launch_rows<WT, SS, true, 2>(a, depth, stream) : launch_rows<WT, SS, true, 1>(a, depth, stream);
+    return parts == 2 ? launch_rows<WT, SS, false, 2>(a, depth, stream) : launch_rows<WT, SS, false, 1>(a, depth, stream);
 }
 
 }  // namespace
 
-hipError_t launch_gemm_rows(GrpArgs &a, int type, int scale_shift, bool swiglu, hipStream_t stream)
+hipError_t launch_gemm_rows(GrpArgs &a, int type, int scale_shift, bool swiglu, int parts, hipStream_t stream)
 {
-    const RowsPlan p = plan_grouped_rows(a.M, a.K, a.R, a.E, type, swiglu, device_cus());
+    const RowsPlan p = plan_grouped_rows(a.M, a.K, a.R, a.E, type, swiglu, device_cus(), parts);
     a.tiles_per_wave = p.tiles_per_wave;
     a.m_tiles = (int32_t)p.m_tiles;
-    if (type == W_MXFP4) return launch_rows<W_MXFP4, 0>(a, p.depth, swiglu, stream);
-    if (type == W_Q4_0) return scale_shift ? launch_rows<W_Q4_0, 1>(a, p.depth, swiglu, stream) : launch_rows<W_Q4_0, 0>(a, p.depth, swiglu, stream);
-    if (type == W_Q8_0) return scale_shift ? launch_rows<W_Q8_0, 1>(a, p.depth, swiglu, stream) : launch_rows<W_Q8_0, 0>(a, p.depth, swiglu, stream);
+    if (type == W_MXFP4) return launch_rows<W_MXFP4, 0>(a, p.depth, swiglu, parts, stream);
+    if (type == W_Q4_0) return scale_shift ? launch_rows<W_Q4_0, 1>(a, p.depth, swiglu, parts, stream) : launch_rows<W_Q4_0, 0>(a, p.depth, swiglu, parts, stream);
+    if (type == W_Q8_0) return scale_shift ? launch_rows<W_Q8_0, 1>(a, p.depth, swiglu, parts, stream) : launch_rows<W_Q8_0, 0>(a, p.depth, swiglu, parts, stream);
     return hipErrorInvalidValue;
 }
 

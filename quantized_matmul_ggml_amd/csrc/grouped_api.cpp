@@ -95,7 +95,7 @@ struct LayerSpace {
     uint64_t offsets, order, place, counts, h, d, bytes;
     int64_t d_pitch;             // floats between d's rows
 };
-bool layer_space(int64_t N, int64_t k, int64_t E, int64_t F, int64_t M, LayerSpace *s)
+bool layer_space(int64_t N, int64_t k, int64_t E, int64_t F, int64_t M, bool split, LayerSpace *s)
 {
     const uint64_t R = (uint64_t)(N * k);            // below 2^31, F and M at most 2^28
     s->d_pitch = (M + 3) / 4 * 4;
@@ -104,7 +104,7 @@ bool layer_space(int64_t N, int64_t k, int64_t E, int64_t F, int64_t M, LayerSpa
     s->place = s->order + align256(4 * R);
     s->counts = s->place + align256(4 * R);
     s->h = s->counts + align256(qmm::moe_group_workspace((int64_t)R, E));
-    s->d = s->h + align256(2 * R * (uint64_t)F);
+    s->d = s->h + align256((split ? 4 : 2) * R * (uint64_t)F);
     s->bytes = s->d + align256(4 * R * (uint64_t)s->d_pitch);
     return s->bytes <= kMaxSpan;
 }
@@ -127,7 +127,7 @@ int check_layer(const qmm_tensor *gate, const qmm_tensor *up, const qmm_tensor *
     // the rows of h are F apart; a tile has 128 of them
     if (!x_reach(x, true) || 256 * (uint64_t)gate->ne[1] >= 1ull << 31 ||
         !fits(gate, R, true) || !fits(down, R, false)) return QMM_ERR_UNSUPPORTED;
-    return layer_space(N, top_k, E, gate->ne[1], down->ne[1], s) ? QMM_OK : QMM_ERR_UNSUPPORTED;
+    return layer_space(N, top_k, E, gate->ne[1], down->ne[1], false, s) ? QMM_OK : QMM_ERR_UNSUPPORTED;
 }
 
 // An adapter tensor: BF16, ne = [cols, rows, L].
@@ -237,6 +237,18 @@ int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const 
     if (!ids || !weights || !workspace) return QMM_ERR_NULL;
     if (((uintptr_t)ids | (uintptr_t)weights) % 4 != 0 || (uintptr_t)workspace % 16 != 0) return QMM_ERR_LAYOUT;
     if (workspace_bytes < s.bytes) return QMM_ERR_SCRATCH;
+    // h between the products.  In one bf16 part it is the activation of every product of
+    // many tokens, and takes 2 R F bytes, but is off by up to 2^-8 of a value, which a
+    // BF16 y shows beside its own rounding (4096 tokens over 8 experts, 2048 x 5632 Q4_0:
+    // 2.35e-3 of y's norm, 1.66e-3 with h exact, and 1.66e-3 with an F32 y too).  Two
+    // parts are off by 2^-16 (1.66e-3, and 2.4e-6), take another 2 R F bytes and a second
+    // matrix instruction in the second product (722 -> 858 us; 64 tokens over 64 experts,
+    // 2048 x 1024 MXFP4 78 -> 81): taken where the caller gives the room, and where its
+    // rows' tiles are reached with 32-bit offsets.
+    LayerSpace both;
+    const bool split = layer_space(N, top_k, E, F, M, true, &both) && workspace_bytes >= both.bytes && 512 * (uint64_t)F < 1ull << 31 &&
+                       qmm::grouped_fits(M, F, R, E, weight_view(w_down).type, false, qmm::device_cus(), 2);
+    if (split) s = both;
     const uint64_t pairs = 4 * (uint64_t)R;
     if (!spans(ids, pairs) || !spans(weights, pairs) || !spans(workspace, s.bytes)) return QMM_ERR_UNSUPPORTED;
     const Range in[] = {range_of(w_gate), range_of(w_up), range_of(w_down), range_of(x), range_of(ids, pairs),
@@ -254,10 +266,11 @@ int qmm_moe_gemm_swiglu(const qmm_tensor *w_gate, const qmm_tensor *w_up, const 
     if (e == hipSuccess && F > 0) {
         const qmm::ExpertView up = expert_view(w_up);
         e = qmm::launch_gemm_grouped(expert_view(w_gate), &up, qmm::ActView{x->data, pitch_elems(x), N}, offsets, order, top_k,
-                                     qmm::GroupedOut{base + s.h, (uint64_t)F, R, true}, st);
+                                     qmm::GroupedOut{base + s.h, (uint64_t)(split ? 2 * F : F), R, true, split}, st);
     }
     if (e == hipSuccess)
-        e = qmm::launch_gemm_grouped(expert_view(w_down), nullptr, qmm::ActView{base + s.h, (uint64_t)F, R}, offsets, nullptr, 1,
+        e = qmm::launch_gemm_grouped(expert_view(w_down), nullptr,
+                                     qmm::ActView{base + s.h, (uint64_t)(split ? 2 * F : F), R, qmm::W_BF16, split}, offsets, nullptr, 1,
                                      qmm::GroupedOut{d, (uint64_t)s.d_pitch, R, false}, st);
     if (e == hipSuccess) e = qmm::launch_moe_combine(d, (uint64_t)s.d_pitch, place, weights, top_k, N, M, grouped_out(y), st);
     return status_of(e);

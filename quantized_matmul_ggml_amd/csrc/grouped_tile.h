@@ -20,7 +20,7 @@ struct GrpArgs {
     int32_t K, qoff, E, top_k;
     int32_t N, R;                 // tokens, grouped rows
     int32_t m_tiles;              // tiles along the weight rows
-    int32_t bf16_out;
+    int32_t bf16_out, split_out;  // split_out: GroupedOut's two parts
     int32_t tiles_per_wave;       // gemm_rows.hip
 };
 
@@ -95,6 +95,19 @@ __device__ inline bool find_tile(const GrpArgs &a, GroupTile &t)
     return true;
 }
 
+// Value m of a row, in two parts: rounded to bf16 (cut, where that gives an infinity),
+// and what is left, rounded, so that their sum is within 2^-16 of it.  An infinity is
+// its own first part.
+__device__ inline void store_split(uint16_t *row, int64_t m, float v)
+{
+    const float near = (float)(__bf16)v, cut = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
+    const float first = fabsf(near) == INFINITY ? cut : near;
+    const float rest = fabsf(first) == INFINITY ? 0.0f : v - first;
+    uint16_t *const p = row + m + (m & ~31);
+    p[0] = (uint16_t)(__builtin_bit_cast(uint32_t, first) >> 16);
+    p[32] = __builtin_bit_cast(uint16_t, (__bf16)rest);
+}
+
 // The token of grouped row r, or -1 if it is none of x's.
 __device__ inline int token_of(const GrpArgs &a, int r)
 {
@@ -104,6 +117,6 @@ __device__ inline int token_of(const GrpArgs &a, int r)
     return token < a.N ? token : -1;
 }
 
-hipError_t launch_gemm_rows(GrpArgs &a, int type, int scale_shift, bool swiglu, hipStream_t stream);
+hipError_t launch_gemm_rows(GrpArgs &a, int type, int scale_shift, bool swiglu, int parts, hipStream_t stream);
 
 }  // namespace qmm

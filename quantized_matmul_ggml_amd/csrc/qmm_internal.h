@@ -64,6 +64,7 @@ struct ActView {
     uint64_t pitch_elems;
     int64_t N;
     int type = W_BF16;
+    bool split = false;          // grouped products: rows of 2 K bf16, as GroupedOut's
 };
 
 // Output: N rows of M floats, row n at data + n * pitch_elems.
@@ -179,6 +180,9 @@ struct GroupedOut {
     uint64_t pitch_elems;
     int64_t R;
     bool bf16;
+    // of a pair: each value in two bf16 parts, rounded and what that leaves, rounded
+    // (2^-16 in all); rows of 32 first parts and 32 second ones in turn
+    bool split = false;
 };
 // The most row tiles of bn rows that R rows of E groups can need.
 inline int64_t grouped_row_tiles(int64_t R, int64_t E, int bn)
@@ -193,7 +197,8 @@ struct RowsPlan {
     int tiles_per_wave, depth;
     int64_t m_tiles;
 };
-inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus,
+                                  int parts = 1)
 {
     RowsPlan p = {1, 8, 0};
     const int64_t kpu = type == W_Q8_0 ? 64 : 128, units = (K + kpu - 1) / kpu;
@@ -202,17 +207,18 @@ inline RowsPlan plan_grouped_rows(int64_t M, int64_t K, int64_t R, int64_t E, in
     // one workgroup's tiles share its activations: as many as still give every CU
     // two workgroups, in one pass over K
     const int64_t used = E < R ? E : R;
-    if (K <= 2048)
+    if (K * parts <= 2048)
         while (p.tiles_per_wave < 4 && used * tiles >= 8 * 2 * cus * 2 * p.tiles_per_wave) p.tiles_per_wave *= 2;
     p.m_tiles = (tiles + 8 * p.tiles_per_wave - 1) / (8 * p.tiles_per_wave);
     return p;
 }
 // Whether one grid takes a launch's tiles in a form (kp as in GroupedForm): its
 // threads stay below 2^32 (kMaxGridThreads).
-inline bool grouped_grid_fits(int kp, int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+inline bool grouped_grid_fits(int kp, int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus,
+                              int parts = 1)
 {
     const int64_t bm = kp ? (swiglu ? 64 : 128) / kp : 0;
-    const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles;
+    const int64_t m = kp ? (M + bm - 1) / bm : plan_grouped_rows(M, K, R, E, type, swiglu, cus, parts).m_tiles;
     const int64_t n = grouped_row_tiles(R, E, kp ? 128 / kp : 16), most = (int64_t)(kMaxGridThreads / 512) - 1;
     return m <= most && n <= most && m * n <= most;
 }
@@ -242,7 +248,7 @@ struct GroupedForm {
 // Q4_0, 256 rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 /
 // 349 / 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80; 64 x 64 Q4_0, 32768 rows
 // 40 / 14 / 8.5 / 10.7, a million rows 1041 / 306 / 131 / 107.
-inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus, int parts = 1)
 {
     const double used = (double)(E < R ? E : R), k1024 = (double)K / 1024;
     auto row_tiles = [&](int bn) {
@@ -253,13 +259,13 @@ inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int 
     const double lone = type == W_MXFP4 ? 2.6 : 4.3;
     const double bytes = (double)M * (double)K * (type == W_Q8_0 ? 1.06 : 0.55) * (swiglu ? 2 : 1);
     GroupedForm best = {0, false};
-    const double streams = row_tiles(16) * bytes / (1e6 * rate) * (K > 2048 ? 1.15 : 1.0);
-    const double starts = 7 * row_tiles(16) * (double)plan_grouped_rows(M, K, R, E, type, swiglu, cus).m_tiles / (2 * (double)cus);
+    const double streams = row_tiles(16) * bytes / (1e6 * rate) * (K * parts > 2048 ? 1.15 : 1.0);
+    const double starts = 7 * row_tiles(16) * (double)plan_grouped_rows(M, K, R, E, type, swiglu, cus, parts).m_tiles / (2 * (double)cus);
     double least = 4 + lone * (double)K / 2048 + (streams > starts ? streams : starts);
-    if (!grouped_grid_fits(0, M, K, R, E, type, swiglu, cus)) least = 1e300;      // and stays the answer if none fits
+    if (!grouped_grid_fits(0, M, K, R, E, type, swiglu, cus, parts)) least = 1e300;      // and stays the answer if none fits
     static constexpr struct { int kp; double fixed, k1024; } forms[] = {{1, 1.4, 8.0}, {2, 0.95, 2.8}, {4, 0.75, 1.2}};
     for (const auto &f : forms) {
-        if (!grouped_grid_fits(f.kp, M, K, R, E, type, swiglu, cus)) continue;
+        if (!grouped_grid_fits(f.kp, M, K, R, E, type, swiglu, cus, parts)) continue;
         const int64_t bm = (swiglu ? 64 : 128) / f.kp;
         const double share = row_tiles(128 / f.kp) * (double)((M + bm - 1) / bm) / (double)cus;
         const double rounds = share <= 1 ? 1.8 : share < 1e9 ? (double)((int64_t)share + ((double)(int64_t)share < share)) : share;
@@ -272,9 +278,9 @@ inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int 
     return best;
 }
 // Whether any form takes the launch.
-inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus)
+inline bool grouped_fits(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus, int parts = 1)
 {
-    return grouped_grid_fits(grouped_form(M, K, R, E, type, swiglu, cus).kp, M, K, R, E, type, swiglu, cus);
+    return grouped_grid_fits(grouped_form(M, K, R, E, type, swiglu, cus, parts).kp, M, K, R, E, type, swiglu, cus, parts);
 }
 hipError_t launch_gemm_grouped(const ExpertView &w, const ExpertView *up, const ActView &x, const int32_t *offsets,
                                const int32_t *order, int top_k, const GroupedOut &y, hipStream_t stream);

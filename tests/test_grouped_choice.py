@@ -1,11 +1,17 @@
 """Which form a launch of grouped products takes (csrc/qmm_internal.h, built for the
 host alone), where one form is many times slower than another."""
+import os
+import random
+import shutil
+import subprocess
+
 import pytest
 
 import test_gpu_grouped_contents as contents
 import test_gpu_grouped_more as more
+import test_gpu_layer_split as split
 import test_gpu_lora_contents as adapters
-from test_grouped_plan import TYPE, plan  # noqa: F401 (a fixture)
+from test_grouped_plan import ROOT, TYPE, _spread, plan  # noqa: F401 (a fixture)
 
 
 @pytest.mark.parametrize("kind", ["mxfp4", "q4_0", "q8_0"])
@@ -46,3 +52,33 @@ def test_shapes_of_the_adapters_contents_tests_take_every_form(plan):  # noqa: F
     plans = plan([f"lora 256 {N} {K} {M} {r} 1" for N, L, r, K, M in shapes])
     got = ["one launch" if p["single"] == "1" else "tiles" if p["tiled"] == "1" else "registers" for p in plans]
     assert got == list(adapters.SHAPES)
+
+
+def test_second_product_of_a_layer_with_h_in_two_parts(tmp_path):
+    """Its rules, and that the GPU tests' shapes take every form."""
+    if not shutil.which("g++"):
+        pytest.skip("g++ not available")
+    exe = str(tmp_path / "plan")
+    r = subprocess.run(["g++", "-O1", "-std=c++17", "-I/opt/rocm/include", "-D__HIP_PLATFORM_AMD__",
+                        os.path.join(ROOT, "tests", "plan", "layer_driver.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+
+    def forms(launches):
+        r = subprocess.run([exe], input="".join(" ".join(map(str, v)) + "\n" for v in launches), capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0, r.stderr
+        return [v.split() for v in r.stdout.splitlines()]
+
+    rng = random.Random(9)
+    launches = [(rng.choice((32, 256, 304)), rng.randint(0, 2), _spread(rng, 1, 1 << 24), _spread(rng, 32, 1 << 21, 32), _spread(rng, 1, 1 << 28),
+                 _spread(rng, 1, 1024)) for _ in range(10000)]
+    assert len(forms(launches)) == len(launches)
+    depths, tiles = set(), set()
+    for form, shapes in split.SHAPES.items():
+        for E, k, N, F, M in shapes:
+            for kind in TYPE:
+                (got, depth, per_wave, fits), = forms([(256, TYPE[kind], M, F, N * k, E)])
+                assert got == form and fits == "1", (kind, form, E, k, N, F, M)
+                if form == "0":
+                    depths.add(depth)
+                    tiles.add(per_wave)
+    assert depths == {"4", "8"} and tiles >= {"1", "2"}
