@@ -63,6 +63,14 @@ inline LoraPlan plan_lora(int64_t N, int64_t K, int64_t M, int64_t r, bool wide,
         while (j < tokens && groups * j < want) j *= 2;
         return j;
     };
+    // Tiles of 32 tokens through LDS want tokens that share an adapter, tiles of 16
+    // through registers take different ones better, and more tokens are prompts more
+    // often.  us in a graph, registers then tiles, four prompts / 24 adapters in turn:
+    //   512 tokens, rank 64, 2048 x 2048, bf16 x    15.8 and 12.7 / 41.7 and 55.5
+    //   640 tokens                                  20.2 and 13.6 / 53.8 and 60.7
+    //  1024 tokens                                  21.1 and 14.6 / 67.7 and 65.5
+    //   640 tokens, rank 128, 2048 x 5632           51.6 and 22.8 / 171 and 123
+    //   640 tokens, rank 64, 2048 x 2048, fp32 x    22.1 and 17.7 / 60.1 and 103
     p.tiled = wide && N > 512;
     const int64_t tile1 = p.tiled ? 32 : 16, tiles1 = (N + tile1 - 1) / tile1;
     int64_t parts = (p.tiled ? 2 : 1) * cus / tiles1;

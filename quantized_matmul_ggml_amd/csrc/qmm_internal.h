@@ -244,7 +244,10 @@ struct GroupedForm {
 //    the workgroups' own time: 7 us for two on each CU, whatever K and M are, as
 //    each finds its tile, fills the whole image and then waits for its weights.
 //    Before it `lone` us for 2048 of K, the way through a row.
-// In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
+// 420 launches over types, M from 16, K from 64, 1 to 1024 experts, even and uneven
+// groups, each timed in all six forms: the one taken is 3.6 % slower than the best on
+// average and 1.7 times at most (200 rows of 64 x 64 Q4_0 over eight experts: 8.5 and
+// 5.1).  In us as streamed / 32 / 64 / 128 rows a tile: 8 experts, gate and up 5632 x 2048
 // Q4_0, 256 rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 /
 // 349 / 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80; 64 x 64 Q4_0, 32768 rows
 // 40 / 14 / 8.5 / 10.7, a million rows 1041 / 306 / 131 / 107.
