@@ -234,9 +234,9 @@ struct GroupedForm {
     int kp;
     bool deep;
 };
-// It is chosen by its estimated time, among those whose tiles fit one grid.  Only R and E are known here, not the groups,
-// so that each group counts half a tile more than its share of R, and a tenth of
-// the groups one tile more than the others.
+// It is chosen by its estimated time, among those whose tiles fit one grid.  Only R
+// and E are known here, not the groups, so that each group counts half a tile more
+// than its share of R, and a tenth of the groups one tile more than the others.
 //  * Tiles: a tile takes a CU `fixed` us and `k1024` more for 1024 of K while its
 //    workgroups overlap, a CU's only one 1.8 times that.
 //  * Rows: what unpacking and memory let through of 16-row tiles' weights, `rate`
@@ -251,6 +251,10 @@ struct GroupedForm {
 // Q4_0, 256 rows 71 / 60 / 51 / 64, 1024 rows 206 / 161 / 116 / 92, 4096 rows 758 / 565 /
 // 349 / 271; the same MXFP4, 512 uneven rows 77 / 82 / 55 / 80; 64 x 64 Q4_0, 32768 rows
 // 40 / 14 / 8.5 / 10.7, a million rows 1041 / 306 / 131 / 107.
+// Rows in two parts (a layer's second product) take every form about as much longer:
+// over 36 layers the form that this estimate gives was 1 % behind the best on average
+// and 13 % at most (sixteen experts, 122 rows, 2048 x 1408 Q4_0, with the rest of the
+// layer 35.7 and 31.6).
 inline GroupedForm grouped_form(int64_t M, int64_t K, int64_t R, int64_t E, int type, bool swiglu, int64_t cus, int parts = 1)
 {
     const double used = (double)(E < R ? E : R), k1024 = (double)K / 1024;
